@@ -35,6 +35,7 @@ int cuda_error(cudaError_t e, const char* what)
 // expires.  Its address is looked up once per device and passed to kernels as a pointer.
 static __device__ int g_status_word;
 static constexpr int kDevMergeLost = 6;   // the value the split-KV merge leaves (ptx.cuh)
+static constexpr int kDevBadPage = 7;     // the value the paged-cache kernels leave
 static constexpr int kMaxDevices = 64;
 static std::atomic<int*> g_status_addr[kMaxDevices];
 static std::atomic<int> g_num_sms[kMaxDevices];
@@ -207,6 +208,7 @@ const char* fmha_error_string(int code)
         case FMHA_ERR_WORKSPACE: return "FMHA_ERR_WORKSPACE: workspace missing or too small";
         case FMHA_ERR_CUDA: return "FMHA_ERR_CUDA: CUDA call or kernel launch failed";
         case FMHA_ERR_TIMEOUT: return "FMHA_ERR_TIMEOUT: a kernel's bounded wait expired";
+        case FMHA_ERR_PAGES: return "FMHA_ERR_PAGES: a paged-cache call met lengths, pages, slots or positions outside their bounds";
         case FMHA_ERR_RACE: return "FMHA_ERR_RACE: overlapping calls on one workspace left a split-KV merge unsettled";
         default: return "unknown fmha status";
     }
@@ -240,6 +242,8 @@ int fmha_check_status(fmha_stream_t stream)
         if (e != cudaSuccess) return cuda_error(e, "cudaMemcpyToSymbol(status)");
         if (v == kDevMergeLost)
             return set_error(FMHA_ERR_RACE, "a split-KV merge counter never settled (device status word set)");
+        if (v == kDevBadPage)
+            return set_error(FMHA_ERR_PAGES, "a paged-cache call met a length, page, slot or position outside its bounds, or ran out of pages");
         return set_error(FMHA_ERR_TIMEOUT, "a kernel's bounded wait expired (device status word set)");
     }
     return FMHA_OK;

@@ -50,6 +50,8 @@ typedef enum {
     FMHA_ERR_WORKSPACE = 3,   /* workspace missing or smaller than fmha_workspace_size() */
     FMHA_ERR_CUDA = 4,        /* a CUDA runtime/driver call or kernel launch failed */
     FMHA_ERR_TIMEOUT = 5,     /* a kernel's bounded wait expired (see fmha_check_status) */
+    FMHA_ERR_PAGES = 7,       /* a paged-cache call met data out of bounds on the device: a length, page,
+                                 slot or position, or too few free pages (see fmha_check_status) */
     FMHA_ERR_RACE = 6         /* a split-KV merge counter never settled: calls sharing one
                                  workspace (or the allocation-free scratch) overlapped on the
                                  GPU, so some output rows may be unmerged (see fmha_check_status) */
@@ -184,6 +186,98 @@ int nvfp4_quantize_scaled(const float* x, uint8_t* q, uint8_t* scales, int64_t n
                           fmha_stream_t stream);
 
 /*
+ * ---- Paged key/value cache -----------------------------------------------------------------------
+ * Keys and values of many requests of growing lengths in pools of equal pages: page p, key/value head
+ * h, token t of the page and feature d are at element p * page_stride + h * head_stride +
+ * t * token_stride + d of either pool.  Heads outside tokens ([pages][Hkv][page_size][D]) and tokens
+ * outside heads ([pages][page_size][Hkv][D]) are both strides of this form; a dense [B][Hkv][Skv][D]
+ * tensor is a cache of B pages of Skv tokens.  A request's tokens j = 0, 1, .. are in the pages of its
+ * row of a block table: page block_table[b][j / page_size], token j % page_size of it.  A slot is a
+ * token's place in the pool, page * page_size + token.
+ *
+ * A step of serving is fmha_page_table (pages and slots for the new tokens), then in every layer
+ * fmha_rope_append (queries, and keys and values into the cache) and fmha_fwd_paged.  All three are
+ * stream-ordered, allocate nothing and can be captured.  Data on the device that is out of bounds (a
+ * length, page, slot or position) is never followed: the call does what its text says and
+ * fmha_check_status reports FMHA_ERR_PAGES.
+ */
+typedef struct {
+    void* k;              /* device BF16 pools, 16-byte aligned */
+    void* v;
+    int num_pages;        /* >= 1 */
+    int page_size;        /* tokens per page, >= 1 (fmha_fwd_paged: a multiple of 8) */
+    int Hkv;              /* key/value heads */
+    int D;                /* 64 or 128 */
+    int64_t page_stride;  /* elements; each a multiple of 8, at least D, below 2^38 */
+    int64_t head_stride;
+    int64_t token_stride;
+} fmha_kv_cache;
+
+/*
+ * Pages, block tables and slots from request lengths, for one step of B requests (at most 8192), in
+ * one launch.
+ *   ctx_lens: int32[B], tokens request b has in the cache; new_lens: int32[B], tokens to come (0: none),
+ *   or a negative number: the request is done and its pages go back.
+ *   free_pages: int32[num_pages], a stack of free pages whose height is *free_count.  First the pages of
+ *   done requests are pushed, in request order and page order; then every other request with more tokens
+ *   than pages is given pages from the top, in request order.
+ *   block_table: int32[B][max_pages]; the entries of new pages are written, no other is.
+ * Outputs: seqlens[b] = ctx + new (0 for a done request); cu_new: int32[B + 1], first new token of each
+ *   request and their total; positions[t] and slots[t], t < T, of the new tokens in request order; behind
+ *   the last one positions 0 and slots -1 (T may be larger than the total, e.g. a captured size);
+ *   *free_count_out, the stack's new height.
+ * seqlens may be the ctx_lens array and free_count_out may be free_count (an update in place); no other
+ * arrays may overlap.  With a length that is negative or passes the table row, a stack height outside
+ * 0..num_pages, too few free pages, or more than T new tokens, nothing is given or taken: seqlens =
+ * ctx_lens, cu_new 0, positions 0, slots -1, the stack as it was, and FMHA_ERR_PAGES from
+ * fmha_check_status.  A token whose page is not one of the pool's gets slot -1 and the same report.
+ * All pointers device memory; slots 8-byte, the others 4-byte aligned.
+ */
+int fmha_page_table(const int32_t* ctx_lens, const int32_t* new_lens, int B, int page_size, int32_t* free_pages,
+                    const int32_t* free_count, int num_pages, int32_t* block_table, int max_pages, int32_t* seqlens,
+                    int32_t* cu_new, int32_t* positions, int64_t* slots, int T, int32_t* free_count_out,
+                    fmha_stream_t stream);
+
+/*
+ * Norms of the query and key heads, position rotation and the store in the cache, in one pass.
+ *   q: BF16, head h of token t at q + t * q_stride + h * D (strides in elements, multiples of 8); k, v
+ *   alike with the cache's Hkv heads: the three may be parts of one projection's rows.
+ *   q_weight, k_weight: BF16[D], y = x / sqrt(mean(x^2) + eps) * weight per head; NULL: y = x.
+ *   cos_sin: FP32 [max_pos][rope_dim], rope_dim / 2 cosines and then as many sines of each position;
+ *   positions: int32[T].  The first rope_dim features of queries and keys are rotated: feature i with
+ *   i + rope_dim / 2, or (interleaved != 0) 2i with 2i + 1.  rope_dim: a multiple of 16 up to D, 0 = none
+ *   (cos_sin and positions are not read).
+ *   slots: int64[T], distinct; a negative slot is padding: nothing of that token is read or written.
+ *   q_out: BF16 [T / Sq][Hq][Sq][D], token t = n * Sq + s at [n][h][s] (Sq = 1: [T][Hq][D]).
+ * Keys and values go to their slots of `cache` (values as they are).  FP32 throughout, one rounding to
+ * BF16 per output.  A token with a slot or position out of bounds is left out like padding and reported.
+ * Pointers 16-byte aligned (positions 4, slots 8).
+ */
+int fmha_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                     const void* q_weight, const void* k_weight, float eps, const float* cos_sin, int max_pos, int rope_dim,
+                     int interleaved, const int32_t* positions, const int64_t* slots, void* q_out,
+                     const fmha_kv_cache* cache, int T, int Hq, int Sq, fmha_stream_t stream);
+
+/*
+ * Attention of the last Sq tokens of each request over its pages: fmha_fwd_ex with K and V row j of
+ * request b taken from the cache through block_table (int32 [B][max_pages]) and seqlens[b] keys (device
+ * int32[B], 0 <= seqlens[b] <= max_pages * page_size).  q, out, lse as in fmha_fwd; D and Hkv are the
+ * cache's; page_size a multiple of 8.
+ *   opts (NULL: defaults): out_kind, num_splits, workspace, causal and the NVFP4 fields as for fmha_fwd_ex;
+ *   seqlens_k must be NULL.  With a workspace of fmha_paged_workspace_size() bytes the keys are split over
+ *   every SM, without one each (request, kv-head) is one CTA's.
+ * Made for up to 16 query rows per key/value head, (Hq / Hkv) * Sq; more rows run in chunks of at most 16,
+ * each reading the keys again.  Entries of the block table behind the last key are not read.  A page out
+ * of the pool reads as zero keys and values, a length out of bounds is clamped, and both are reported.
+ */
+int fmha_fwd_paged(const void* q, const fmha_kv_cache* cache, const int32_t* block_table, int max_pages,
+                   const int32_t* seqlens, void* out, float* lse, int B, int Hq, int Sq, float scale,
+                   fmha_stream_t stream, const fmha_opts* opts);
+
+/* Bytes of workspace fmha_fwd_paged needs for this problem and these options (0 if none or invalid). */
+size_t fmha_paged_workspace_size(int B, int Hq, int Sq, const fmha_kv_cache* cache, const fmha_opts* opts);
+
+/*
  * Test hook: raw S = Q K^T in FP32, no scale ("CURRENT_ISSUE.md" @57d67e6, "The 4x Bug":
  * the single tcgen05 MMA product checked against a scalar dot product).
  *   q: BF16 [Sq,D], k: BF16 [Skv,D], s: FP32 [Sq,Skv]; D in {16, 64, 128, 512}.
@@ -202,8 +296,9 @@ int fmha_selftest(int which, const void* in, void* out, size_t out_bytes, int pa
 /*
  * Waits for `stream`, then returns FMHA_ERR_TIMEOUT if any kernel of this library timed out
  * in a bounded wait since the last call, FMHA_ERR_RACE if a split-KV merge found its arrival
- * counter changing under it (overlapping calls on one workspace), clearing that state in both
- * cases; FMHA_ERR_CUDA if the stream reports an error; else FMHA_OK.
+ * counter changing under it (overlapping calls on one workspace), FMHA_ERR_PAGES if a paged-cache
+ * call met device data out of bounds, clearing that state in all three cases (of several, the
+ * latest is reported); FMHA_ERR_CUDA if the stream reports an error; else FMHA_OK.
  */
 int fmha_check_status(fmha_stream_t stream);
 
