@@ -560,7 +560,96 @@ __global__ void __launch_bounds__(decode_threads<EPI>(), 1)
         if constexpr (EPI) setmaxnreg_dec<kRegsCtl>();
       if (warp == tma_warp<EPI>()) {
         // ------------------------------------------------ TMA producer
-        if (lane_id() == 0) {
+        if constexpr (PAGED) {
+            // A tile is filled in boxes of p.box keys, each inside one page, up to the request's length (rows
+            // behind it keep what the buffer held: their scores are masked and their V rows zeroed).  Lane
+            // (i, a) of the warp looks up the page of box i and issues its 64-feature half a, for K and for V;
+            // the next tile's pages are looked up before this tile's buffers are waited for.  A page outside
+            // the pool loads zeros (the tensor map's fill) and sets the status.
+            const int lane = static_cast<int>(lane_id());
+            if (lane == 0) {
+                tma_prefetch_desc(&qmap);
+                tma_prefetch_desc(&kmap);
+                tma_prefetch_desc(&vmap);
+            }
+            const uint64_t pol = policy_evict_first();
+            Ring qr(2), kr(S), vr(S);
+            uint32_t kcnt[S], vcnt[S], qcnt[2] = {0, 0};
+            for (int i = 0; i < S; ++i) kcnt[i] = vcnt[i] = 0;
+            const int boxes = kTileKV / p.box;
+            const int i = lane % boxes, a = lane / boxes;
+            // lane 0 waits for the buffer and announces `bytes`; the warp goes on unless the CTA has aborted
+            auto claim = [&](uint64_t* empty, uint64_t* full, uint32_t phase, uint32_t bytes) {
+                int go = 0;
+                if (lane == 0) {
+                    mbar_wait(empty, phase ^ 1, wc);
+                    go = aborted(wc) ? 0 : 1;
+                    if (go) mbar_arrive_expect_tx(full, bytes);
+                }
+                return __shfl_sync(0xffffffffu, go, 0) != 0;
+            };
+            while (sched.next(it)) {
+                if (it.t1 <= it.t0) continue;
+                const int b = it.u / p.Hkv, head = (it.u % p.Hkv) / p.chunks;
+                const int32_t* row = p.table + static_cast<size_t>(b) * p.max_pages;
+                // page and first key in it of this lane's box of tile t (-1: it has none)
+                int page = 0, off = -1;
+                auto look_up = [&](int t) {
+                    const int j = t * kTileKV + i * p.box;
+                    if (a < C::kAtoms && j < it.n) {
+                        const int s = j / p.page;
+                        page = row[s];
+                        off = j - s * p.page;
+                    } else {
+                        off = -1;
+                    }
+                };
+                look_up(it.t0);
+                if (claim(&q_empty[qr.idx], &q_full[qr.idx], qr.phase, C::kQBytes)) {
+                    if (lane < C::kAtoms)
+                        tma_load_3d(smem + C::kOffQ + qr.idx * C::kQBytes + lane * (kN * 128), &qmap, &q_full[qr.idx], lane * 64,
+                                    (it.u % p.chunks) * p.G, it.u / p.chunks);
+                    ++qcnt[qr.idx];
+                }
+                qr.advance();
+                for (int t = it.t0; t < it.t1; ++t) {
+                    int page_t = page;
+                    const int off_t = off;
+                    if (t + 1 < it.t1) look_up(t + 1);
+                    if (off_t >= 0 && (page_t < 0 || page_t >= p.num_pages)) {
+                        page_t = p.num_pages;
+                        atomicExch(p.status, kDevBadPage);
+                    }
+                    const int used = (min(it.n - t * kTileKV, kTileKV) + p.box - 1) / p.box;
+                    const uint32_t bytes = static_cast<uint32_t>(used * p.box * 128 * C::kAtoms);
+                    const int at = a * (kTileKV * 128) + i * p.box * 128;
+                    if (claim(&k_empty[kr.idx], &k_full[kr.idx], kr.phase, bytes)) {
+                        if (off_t >= 0)
+                            tma_load_4d_hint(smem + C::kOffK + kr.idx * C::kKVBytes + at, &kmap, &k_full[kr.idx], a * 64, off_t, head,
+                                             page_t, pol);
+                        ++kcnt[kr.idx];
+                    }
+                    kr.advance();
+                    if (claim(&v_empty[vr.idx], &v_full[vr.idx], vr.phase, bytes)) {
+                        if (off_t >= 0)
+                            tma_load_4d_hint(smem + C::kOffV + vr.idx * C::kKVBytes + at, &vmap, &v_full[vr.idx], a * 64, off_t, head,
+                                             page_t, pol);
+                        ++vcnt[vr.idx];
+                    }
+                    vr.advance();
+                }
+            }
+            // nothing may still be landing in shared memory when the CTA exits
+            if (lane == 0) {
+                for (int n = 0; n < S; ++n) {
+                    if (kcnt[n]) drain_wait(&k_full[n], (kcnt[n] - 1) & 1, kDrainLimit);
+                    if (vcnt[n]) drain_wait(&v_full[n], (vcnt[n] - 1) & 1, kDrainLimit);
+                }
+                for (int n = 0; n < 2; ++n)
+                    if (qcnt[n]) drain_wait(&q_full[n], (qcnt[n] - 1) & 1, kDrainLimit);
+            }
+            __syncwarp();
+        } else if (lane_id() == 0) {
             tma_prefetch_desc(&qmap);
             tma_prefetch_desc(&kmap);
             tma_prefetch_desc(&vmap);
@@ -568,25 +657,6 @@ __global__ void __launch_bounds__(decode_threads<EPI>(), 1)
             Ring qr(2), kr(S), vr(S);
             uint32_t kcnt[S], vcnt[S], qcnt[2] = {0, 0};
             for (int i = 0; i < S; ++i) kcnt[i] = vcnt[i] = 0;
-            // Paged: a tile is filled in boxes of p.box keys, each inside one page, up to the request's
-            // length (rows behind it keep what the buffer held: their scores are masked and their V rows
-            // zeroed).  A page outside the pool loads zeros (the tensor map's fill) and sets the status.
-            auto load_pages = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int t) {
-                const int j0 = t * kTileKV, j1 = min(j0 + kTileKV, it.n);
-                const int boxes = (j1 - j0 + p.box - 1) / p.box;
-                mbar_arrive_expect_tx(bar, static_cast<uint32_t>(boxes * p.box * 128 * C::kAtoms));
-                const int b = it.u / p.Hkv, head = (it.u % p.Hkv) / p.chunks;
-                for (int i = 0; i < boxes; ++i) {
-                    const int j = j0 + i * p.box, slot = j / p.page;
-                    int page = p.table[static_cast<size_t>(b) * p.max_pages + slot];
-                    if (page < 0 || page >= p.num_pages) {
-                        page = p.num_pages;
-                        atomicExch(p.status, kDevBadPage);
-                    }
-                    for (int a = 0; a < C::kAtoms; ++a)
-                        tma_load_4d_hint(dst + a * (kTileKV * 128) + i * p.box * 128, map, bar, a * 64, j - slot * p.page, head, page, pol);
-                }
-            };
             while (sched.next(it)) {
                 if (it.t1 <= it.t0) continue;
                 mbar_wait(&q_empty[qr.idx], qr.phase ^ 1, wc);
@@ -594,10 +664,7 @@ __global__ void __launch_bounds__(decode_threads<EPI>(), 1)
                     uint8_t* dst = smem + C::kOffQ + qr.idx * C::kQBytes;
                     mbar_arrive_expect_tx(&q_full[qr.idx], C::kQBytes);
                     for (int a = 0; a < C::kAtoms; ++a)
-                        if constexpr (PAGED)
-                            tma_load_3d(dst + a * (kN * 128), &qmap, &q_full[qr.idx], a * 64, (it.u % p.chunks) * p.G, it.u / p.chunks);
-                        else
-                            tma_load_3d(dst + a * (kN * 128), &qmap, &q_full[qr.idx], a * 64, 0, it.u);
+                        tma_load_3d(dst + a * (kN * 128), &qmap, &q_full[qr.idx], a * 64, 0, it.u);
                     ++qcnt[qr.idx];
                 }
                 qr.advance();
@@ -605,28 +672,20 @@ __global__ void __launch_bounds__(decode_threads<EPI>(), 1)
                     mbar_wait(&k_empty[kr.idx], kr.phase ^ 1, wc);
                     if (!aborted(wc)) {
                         uint8_t* dst = smem + C::kOffK + kr.idx * C::kKVBytes;
-                        if constexpr (PAGED) {
-                            load_pages(dst, &kmap, &k_full[kr.idx], t);
-                        } else {
                         mbar_arrive_expect_tx(&k_full[kr.idx], C::kKVBytes);
                         for (int a = 0; a < C::kAtoms; ++a)
                             tma_load_3d_hint(dst + a * (kTileKV * 128), &kmap, &k_full[kr.idx], a * 64, t * kTileKV,
                                              it.u, pol);
-                        }
                         ++kcnt[kr.idx];
                     }
                     kr.advance();
                     mbar_wait(&v_empty[vr.idx], vr.phase ^ 1, wc);
                     if (!aborted(wc)) {
                         uint8_t* dst = smem + C::kOffV + vr.idx * C::kKVBytes;
-                        if constexpr (PAGED) {
-                            load_pages(dst, &vmap, &v_full[vr.idx], t);
-                        } else {
                         mbar_arrive_expect_tx(&v_full[vr.idx], C::kKVBytes);
                         for (int a = 0; a < C::kAtoms; ++a)
                             tma_load_3d_hint(dst + a * (kTileKV * 128), &vmap, &v_full[vr.idx], a * 64, t * kTileKV,
                                              it.u, pol);
-                        }
                         ++vcnt[vr.idx];
                     }
                     vr.advance();
