@@ -40,6 +40,17 @@ DecodeWs decode_ws_layout(const AttnArgs& a, bool split, int nsm)
 }
 
 template <int D, bool CAUSAL>
+auto kernel_for(int G) -> decltype(&decode_kernel<D, CAUSAL, 1>)
+{
+    switch (decode_columns(G)) {
+        case 1: return decode_kernel<D, CAUSAL, 1>;
+        case 4: return decode_kernel<D, CAUSAL, 4>;
+        case 8: return decode_kernel<D, CAUSAL, 8>;
+        default: return decode_kernel<D, CAUSAL, 16>;
+    }
+}
+
+template <int D, bool CAUSAL>
 int run_decode(const AttnArgs& a, bool split, void* ws, cudaStream_t st)
 {
     using C = DecodeCfg<D>;
@@ -110,10 +121,9 @@ int run_decode(const AttnArgs& a, bool split, void* ws, cudaStream_t st)
     // The epilogue warpgroup takes each item's epilogue off the softmax warps when a unit has several
     // query columns (publishing a 16-column partial costs several tiles' streaming time); with one
     // column the epilogue is short and the six-warp kernel, whose softmax warps run it, measured faster.
+    const auto kernel = kernel_for<D, CAUSAL>(G);
     const bool epi = G > 1;
-    const void* fn = epi ? reinterpret_cast<const void*>(decode_kernel<D, CAUSAL, true>)
-                         : reinterpret_cast<const void*>(decode_kernel<D, CAUSAL, false>);
-    FMHA_CHECK_CUDA(set_smem_limit_once(fn, C::kSmemBytes));
+    FMHA_CHECK_CUDA(set_smem_limit_once(reinterpret_cast<const void*>(kernel), C::kSmemBytes));
     // one CTA per SM, or one per key tile when a uniform-length problem has fewer tiles than SMs (a
     // small problem then launches only the CTAs that have work)
     int grid = split ? nsm : (U < nsm ? U : nsm);
@@ -134,10 +144,9 @@ int run_decode(const AttnArgs& a, bool split, void* ws, cudaStream_t st)
     }
     if (grid > 0) {
         timing_mark_begin(st);
-        const cudaError_t e = epi ? launch_pdl(decode_kernel<D, CAUSAL, true>, dim3(static_cast<unsigned>(grid)),
-                                               dim3(decode_threads<true>()), C::kSmemBytes, st, qmap, kmap, vmap, p)
-                                  : launch_pdl(decode_kernel<D, CAUSAL, false>, dim3(static_cast<unsigned>(grid)),
-                                               dim3(decode_threads<false>()), C::kSmemBytes, st, qmap, kmap, vmap, p);
+        const cudaError_t e = launch_pdl(kernel, dim3(static_cast<unsigned>(grid)),
+                                         dim3(epi ? decode_threads<true>() : decode_threads<false>()), C::kSmemBytes, st, qmap,
+                                         kmap, vmap, p);
         timing_mark_end(st);
         FMHA_CHECK_CUDA(e);
         count_launch();

@@ -238,6 +238,65 @@ __device__ __forceinline__ uint32_t sw128_offset(int r, int k, uint32_t atom_byt
 }
 
 
+// Tensor Memory loads and stores of N consecutive columns of this warp's 32 lanes
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N])
+{
+    static_assert(N == 1 || N == 4 || N == 8 || N == 16 || N == 32, "column counts in use");
+    if constexpr (N == 1)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r[0]) : "r"(taddr));
+    else if constexpr (N == 4)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(taddr));
+    else if constexpr (N == 8)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "r"(taddr));
+    else if constexpr (N == 16)
+        tmem_ld16(taddr, r);
+    else
+        tmem_ld32(taddr, r);
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[N])
+{
+    static_assert(N == 8 || N == 16 || N == 32, "column counts in use");
+    if constexpr (N == 8)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+                     "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                     : "memory");
+    else if constexpr (N == 16)
+        tmem_st16(taddr, r);
+    else
+        tmem_st32(taddr, r);
+}
+
+// Barrier over the first 128 threads' warps that also returns whether any of them passes true
+__device__ __forceinline__ bool bar_any128(int id, bool v)
+{
+    int r;
+    asm volatile(
+        "{\n"
+        ".reg .pred a, b;\n"
+        "setp.ne.u32 a, %1, 0;\n"
+        "barrier.cta.red.or.pred b, %2, 128, a;\n"
+        "selp.u32 %0, 1, 0, b;\n"
+        "}\n"
+        : "=r"(r)
+        : "r"(v ? 1 : 0), "r"(id)
+        : "memory");
+    return r != 0;
+}
+
+// Largest value of the warp's 32 lanes (NaN loses against any number)
+__device__ __forceinline__ float redux_max(float v)
+{
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
 // Bounded wait that ignores the abort flag: used at teardown so nothing is still in flight.
 __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, long long limit)
 {
@@ -302,13 +361,17 @@ __device__ int unit_partial_slots(const DecodeParams& p, int u, int P, int* slot
 
 constexpr int kMaxFixSlots = 512;
 
-template <int D, bool CAUSAL, bool EPI, bool PAGED = false>
-__global__ void __launch_bounds__(decode_threads<EPI>(), 1)
+// Columns the softmax computes for units of G rows (the MMA's N stays kN): 1, 4, 8 or 16.
+inline int decode_columns(int G) { return G <= 1 ? 1 : G <= 4 ? 4 : G <= 8 ? 8 : 16; }
+
+template <int D, bool CAUSAL, int NC, bool PAGED = false>
+__global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
     decode_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap, const __grid_constant__ DecodeParams p)
 {
     using C = DecodeCfg<D>;
     constexpr int S = C::kStages;
+    constexpr bool EPI = NC > 1;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
 
@@ -318,8 +381,7 @@ __global__ void __launch_bounds__(decode_threads<EPI>(), 1)
     __shared__ float ep_m[2][kN];                  // the columns' reference maxima
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
-    __shared__ float red_max[2][4][kN];
-    __shared__ uint32_t red_need[2][4];   // per warp: columns whose scores passed the reference + kRescaleD
+    __shared__ float red_max[4][kN];
     __shared__ float red_sum[4][kN];
     __shared__ float col_inv[kN], col_lse[kN];   // per query column: 1 / L and the LSE of this range
     __shared__ int ep_abort, fx_last;          // softmax warps: abort snapshot, "this CTA merges"
@@ -337,13 +399,13 @@ __global__ void __launch_bounds__(decode_threads<EPI>(), 1)
             mbar_init(&q_full[i], 1);
             mbar_init(&q_empty[i], 1);
             mbar_init(&s_full[i], 1);
-            mbar_init(&s_empty[i], 128);
-            mbar_init(&p_full[i], 128);
+            mbar_init(&s_empty[i], 4);   // one arrival per warp
+            mbar_init(&p_full[i], 4);   // one arrival per warp
             mbar_init(&p_empty[i], 1);
             mbar_init(&o_full[i], 1);
-            mbar_init(&o_empty[i], 128);
-            mbar_init(&ep_full[i], 128);
-            mbar_init(&ep_empty[i], 128);
+            mbar_init(&o_empty[i], 4);   // one arrival per warp
+            mbar_init(&ep_full[i], 4);   // one arrival per warp
+            mbar_init(&ep_empty[i], 4);   // one arrival per warp
         }
         for (int i = 0; i < S; ++i) {
             mbar_init(&k_full[i], 1);
@@ -381,8 +443,8 @@ __global__ void __launch_bounds__(decode_threads<EPI>(), 1)
     // Memory lane) and output column, ew: warp within the group.
     // slots_ready: fx_n / fx_slot already hold this item's partial slots (the epilogue warpgroup finds
     // them while it waits for the item)
-    auto run_epilogue = [&](const Item& it, bool empty, const float (&m)[kN], const float (&l)[kN],
-                            const float (&acc)[kN], int tid, int ew, int bar, bool slots_ready) {
+    auto run_epilogue = [&](const Item& it, bool empty, const float (&m)[NC], const float (&l)[NC],
+                            const float (&acc)[NC], int tid, int ew, int bar, bool slots_ready) {
         const int lane = static_cast<int>(lane_id());
         const int G = unit_cols<PAGED>(p, it.u);
         const float nv_sg = p.nv_sg ? *p.nv_sg : 0.f;
@@ -400,22 +462,21 @@ __global__ void __launch_bounds__(decode_threads<EPI>(), 1)
         };
         // ---- epilogue: L = sum over the 128 key lanes, O = acc · (1 / L), lse = ln2 * (m + log2 L)
         if (!empty) {
-            if (G == 1) {
+            if (NC == 1) {
                 const float s = warp_sum(l[0]);
                 if (lane == 0) red_sum[ew][0] = s;
             } else {
                 // all columns' butterflies interleaved: five rounds of independent shuffles
-                float v[kN];
+                float v[NC];
 #pragma unroll
-                for (int q = 0; q < kN; ++q) v[q] = q < G ? l[q] : 0.f;
+                for (int q = 0; q < NC; ++q) v[q] = l[q];
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-                    for (int q = 0; q < kN; ++q) v[q] += __shfl_xor_sync(0xffffffffu, v[q], o);
+                    for (int q = 0; q < NC; ++q) v[q] += __shfl_xor_sync(0xffffffffu, v[q], o);
                 if (lane == 0)
 #pragma unroll
-                    for (int q = 0; q < kN; ++q)
-                        if (q < G) red_sum[ew][q] = v[q];
+                    for (int q = 0; q < NC; ++q) red_sum[ew][q] = v[q];
             }
         }
         // red_sum is complete, and every thread is past its reads of the previous item's
@@ -426,7 +487,7 @@ __global__ void __launch_bounds__(decode_threads<EPI>(), 1)
             const float Lq = empty ? 0.f : (red_sum[0][tid] + red_sum[1][tid]) + (red_sum[2][tid] + red_sum[3][tid]);
             float mq = m[0];
 #pragma unroll
-            for (int q = 1; q < kN; ++q)
+            for (int q = 1; q < NC; ++q)
                 if (q == tid) mq = m[q];
             const bool none = !(Lq > 0.f);   // no visible key in this range
             col_inv[tid] = none ? 0.f : 1.f / Lq;
@@ -443,7 +504,7 @@ __global__ void __launch_bounds__(decode_threads<EPI>(), 1)
         float local_amax = 0.f;
         if (tid < D) {
 #pragma unroll
-            for (int q = 0; q < kN; ++q) {
+            for (int q = 0; q < NC; ++q) {
                 if (q >= G) break;
                 const float o = col_inv[q] > 0.f ? acc[q] * col_inv[q] : 0.f;   // 0: no visible key in this range
                 const float lse_v = col_lse[q];
@@ -493,9 +554,9 @@ __global__ void __launch_bounds__(decode_threads<EPI>(), 1)
                     // (threads q < G) column q's partial LSEs, all in flight at once, so the merge
                     // costs one L2 round trip whatever the number of columns (a round per few
                     // columns was one dependent trip each, slow while the other CTAs stream)
-                    float ov[kN][4];
+                    float ov[NC][4];
 #pragma unroll
-                    for (int q = 0; q < kN; ++q)
+                    for (int q = 0; q < NC; ++q)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const bool use = q < G && i < ns && tid < D;
@@ -518,7 +579,7 @@ __global__ void __launch_bounds__(decode_threads<EPI>(), 1)
                     }
                     named_bar_sync(bar, 128);
 #pragma unroll
-                    for (int q = 0; q < kN; ++q) {
+                    for (int q = 0; q < NC; ++q) {
                         if (q >= G) break;
                         float o = 0.f;
 #pragma unroll
@@ -729,6 +790,9 @@ __global__ void __launch_bounds__(decode_threads<EPI>(), 1)
                 vr.advance();
                 orr.advance();
             };
+            // QK of a tile is issued ahead of PV of the tile before it, across work items too, so that tile's
+            // softmax overlaps it
+            bool behind = false;
             while (sched.next(it)) {
                 if (it.t1 <= it.t0) continue;
                 mbar_wait(&q_full[qr.idx], qr.phase, wc);
@@ -748,15 +812,16 @@ __global__ void __launch_bounds__(decode_threads<EPI>(), 1)
                         }
                         mma_commit(&s_full[sr.idx]);
                         mma_commit(&k_empty[kr.idx]);
+                        if (t + 1 == it.t1) mma_commit(&q_empty[qr.idx]);
                     }
                     kr.advance();
                     sr.advance();
-                    if (t > it.t0) pv();   // PV of the previous tile overlaps this tile's softmax
+                    if (behind) pv();
+                    behind = true;
                 }
-                pv();
-                if (!aborted(wc)) mma_commit(&q_empty[qr.idx]);
                 qr.advance();
             }
+            if (behind) pv();
             mma_commit(&mma_done);
             drain_wait(&mma_done, 0, kDrainLimit);
         }
@@ -771,88 +836,86 @@ __global__ void __launch_bounds__(decode_threads<EPI>(), 1)
         uint32_t tile_ctr = 0;
         while (sched.next(it)) {
             const int G = unit_cols<PAGED>(p, it.u);
-            float m[kN], l[kN], acc[kN], alpha_prev[kN];
+            float m[NC], l[NC], acc[NC], alpha_prev[NC];
             // keys visible to column q: 0 .. lim[q] - 1 (causal: query q % Sq sees keys up to
             // (q % Sq) + n - Sq; otherwise all n)
-            int lim[kN];
+            int lim[NC];
 #pragma unroll
-            for (int q = 0; q < kN; ++q)
+            for (int q = 0; q < NC; ++q)
                 lim[q] = CAUSAL ? it.n - p.Sq + 1 + (((PAGED ? (it.u % p.chunks) * p.G : 0) + q) % p.Sq) : it.n;
 #pragma unroll
-            for (int q = 0; q < kN; ++q) {
-                m[q] = -INFINITY;
+            for (int q = 0; q < NC; ++q) {
+                m[q] = q < G ? -INFINITY : INFINITY;   // a column without a query: P = 0, never the largest
                 l[q] = 0.f;
                 acc[q] = 0.f;
-                alpha_prev[q] = 0.f;
+                alpha_prev[q] = 1.f;
             }
-            auto consume = [&](const float (&al)[kN]) {
+            bool moved_prev = false;
+            auto consume = [&]() {
                 mbar_wait(&o_full[orr.idx], orr.phase, wc);
                 tc_fence_after();
-                uint32_t ov[16];
-                tmem_ld16(tmem + lane_base + 32 + orr.idx * 16, ov);
+                uint32_t ov[NC];
+                tmem_ld<NC>(tmem + lane_base + 32 + orr.idx * 16, ov);
                 tmem_ld_wait();
                 tc_fence_before();
-                mbar_arrive(&o_empty[orr.idx]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&o_empty[orr.idx]);
                 orr.advance();
+                if (moved_prev) {
 #pragma unroll
-                for (int q = 0; q < kN; ++q) acc[q] = fmaf(acc[q], al[q], __uint_as_float(ov[q]));
+                    for (int q = 0; q < NC; ++q) acc[q] = fmaf(acc[q], alpha_prev[q], __uint_as_float(ov[q]));
+                } else {
+#pragma unroll
+                    for (int q = 0; q < NC; ++q) acc[q] += __uint_as_float(ov[q]);
+                }
             };
             for (int t = it.t0; t < it.t1; ++t) {
                 mbar_wait(&s_full[sr.idx], sr.phase, wc);
                 tc_fence_after();
-                uint32_t sv[16];
-                tmem_ld16(tmem + lane_base + sr.idx * 16, sv);
+                uint32_t sv[NC];
+                tmem_ld<NC>(tmem + lane_base + sr.idx * 16, sv);
                 tmem_ld_wait();
                 tc_fence_before();
-                mbar_arrive(&s_empty[sr.idx]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s_empty[sr.idx]);
                 sr.advance();
 
                 const int kv = t * kTileKV + tid;
                 const bool valid = kv < it.n;
-                float x[kN];
-#pragma unroll
-                for (int q = 0; q < kN; ++q) x[q] = (CAUSAL ? kv < lim[q] : valid) ? __uint_as_float(sv[q]) * p.c : -INFINITY;
                 // Lazy column max (as the row-tile kernel's lazy rescale): the reference m[q] moves only
                 // when some score of column q exceeds it by more than 2^8, so P <= 256 and the final
                 // O = acc / L and LSE = m + log2 L are exact for any reference.  Usually no column
-                // moves and no max is reduced: one OR of flags across the four warps decides.
-                float(*rb)[kN] = red_max[tile_ctr & 1];
-                uint32_t need = 0;
+                // moves and no max is reduced: one barrier that also ORs a flag decides.
+                float x[NC], pv[NC];
+                bool above = false;
 #pragma unroll
-                for (int q = 0; q < kN; ++q)
-                    if (q < G && x[q] > m[q] + kRescaleD) need |= 1u << q;
-                need = __reduce_or_sync(0xffffffffu, need);
-                if (lane == 0) red_need[tile_ctr & 1][warp] = need;
-                named_bar_sync(1, 128);
-                need = red_need[tile_ctr & 1][0] | red_need[tile_ctr & 1][1] | red_need[tile_ctr & 1][2] | red_need[tile_ctr & 1][3];
-                if (need) {   // the same value in all four warps
-#pragma unroll
-                    for (int q = 0; q < kN; ++q)
-                        if ((need >> q) & 1u) {
-                            const float mx = warp_max(x[q]);
-                            if (lane == 0) rb[warp][q] = mx;
-                        }
-                    named_bar_sync(1, 128);
+                for (int q = 0; q < NC; ++q) {
+                    x[q] = (CAUSAL ? kv < lim[q] : valid) ? __uint_as_float(sv[q]) * p.c : -INFINITY;
+                    above |= x[q] > m[q] + kRescaleD;
                 }
-                ++tile_ctr;
-                float alpha[kN], pv[kN];
+                const bool moved = bar_any128(1, above);   // the same in all four warps
+                float alpha[NC];
+                if (moved) {
 #pragma unroll
-                for (int q = 0; q < kN; ++q) {
-                    if (q < G) {
-                        alpha[q] = 1.f;
-                        if ((need >> q) & 1u) {
-                            const float mt = fmaxf(fmaxf(rb[0][q], rb[1][q]), fmaxf(rb[2][q], rb[3][q]));
-                            // a column without a finite reference yet has nothing to rescale
-                            alpha[q] = m[q] == -INFINITY ? 0.f : ex2_approx(m[q] - mt);
-                            m[q] = mt;
-                        }
-                        // a column with no visible key so far keeps m = -inf (no -inf - -inf)
-                        pv[q] = m[q] == -INFINITY ? 0.f : ex2_approx(x[q] - m[q]);
-                        l[q] = fmaf(l[q], alpha[q], pv[q]);
-                    } else {
-                        alpha[q] = 0.f;
-                        pv[q] = 0.f;
+                    for (int q = 0; q < NC; ++q) {
+                        const float mx = redux_max(x[q]);
+                        if (lane == 0) red_max[warp][q] = mx;
                     }
+                    named_bar_sync(1, 128);
+#pragma unroll
+                    for (int q = 0; q < NC; ++q) {
+                        const float mt = fmaxf(fmaxf(red_max[0][q], red_max[1][q]), fmaxf(red_max[2][q], red_max[3][q]));
+                        const bool up = mt > m[q] + kRescaleD;
+                        // a column without a finite reference yet has nothing to rescale
+                        alpha[q] = !up ? 1.f : m[q] == -INFINITY ? 0.f : ex2_approx(m[q] - mt);
+                        m[q] = up ? mt : m[q];
+                    }
+                }
+                // a column with no visible key so far keeps m = -inf: its scores are -inf, and so is x - 0
+#pragma unroll
+                for (int q = 0; q < NC; ++q) {
+                    pv[q] = ex2_approx(x[q] - (m[q] == -INFINITY ? 0.f : m[q]));
+                    l[q] = moved ? fmaf(l[q], alpha[q], pv[q]) : l[q] + pv[q];
                 }
                 // Keys at or beyond n in a partial tile: their V rows may hold anything (NaN in
                 // padded memory) and P = 0 does not cancel NaN in the MMA, so zero those rows.
@@ -869,19 +932,23 @@ __global__ void __launch_bounds__(decode_threads<EPI>(), 1)
                     }
                 }
                 vr.advance();
+                // rows of P beyond NC keep what they held: they only reach columns of O that nobody reads
                 mbar_wait(&p_empty[pr.idx], pr.phase ^ 1, wc);
                 uint8_t* sP = smem + C::kOffP + pr.idx * C::kPBytes;
 #pragma unroll
-                for (int q = 0; q < kN; ++q)
+                for (int q = 0; q < NC; ++q)
                     *reinterpret_cast<uint16_t*>(sP + sw128_offset(q, tid, kN * 128)) = float_to_bf16_bits(pv[q]);
                 fence_proxy_async_smem();
-                mbar_arrive(&p_full[pr.idx]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[pr.idx]);
                 pr.advance();
-                if (t > it.t0) consume(alpha_prev);
+                if (t > it.t0) consume();
+                moved_prev = moved;
+                if (moved)
 #pragma unroll
-                for (int q = 0; q < kN; ++q) alpha_prev[q] = alpha[q];
+                    for (int q = 0; q < NC; ++q) alpha_prev[q] = alpha[q];
             }
-            if (it.t1 > it.t0) consume(alpha_prev);
+            if (it.t1 > it.t0) consume();
 
             if constexpr (!EPI) {
                 run_epilogue(it, it.t1 <= it.t0, m, l, acc, tid, warp, 1, false);
@@ -895,19 +962,22 @@ __global__ void __launch_bounds__(decode_threads<EPI>(), 1)
                 mbar_wait(&ep_empty[hr.idx], hr.phase ^ 1, wc);
                 tc_fence_after();
                 __syncwarp();   // tcgen05.st is warp-collective
-                uint32_t hv[32];
+                if constexpr (EPI) {
+                    uint32_t hv[2 * NC];
 #pragma unroll
-                for (int q = 0; q < kN; ++q) {
-                    hv[q] = __float_as_uint(acc[q]);
-                    hv[kN + q] = __float_as_uint(l[q]);
+                    for (int q = 0; q < NC; ++q) {
+                        hv[q] = __float_as_uint(acc[q]);
+                        hv[NC + q] = __float_as_uint(l[q]);
+                    }
+                    tmem_st<2 * NC>(tmem + lane_base + 64 + hr.idx * 32, hv);
+                    tmem_st_wait();
                 }
-                tmem_st32(tmem + lane_base + 64 + hr.idx * 32, hv);
-                tmem_st_wait();
                 if (tid == 0)
 #pragma unroll
-                    for (int q = 0; q < kN; ++q) ep_m[hr.idx][q] = m[q];
+                    for (int q = 0; q < NC; ++q) ep_m[hr.idx][q] = m[q];
                 tc_fence_before();
-                mbar_arrive(&ep_full[hr.idx]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ep_full[hr.idx]);
             }
             hr.advance();
         }
@@ -929,20 +999,21 @@ __global__ void __launch_bounds__(decode_threads<EPI>(), 1)
             tc_fence_after();
             __syncwarp();   // tcgen05.ld is warp-collective
             const bool empty = it.t1 <= it.t0;
-            float m[kN], l[kN], acc[kN];
+            float m[NC], l[NC], acc[NC];
             {
-                uint32_t hv[32];
-                tmem_ld32(tmem + lane_base + 64 + hr.idx * 32, hv);
+                uint32_t hv[2 * NC];
+                tmem_ld<2 * NC>(tmem + lane_base + 64 + hr.idx * 32, hv);
                 tmem_ld_wait();
 #pragma unroll
-                for (int q = 0; q < kN; ++q) {
+                for (int q = 0; q < NC; ++q) {
                     acc[q] = __uint_as_float(hv[q]);
-                    l[q] = __uint_as_float(hv[kN + q]);
+                    l[q] = __uint_as_float(hv[NC + q]);
                     m[q] = ep_m[hr.idx][q];
                 }
             }
             tc_fence_before();
-            mbar_arrive(&ep_empty[hr.idx]);
+            __syncwarp();
+            if (lane_id() == 0) mbar_arrive(&ep_empty[hr.idx]);
             hr.advance();
 
             run_epilogue(it, empty, m, l, acc, tid, ew, 2, pre);

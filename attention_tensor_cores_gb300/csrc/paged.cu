@@ -90,6 +90,17 @@ int make_pool_map(CUtensorMap* map, const void* pool, const fmha_kv_cache* c, in
 }
 
 template <int D, bool CAUSAL>
+auto kernel_for(int G) -> decltype(&decode_kernel<D, CAUSAL, 1, true>)
+{
+    switch (decode_columns(G)) {
+        case 1: return decode_kernel<D, CAUSAL, 1, true>;
+        case 4: return decode_kernel<D, CAUSAL, 4, true>;
+        case 8: return decode_kernel<D, CAUSAL, 8, true>;
+        default: return decode_kernel<D, CAUSAL, 16, true>;
+    }
+}
+
+template <int D, bool CAUSAL>
 int run_paged(const PagedArgs& a, bool split, const PagedWs& w, uint8_t* base, cudaStream_t st)
 {
     using C = DecodeCfg<D>;
@@ -153,15 +164,12 @@ int run_paged(const PagedArgs& a, bool split, const PagedWs& w, uint8_t* base, c
         count_launch();
     }
     const bool epi = s.G > 1;   // as in the dense decode: the epilogue warpgroup pays with several columns
-    const void* fn = epi ? reinterpret_cast<const void*>(decode_kernel<D, CAUSAL, true, true>)
-                         : reinterpret_cast<const void*>(decode_kernel<D, CAUSAL, false, true>);
-    FMHA_CHECK_CUDA(set_smem_limit_once(fn, C::kSmemBytes));
+    const auto kernel = kernel_for<D, CAUSAL>(s.G);
+    FMHA_CHECK_CUDA(set_smem_limit_once(reinterpret_cast<const void*>(kernel), C::kSmemBytes));
     const unsigned grid = static_cast<unsigned>(split ? nsm : (s.U < nsm ? s.U : nsm));
     timing_mark_begin(st);
-    const cudaError_t e = epi ? launch_pdl(decode_kernel<D, CAUSAL, true, true>, dim3(grid), dim3(decode_threads<true>()),
-                                           C::kSmemBytes, st, qmap, kmap, vmap, p)
-                              : launch_pdl(decode_kernel<D, CAUSAL, false, true>, dim3(grid), dim3(decode_threads<false>()),
-                                           C::kSmemBytes, st, qmap, kmap, vmap, p);
+    const cudaError_t e = launch_pdl(kernel, dim3(grid), dim3(epi ? decode_threads<true>() : decode_threads<false>()), C::kSmemBytes,
+                                     st, qmap, kmap, vmap, p);
     timing_mark_end(st);
     FMHA_CHECK_CUDA(e);
     count_launch();
