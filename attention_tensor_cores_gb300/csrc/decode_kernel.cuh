@@ -41,6 +41,17 @@ namespace atc_gb300 {
 namespace {
 
 constexpr int kTileKV = 128;    // keys per tile = MMA M
+
+// A K or V tile in shared memory is made of 1024-byte swizzle atoms, 8 keys of 64 features each.  Dense:
+// the 16 atoms of the first 64 features, then those of the next.  Paged at D = 128: the two atoms of 8 keys
+// side by side, so that a TMA box can bring whole keys.
+template <int D, bool PAGED>
+struct TileLayout {
+    static constexpr bool kInter = PAGED && D == 128;
+    static constexpr int kGroup = kInter ? 2048 : 1024;            // bytes from 8 keys to the next 8
+    static constexpr int kHalf = kInter ? 1024 : kTileKV * 128;    // bytes from 64 features to the next 64
+    __device__ static constexpr int row(int k) { return (k >> 3) * kGroup + (k & 7) * 128; }
+};
 constexpr int kN = 16;          // query rows per unit, padded (MMA N)
 // EPI: softmax, epilogue and control warpgroups (warps 0-3, 4-7, 8-11: producer 8, MMA 9); else the
 // softmax warps run each item's epilogue themselves and warps 4 and 5 are the producer and the MMA.
@@ -108,6 +119,7 @@ struct DecodeParams {
     int max_pages, num_pages;
     int page;                // keys per page, a multiple of 8
     int box;                 // keys per TMA box: the largest power of two up to 128 dividing `page`
+    int groups;              // D = 128: runs of 8 keys from one page to the next in the tensor map
     int cap;                 // max_pages * page: lengths are clamped to it
     int chunks;              // units per key/value head: its Gtot query rows in chunks of G
     int Gtot;
@@ -218,6 +230,16 @@ struct Sched {
 
 // Status word value of a page index outside the pool or a length outside its table row
 constexpr int kDevBadPage = 7;
+
+__device__ __forceinline__ void tma_load_5d_hint(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z, int w, int v,
+                                                 uint64_t policy)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2], %8;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "l"(policy)
+        : "memory");
+}
 
 __device__ __forceinline__ void tma_load_4d_hint(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z, int w,
                                                  uint64_t policy)
@@ -623,10 +645,10 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
         // ------------------------------------------------ TMA producer
         if constexpr (PAGED) {
             // A tile is filled in boxes of p.box keys, each inside one page, up to the request's length (rows
-            // behind it keep what the buffer held: their scores are masked and their V rows zeroed).  Lane
-            // (i, a) of the warp looks up the page of box i and issues its 64-feature half a, for K and for V;
-            // the next tile's pages are looked up before this tile's buffers are waited for.  A page outside
-            // the pool loads zeros (the tensor map's fill) and sets the status.
+            // behind it keep what the buffer held: their scores are masked and their V rows zeroed).  Lane i
+            // of the warp looks up the page of box i and issues it, for K and for V; the next tile's pages
+            // are looked up before this tile's buffers are waited for.  A page outside the pool loads zeros
+            // (the tensor map's fill) and sets the status.
             const int lane = static_cast<int>(lane_id());
             if (lane == 0) {
                 tma_prefetch_desc(&qmap);
@@ -637,8 +659,15 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
             Ring qr(2), kr(S), vr(S);
             uint32_t kcnt[S], vcnt[S], qcnt[2] = {0, 0};
             for (int i = 0; i < S; ++i) kcnt[i] = vcnt[i] = 0;
-            const int boxes = kTileKV / p.box;
-            const int i = lane % boxes, a = lane / boxes;
+            const int i = lane, boxes = kTileKV / p.box;
+            using L = TileLayout<D, PAGED>;
+            auto load_box = [&](uint8_t* tile, const CUtensorMap* map, uint64_t* bar, int page, int off, int head) {
+                uint8_t* dst = tile + i * (p.box / 8) * L::kGroup;
+                if constexpr (L::kInter)
+                    tma_load_5d_hint(dst, map, bar, 0, 0, 0, page * p.groups + off / 8, head, pol);
+                else
+                    tma_load_4d_hint(dst, map, bar, 0, off, head, page, pol);
+            };
             // lane 0 waits for the buffer and announces `bytes`; the warp goes on unless the CTA has aborted
             auto claim = [&](uint64_t* empty, uint64_t* full, uint32_t phase, uint32_t bytes) {
                 int go = 0;
@@ -657,7 +686,7 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
                 int page = 0, off = -1;
                 auto look_up = [&](int t) {
                     const int j = t * kTileKV + i * p.box;
-                    if (a < C::kAtoms && j < it.n) {
+                    if (i < boxes && j < it.n) {
                         const int s = j / p.page;
                         page = row[s];
                         off = j - s * p.page;
@@ -683,18 +712,15 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
                     }
                     const int used = (min(it.n - t * kTileKV, kTileKV) + p.box - 1) / p.box;
                     const uint32_t bytes = static_cast<uint32_t>(used * p.box * 128 * C::kAtoms);
-                    const int at = a * (kTileKV * 128) + i * p.box * 128;
                     if (claim(&k_empty[kr.idx], &k_full[kr.idx], kr.phase, bytes)) {
                         if (off_t >= 0)
-                            tma_load_4d_hint(smem + C::kOffK + kr.idx * C::kKVBytes + at, &kmap, &k_full[kr.idx], a * 64, off_t, head,
-                                             page_t, pol);
+                            load_box(smem + C::kOffK + kr.idx * C::kKVBytes, &kmap, &k_full[kr.idx], page_t, off_t, head);
                         ++kcnt[kr.idx];
                     }
                     kr.advance();
                     if (claim(&v_empty[vr.idx], &v_full[vr.idx], vr.phase, bytes)) {
                         if (off_t >= 0)
-                            tma_load_4d_hint(smem + C::kOffV + vr.idx * C::kKVBytes + at, &vmap, &v_full[vr.idx], a * 64, off_t, head,
-                                             page_t, pol);
+                            load_box(smem + C::kOffV + vr.idx * C::kKVBytes, &vmap, &v_full[vr.idx], page_t, off_t, head);
                         ++vcnt[vr.idx];
                     }
                     vr.advance();
@@ -765,7 +791,8 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
         if (lane_id() == 0) {
             constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kN, false, false);
             constexpr uint32_t idesc_pv = idesc_bf16_f32(128, kN, true, false);
-            constexpr uint32_t lbo_v = (D >= 128) ? 16384u : 0u;   // D = 64: M rows 64..127 repeat 0..63
+            using L = TileLayout<D, PAGED>;
+            constexpr uint32_t lbo_v = (D >= 128) ? L::kHalf : 0u;   // D = 64: M rows 64..127 repeat 0..63
             Ring qr(2), kr(S), vr(S), sr(2), pr(2), orr(2);
             auto pv = [&]() {
                 mbar_wait(&p_full[pr.idx], pr.phase, wc);
@@ -778,7 +805,7 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
                     const uint32_t dO = tmem + 32 + orr.idx * 16;
 #pragma unroll
                     for (int ks = 0; ks < kTileKV / 16; ++ks) {
-                        const uint64_t da = sdesc_sw128(sV + ks * 2048, lbo_v, 1024);
+                        const uint64_t da = sdesc_sw128(sV + ks * 2 * L::kGroup, lbo_v, L::kGroup);
                         const uint64_t db = sdesc_sw128(sP + (ks >> 2) * (kN * 128) + (ks & 3) * 32, 16, 1024);
                         mma_ss(dO, da, db, idesc_pv, ks > 0 ? 1u : 0u);
                     }
@@ -806,7 +833,7 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
                         const uint32_t dS = tmem + sr.idx * 16;
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint64_t da = sdesc_sw128(sK + (kk >> 2) * (kTileKV * 128) + (kk & 3) * 32, 16, 1024);
+                            const uint64_t da = sdesc_sw128(sK + (kk >> 2) * L::kHalf + (kk & 3) * 32, 16, L::kGroup);
                             const uint64_t db = sdesc_sw128(sQ + (kk >> 2) * (kN * 128) + (kk & 3) * 32, 16, 1024);
                             mma_ss(dS, da, db, idesc_qk, kk > 0 ? 1u : 0u);
                         }
@@ -923,12 +950,12 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
                 if ((t + 1) * kTileKV > it.n) {
                     mbar_wait(&v_full[vr.idx], vr.phase, wc);
                     if (!valid) {
-                        uint8_t* rowp = smem + C::kOffV + vr.idx * C::kKVBytes + tid * 128;
+                        uint8_t* rowp = smem + C::kOffV + vr.idx * C::kKVBytes + TileLayout<D, PAGED>::row(tid);
 #pragma unroll
                         for (int a = 0; a < C::kAtoms; ++a)
 #pragma unroll
                             for (int i = 0; i < 8; ++i)
-                                reinterpret_cast<uint4*>(rowp + a * (kTileKV * 128))[i] = make_uint4(0, 0, 0, 0);
+                                reinterpret_cast<uint4*>(rowp + a * TileLayout<D, PAGED>::kHalf)[i] = make_uint4(0, 0, 0, 0);
                     }
                 }
                 vr.advance();

@@ -5,10 +5,10 @@
 //   pool[table[b][j / page]][kv-head][j % page]
 //
 // A 128-key tile is filled by TMA boxes of the largest power of two of keys that divides both the page
-// and the tile, one tensor map of four dimensions (feature, key in page, head, page) per pool, so any
-// strides of pages, heads and keys work and offsets never pass through 32-bit arithmetic.  A box of
-// 2^i >= 8 rows of 64 features is a whole number of 128-byte-swizzle atoms, which makes the tile in
-// shared memory the same as a dense one.
+// and the tile; the tensor maps take any strides of pages, heads and keys, and offsets never pass through
+// 32-bit arithmetic.  A box of 2^i >= 8 keys is a whole number of 128-byte-swizzle atoms of 8 keys x 64
+// features.  At D = 128 the map has five dimensions (feature of 64, key of 8, half of the features, run of
+// 8 keys over all pages, head), so that one box brings whole 256-byte keys: half the boxes.
 #include <cuda_runtime.h>
 
 #include "decode_kernel.cuh"
@@ -79,8 +79,19 @@ PagedWs paged_ws(int B, int Hq, int Sq, const fmha_kv_cache* c, const fmha_opts*
     return w;
 }
 
+// D = 128: runs of 8 keys from one page to the next
+int64_t page_groups(const fmha_kv_cache* c) { return c->num_pages > 1 ? c->page_stride / (8 * c->token_stride) : c->page_size / 8; }
+
 int make_pool_map(CUtensorMap* map, const void* pool, const fmha_kv_cache* c, int box)
 {
+    if (c->D == 128) {
+        const uint64_t dims[5] = {64, 8, 2, static_cast<uint64_t>((c->num_pages - 1) * page_groups(c) + c->page_size / 8),
+                                  static_cast<uint64_t>(c->Hkv)};
+        const uint64_t strides[4] = {static_cast<uint64_t>(c->token_stride) * 2, 128, static_cast<uint64_t>(c->token_stride) * 16,
+                                     static_cast<uint64_t>(c->head_stride) * 2};
+        const uint32_t boxes[5] = {64, 8, 2, static_cast<uint32_t>(box / 8), 1};
+        return make_tmap_bf16(map, pool, 5, dims, strides, boxes);
+    }
     const uint64_t dims[4] = {static_cast<uint64_t>(c->D), static_cast<uint64_t>(c->page_size), static_cast<uint64_t>(c->Hkv),
                               static_cast<uint64_t>(c->num_pages)};
     const uint64_t strides[3] = {static_cast<uint64_t>(c->token_stride) * 2, static_cast<uint64_t>(c->head_stride) * 2,
@@ -139,6 +150,7 @@ int run_paged(const PagedArgs& a, bool split, const PagedWs& w, uint8_t* base, c
     p.num_pages = a.c->num_pages;
     p.page = a.c->page_size;
     p.box = box;
+    p.groups = static_cast<int>(page_groups(a.c));
     p.cap = a.max_pages * a.c->page_size;
     p.Skv = p.cap;
     p.split = split ? 1 : 0;
@@ -187,6 +199,10 @@ int check_paged(const fmha_kv_cache* c, int B, int Hq, int Sq, int max_pages, co
     if (B < 0 || Hq <= 0 || Sq < 0 || max_pages < 1 || Hq % c->Hkv != 0)
         return set_error(FMHA_ERR_INVALID, std::string(who) + ": need B >= 0, Sq >= 0, max_pages >= 1, Hq > 0 a multiple of Hkv");
     if (c->page_size % 8 != 0) return set_error(FMHA_ERR_UNSUPPORTED, std::string(who) + ": page_size must be a multiple of 8");
+    if (c->D == 128 && c->num_pages > 1 &&
+        (c->page_stride % (8 * c->token_stride) != 0 || page_groups(c) < c->page_size / 8 || page_groups(c) * (c->num_pages + 1LL) >= (1LL << 31)))
+        return set_error(FMHA_ERR_UNSUPPORTED, std::string(who) + ": with D = 128, page_stride must be a multiple of 8 * token_stride that "
+                                                                  "holds a page, and the pool less than 2^31 runs of 8 tokens");
     const long long cap = static_cast<long long>(max_pages) * c->page_size;
     const long long rows = static_cast<long long>(B) * Hq * Sq;
     const long long units = static_cast<long long>(B) * c->Hkv * ((static_cast<long long>(Hq / c->Hkv) * Sq + kN - 1) / kN);

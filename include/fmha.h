@@ -262,7 +262,7 @@ int fmha_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_s
  * Attention of the last Sq tokens of each request over its pages: fmha_fwd_ex with K and V row j of
  * request b taken from the cache through block_table (int32 [B][max_pages]) and seqlens[b] keys (device
  * int32[B], 0 <= seqlens[b] <= max_pages * page_size).  q, out, lse as in fmha_fwd; D and Hkv are the
- * cache's; page_size a multiple of 8.
+ * cache's; page_size a multiple of 8; with D = 128 page_stride a multiple of 8 * token_stride.
  *   opts (NULL: defaults): out_kind, num_splits, workspace, causal and the NVFP4 fields as for fmha_fwd_ex;
  *   seqlens_k must be NULL.  With a workspace of fmha_paged_workspace_size() bytes the keys are split over
  *   every SM, without one each (request, kv-head) is one CTA's.
