@@ -94,7 +94,7 @@ struct DecodeParams {
     int Sq;             // query rows per head (column q of a unit is query q % Sq)
     float c;            // scale * log2(e)
     const int32_t* seqlens;
-    const int32_t* prefix;   // [U+1] tile prefix (ragged split mode), else NULL
+    const int32_t* prefix;   // tile prefix of units (dense) or batch entries (paged), else NULL
     int tiles_uniform;       // tiles per unit when prefix == NULL
     int split;               // 1 = stream-K partition, 0 = whole units per CTA
     // outputs
@@ -159,6 +159,7 @@ struct Item {
 template <bool PAGED>
 struct Sched {
     const DecodeParams* p;
+    const int* pre;     // paged split mode: exclusive prefix of the batch entries' tiles
     long long g, g1;    // split mode: current / end global tile
     int u;              // whole-unit mode: next unit
     int cta, nctas;
@@ -175,13 +176,16 @@ struct Sched {
     }
     __device__ int unit_keys(int u) const { return p->seqlens ? batch_keys<PAGED>(*p, u / p->Hkv) : p->Skv; }
 
-    __device__ void init(const DecodeParams* pp, int c, int n)
+    __device__ void init(const DecodeParams* pp, int c, int n, const int* prefix)
     {
         p = pp;
+        pre = prefix;
         cta = c;
         nctas = n;
         if (p->split) {
-            const long long T = p->prefix ? p->prefix[p->U] : static_cast<long long>(p->U) * p->tiles_uniform;
+            const long long T = PAGED       ? static_cast<long long>(pre[p->U / p->Hkv]) * p->Hkv
+                                : p->prefix ? p->prefix[p->U]
+                                            : static_cast<long long>(p->U) * p->tiles_uniform;
             g = (static_cast<long long>(c) * T) / n;
             g1 = (static_cast<long long>(c + 1) * T) / n;
         } else {
@@ -193,6 +197,25 @@ struct Sched {
     {
         if (p->split) {
             if (g >= g1) return false;
+            if constexpr (PAGED) {
+                // the last batch entry that starts at or before tile g (one without tiles ends there too)
+                int lo = 0, hi = p->U / p->Hkv - 1;
+                while (lo < hi) {
+                    const int mid = (lo + hi + 1) >> 1;
+                    if (static_cast<long long>(pre[mid]) * p->Hkv <= g) lo = mid; else hi = mid - 1;
+                }
+                const int nt = pre[lo + 1] - pre[lo];
+                const int r = static_cast<int>(g - static_cast<long long>(pre[lo]) * p->Hkv);   // < Hkv * nt < 2^31
+                const int i = r / nt;
+                it.u = lo * p->Hkv + i;
+                it.t0 = r - i * nt;
+                it.t1 = static_cast<int>(min(static_cast<long long>(nt), g1 - g + it.t0));
+                it.n = batch_keys<true>(*p, lo);
+                it.whole = (it.t0 == 0 && it.t1 == nt);
+                it.slot = it.u + cta;
+                g += it.t1 - it.t0;
+                return true;
+            }
             int uu;
             if (p->prefix) {   // last unit whose start <= g (prefix is non-decreasing)
                 int lo = 0, hi = p->U - 1;
@@ -359,11 +382,15 @@ __device__ __forceinline__ float warp_sum(float v)
 // Stream-K: the CTAs holding partials of unit u are c0..c1 of P, skipping CTAs whose tile range is
 // empty (possible when there are fewer tiles than CTAs).  Fills slots[] (partial slots u + c, at
 // most cap) and returns how many there are; 0 for a unit without tiles.
-__device__ int unit_partial_slots(const DecodeParams& p, int u, int P, int* slots, int cap)
+template <bool PAGED>
+__device__ __forceinline__ void unit_range(const DecodeParams& p, const int* pre, int u, int& tiles, long long& Tu, long long& T)
 {
-    int tiles;
-    long long Tu, T;
-    if (p.prefix) {
+    if constexpr (PAGED) {
+        const int b = u / p.Hkv;
+        tiles = pre[b + 1] - pre[b];
+        Tu = static_cast<long long>(pre[b]) * p.Hkv + static_cast<long long>(u - b * p.Hkv) * tiles;
+        T = static_cast<long long>(pre[p.U / p.Hkv]) * p.Hkv;
+    } else if (p.prefix) {
         tiles = p.prefix[u + 1] - p.prefix[u];
         Tu = p.prefix[u];
         T = p.prefix[p.U];
@@ -372,6 +399,14 @@ __device__ int unit_partial_slots(const DecodeParams& p, int u, int P, int* slot
         Tu = static_cast<long long>(u) * tiles;
         T = static_cast<long long>(p.U) * tiles;
     }
+}
+
+template <bool PAGED>
+__device__ int unit_partial_slots(const DecodeParams& p, const int* pre, int u, int P, int* slots, int cap)
+{
+    int tiles;
+    long long Tu, T;
+    unit_range<PAGED>(p, pre, u, tiles, Tu, T);
     if (tiles <= 0) return 0;
     const int c0 = static_cast<int>(min((((Tu + 1) * P) - 1) / T, static_cast<long long>(P - 1)));
     const int c1 = static_cast<int>(min((((Tu + tiles) * P) - 1) / T, static_cast<long long>(P - 1)));
@@ -382,6 +417,29 @@ __device__ int unit_partial_slots(const DecodeParams& p, int u, int P, int* slot
 }
 
 constexpr int kMaxFixSlots = 512;
+constexpr int kFixChunk = 32;   // partials whose weights are in shared memory at once
+
+// Paged split mode finds the work split itself when it has up to this many batch entries: every CTA sums
+// the entries' tiles into its shared memory, which costs less than a launch that leaves them in global
+// memory.
+constexpr int kInlineB = 1024;
+
+// O = 0 and LSE = -inf for batch entry b without keys, by the whole CTA
+__device__ __forceinline__ void write_empty_entry(const DecodeParams& p, int b)
+{
+    const size_t rows = static_cast<size_t>(p.Hkv / p.chunks) * p.Gtot, r0 = b * rows, n = rows * p.D;
+    for (size_t i = threadIdx.x; i < n; i += blockDim.x) {
+        if (p.o_stage) p.o_stage[r0 * p.D + i] = 0.f;
+        if (p.out) {
+            if (p.out_f32)
+                static_cast<float*>(p.out)[r0 * p.D + i] = 0.f;
+            else
+                static_cast<uint16_t*>(p.out)[r0 * p.D + i] = 0;
+        }
+    }
+    if (p.lse)
+        for (size_t i = threadIdx.x; i < rows; i += blockDim.x) p.lse[r0 + i] = -INFINITY;
+}
 
 // Columns the softmax computes for units of G rows (the MMA's N stays kN): 1, 4, 8 or 16.
 inline int decode_columns(int G) { return G <= 1 ? 1 : G <= 4 ? 4 : G <= 8 ? 8 : 16; }
@@ -409,7 +467,8 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
     __shared__ int ep_abort, fx_last;          // softmax warps: abort snapshot, "this CTA merges"
     __shared__ int fx_n;
     __shared__ int fx_slot[kMaxFixSlots];
-    __shared__ float fx_w[kN][4], fx_lse[kN];   // merge: per column, the partials' weights and the merged LSE
+    __shared__ float fx_w[kN][kFixChunk], fx_lse[kN];   // merge: per column, the partials' weights and the merged LSE
+    __shared__ int pre_sh[PAGED ? kInlineB + 1 : 1], pre_warp[PAGED ? 12 : 1];
 
     const int warp = threadIdx.x / 32;
     griddep_launch_dependents();
@@ -449,14 +508,43 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
     griddep_wait();   // the previous kernel of the stream has completed: global memory from here on
     if (blockIdx.x == 0 && threadIdx.x == 0 && p.nv_ts) *p.nv_ts = *p.nv_sg;   // single-pass NVFP4: report s_g
 
+    const int* pre = p.prefix;
     if constexpr (PAGED) {
+        const int B = p.U / p.Hkv;
         if (blockIdx.x == 0)
-            for (int b = threadIdx.x; b < p.U / p.Hkv; b += blockDim.x)
+            for (int b = threadIdx.x; b < B; b += blockDim.x)
                 if (p.seqlens[b] < 0 || p.seqlens[b] > p.cap) atomicExch(p.status, kDevBadPage);
+        if (p.split && !p.prefix) {
+            // a run of entries per thread, then a scan over the threads
+            const int per = (B + blockDim.x - 1) / blockDim.x;
+            const int b0 = min(B, static_cast<int>(threadIdx.x) * per), b1 = min(B, b0 + per);
+            int own = 0;
+            for (int b = b0; b < b1; ++b) own += (batch_keys<true>(p, b) + kTileKV - 1) / kTileKV;
+            int inc = own;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, inc, o);
+                if ((threadIdx.x & 31) >= o) inc += v;
+            }
+            if ((threadIdx.x & 31) == 31) pre_warp[warp] = inc;
+            __syncthreads();
+            int run = inc - own;
+            for (int w = 0; w < warp; ++w) run += pre_warp[w];
+            for (int b = b0; b < b1; ++b) {
+                pre_sh[b] = run;
+                run += (batch_keys<true>(p, b) + kTileKV - 1) / kTileKV;
+            }
+            if (threadIdx.x == blockDim.x - 1) pre_sh[B] = run;
+            __syncthreads();
+            pre = pre_sh;
+        }
+        if (p.fixup)   // no combine kernel runs: entries without keys are written here
+            for (int b = blockIdx.x; b < B; b += gridDim.x)
+                if (pre[b + 1] == pre[b]) write_empty_entry(p, b);
     }
 
     Sched<PAGED> sched;
-    sched.init(&p, blockIdx.x, gridDim.x);
+    sched.init(&p, blockIdx.x, gridDim.x, pre);
     Item it;
 
     // The epilogue of one item, run by 128 threads: the epilogue warpgroup (named barrier 2) when a
@@ -470,17 +558,17 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
         const int lane = static_cast<int>(lane_id());
         const int G = unit_cols<PAGED>(p, it.u);
         const float nv_sg = p.nv_sg ? *p.nv_sg : 0.f;
-        // final output of one row at column tid (tid < D); the |O| max goes to amax_acc
-        auto write_final = [&](size_t row, float o, float lse_v, float& amax_acc) {
-            if (p.o_stage) p.o_stage[row * D + tid] = o;
+        // final output of one row at column d; the |O| max goes to amax_acc
+        auto write_final = [&](size_t row, float o, float lse_v, float& amax_acc, int d) {
+            if (p.o_stage) p.o_stage[row * D + d] = o;
             if (p.amax_bits) amax_acc = fmaxf(amax_acc, fabsf(o));
             if (p.out) {
                 if (p.out_f32)
-                    static_cast<float*>(p.out)[row * D + tid] = o;
+                    static_cast<float*>(p.out)[row * D + d] = o;
                 else
-                    static_cast<uint16_t*>(p.out)[row * D + tid] = float_to_bf16_bits(o);
+                    static_cast<uint16_t*>(p.out)[row * D + d] = float_to_bf16_bits(o);
             }
-            if (tid == 0 && p.lse) p.lse[row] = lse_v;
+            if (d == 0 && p.lse) p.lse[row] = lse_v;
         };
         // ---- epilogue: L = sum over the 128 key lanes, O = acc · (1 / L), lse = ln2 * (m + log2 L)
         if (!empty) {
@@ -532,7 +620,7 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
                 const float lse_v = col_lse[q];
                 const size_t row = unit_row0<PAGED>(p, it.u) + q;
                 if (final_here) {
-                    write_final(row, o, lse_v, local_amax);
+                    write_final(row, o, lse_v, local_amax, tid);
                     // single-pass NVFP4: a warp holds 32 consecutive columns of the row
                     if (p.nv_codes) nvfp4_encode_lanes(o, nv_sg, tid, p.nv_codes + row * (D / 2), p.nv_scales + row * (D / 16));
                 } else {
@@ -553,7 +641,7 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
             // fence waits for the stores instead of 128.
             named_bar_sync(bar, 128);
             if (tid == 0) {
-                const int n = slots_ready ? fx_n : unit_partial_slots(p, it.u, static_cast<int>(gridDim.x), fx_slot, kMaxFixSlots);
+                const int n = slots_ready ? fx_n : unit_partial_slots<PAGED>(p, pre, it.u, static_cast<int>(gridDim.x), fx_slot, kMaxFixSlots);
                 fx_n = n;
                 __threadfence();
                 const int arrived = n > 0 ? arrive_unit(p.unit_ctr + it.u, p.gen, n) : 0;
@@ -606,27 +694,70 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
                         float o = 0.f;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) o = fmaf(fx_w[q][i], ov[q][i], o);
-                        if (tid < D) write_final(unit_row0<PAGED>(p, it.u) + q, o, fx_lse[q], amax_m);
+                        if (tid < D) write_final(unit_row0<PAGED>(p, it.u) + q, o, fx_lse[q], amax_m, tid);
                     }
                 } else {
-                    for (int q = 0; q < G; ++q) {
-                        float mx = -INFINITY;
-                        for (int i = 0; i < ns; ++i) mx = fmaxf(mx, __ldcg(p.part_lse + static_cast<size_t>(fx_slot[i]) * kN + q));
-                        // partials without a visible key carry lse = -inf and weigh 0; all of them -> empty row
-                        const bool any = mx > -INFINITY;
-                        float sum = 0.f;
-                        if (any)
-                            for (int i = 0; i < ns; ++i) sum += __expf(__ldcg(p.part_lse + static_cast<size_t>(fx_slot[i]) * kN + q) - mx);
-                        const float lse_all = (ns > 0 && any) ? mx + __logf(sum) : -INFINITY;
-                        if (tid < D) {
-                            float o = 0.f;
-                            if (any)
-                                for (int i = 0; i < ns; ++i) {
-                                    const size_t sl = static_cast<size_t>(fx_slot[i]) * kN + q;
-                                    o = fmaf(__expf(__ldcg(p.part_lse + sl) - lse_all), __ldcg(p.part_o + sl * D + tid), o);
-                                }
-                            write_final(unit_row0<PAGED>(p, it.u) + q, o, lse_all, amax_m);
+                    // Many partials (a long sequence over many CTAs): two round trips whatever their number up
+                    // to 32.  First the partials' LSEs, a warp per column and a lane per partial; then every
+                    // partial's O, four groups of lanes of a warp taking every fourth partial and eight lanes 32
+                    // columns of D, summed over the groups by shuffles at the end.
+                    const int d = ew * 32 + (lane & 7) * 4, first = lane >> 3;
+                    float4 sum4[NC];
+#pragma unroll
+                    for (int q = 0; q < NC; ++q) sum4[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int c0 = 0; c0 < ns; c0 += kFixChunk) {
+                        const int nc = min(kFixChunk, ns - c0);
+                        if (c0) named_bar_sync(bar, 128);   // the previous chunk's weights have been used
+                        for (int q = ew; q < G; q += 4) {
+                            if (c0 == 0) {
+                                float mx = -INFINITY, sum = 0.f;
+                                for (int i = lane; i < ns; i += 32)
+                                    mx = fmaxf(mx, __ldcg(p.part_lse + static_cast<size_t>(fx_slot[i]) * kN + q));
+                                mx = redux_max(mx);
+                                // partials without a visible key carry lse = -inf and weigh 0; all of them -> empty row
+                                if (mx > -INFINITY)
+                                    for (int i = lane; i < ns; i += 32)
+                                        sum += __expf(__ldcg(p.part_lse + static_cast<size_t>(fx_slot[i]) * kN + q) - mx);
+                                sum = warp_sum(sum);
+                                if (lane == 0) fx_lse[q] = mx > -INFINITY ? mx + __logf(sum) : -INFINITY;
+                                __syncwarp();
+                            }
+                            const float all = fx_lse[q];
+                            if (lane < nc)
+                                fx_w[q][lane] = all > -INFINITY ? __expf(__ldcg(p.part_lse + static_cast<size_t>(fx_slot[c0 + lane]) * kN + q) - all) : 0.f;
                         }
+                        named_bar_sync(bar, 128);
+                        if (d < D) {
+#pragma unroll(NC == 1 ? 8 : 1)
+                            for (int i = first; i < nc; i += 4) {
+                                const float* src = p.part_o + static_cast<size_t>(fx_slot[c0 + i]) * kN * D + d;
+                                float4 v[NC];
+#pragma unroll
+                                for (int q = 0; q < NC; ++q)
+                                    v[q] = q < G ? __ldcg(reinterpret_cast<const float4*>(src + q * D)) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                                for (int q = 0; q < NC; ++q) {
+                                    const float w = q < G ? fx_w[q][i] : 0.f;
+                                    sum4[q].x = fmaf(w, v[q].x, sum4[q].x);
+                                    sum4[q].y = fmaf(w, v[q].y, sum4[q].y);
+                                    sum4[q].z = fmaf(w, v[q].z, sum4[q].z);
+                                    sum4[q].w = fmaf(w, v[q].w, sum4[q].w);
+                                }
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int q = 0; q < NC; ++q) {
+                        if (q >= G) break;
+                        float o[4] = {sum4[q].x, sum4[q].y, sum4[q].z, sum4[q].w};
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            o[x] += __shfl_xor_sync(0xffffffffu, o[x], 8);
+                            o[x] += __shfl_xor_sync(0xffffffffu, o[x], 16);
+                        }
+                        // the four lanes of a column group hold the same sums: each writes one column
+                        const float mine = first == 0 ? o[0] : first == 1 ? o[1] : first == 2 ? o[2] : o[3];
+                        if (d < D) write_final(unit_row0<PAGED>(p, it.u) + q, mine, fx_lse[q], amax_m, d + first);
                     }
                 }
                 if (p.amax_bits) {
@@ -860,7 +991,6 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
         const int lane = static_cast<int>(lane_id());
         const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
         Ring sr(2), pr(2), orr(2), vr(S), hr(2);
-        uint32_t tile_ctr = 0;
         while (sched.next(it)) {
             const int G = unit_cols<PAGED>(p, it.u);
             float m[NC], l[NC], acc[NC], alpha_prev[NC];
@@ -1020,8 +1150,8 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
         while (sched.next(it)) {   // the softmax warpgroup's sequence of items
             // a partial's slots (64-bit divisions) while the softmax warps still stream the item, off
             // the path from its last tile to its arrival count
-            const bool pre = p.fixup && !(it.whole && !(p.split && p.nv_codes)) && it.t1 > it.t0;
-            if (pre && tid == 0) fx_n = unit_partial_slots(p, it.u, static_cast<int>(gridDim.x), fx_slot, kMaxFixSlots);
+            const bool partial = p.fixup && !(it.whole && !(p.split && p.nv_codes)) && it.t1 > it.t0;
+            if (partial && tid == 0) fx_n = unit_partial_slots<PAGED>(p, pre, it.u, static_cast<int>(gridDim.x), fx_slot, kMaxFixSlots);
             mbar_wait(&ep_full[hr.idx], hr.phase, wc);
             tc_fence_after();
             __syncwarp();   // tcgen05.ld is warp-collective
@@ -1043,7 +1173,7 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
             if (lane_id() == 0) mbar_arrive(&ep_empty[hr.idx]);
             hr.advance();
 
-            run_epilogue(it, empty, m, l, acc, tid, ew, 2, pre);
+            run_epilogue(it, empty, m, l, acc, tid, ew, 2, partial);
         }
       }
     }
@@ -1057,14 +1187,15 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
 template <bool PAGED>
 __global__ void __launch_bounds__(1024) tile_prefix_kernel(const __grid_constant__ DecodeParams p, int32_t* prefix)
 {
-    const int U = p.U;
+    // dense: the units' tiles; paged: the batch entries' tiles
+    const int U = PAGED ? p.U / p.Hkv : p.U, per_entry = PAGED ? 1 : p.Hkv;
     griddep_launch_dependents();
     griddep_wait();
     __shared__ int part[1024];
     const int per = (U + 1023) / 1024;
     const int b0 = threadIdx.x * per;
     int s = 0;
-    for (int u = b0; u < min(U, b0 + per); ++u) s += (batch_keys<PAGED>(p, u / p.Hkv) + kTileKV - 1) / kTileKV;
+    for (int u = b0; u < min(U, b0 + per); ++u) s += (batch_keys<PAGED>(p, u / per_entry) + kTileKV - 1) / kTileKV;
     part[threadIdx.x] = s;
     __syncthreads();
     for (int off = 1; off < 1024; off <<= 1) {
@@ -1076,7 +1207,7 @@ __global__ void __launch_bounds__(1024) tile_prefix_kernel(const __grid_constant
     int run = threadIdx.x ? part[threadIdx.x - 1] : 0;
     for (int u = b0; u < min(U, b0 + per); ++u) {
         prefix[u] = run;
-        run += (batch_keys<PAGED>(p, u / p.Hkv) + kTileKV - 1) / kTileKV;
+        run += (batch_keys<PAGED>(p, u / per_entry) + kTileKV - 1) / kTileKV;
     }
     if (threadIdx.x == 1023) prefix[U] = part[1023];
 }
@@ -1104,15 +1235,7 @@ __global__ void combine_kernel(const __grid_constant__ DecodeParams p, int nctas
     if (threadIdx.x < 32) {
         int tiles;
         long long Tu, T;
-        if (p.prefix) {
-            tiles = p.prefix[u + 1] - p.prefix[u];
-            Tu = p.prefix[u];
-            T = p.prefix[p.U];
-        } else {
-            tiles = p.tiles_uniform;
-            Tu = static_cast<long long>(u) * tiles;
-            T = static_cast<long long>(p.U) * tiles;
-        }
+        unit_range<PAGED>(p, p.prefix, u, tiles, Tu, T);
         int cnt = 0;
         if (tiles > 0) {
             const long long P = nctas;

@@ -53,6 +53,11 @@ struct PagedWs {
     size_t prefix_off, ctr_off, lse_off, o_off, stage_off, amax_off, total;
 };
 
+// The kernel finds the work split and merges split units itself, except for single-pass NVFP4, whose rows a
+// combine kernel encodes (as in the dense decode), and very large batches, whose split a kernel of its own
+// finds.
+bool needs_prefix(int B, bool encode) { return encode || B > kInlineB; }
+
 PagedWs paged_ws(int B, int Hq, int Sq, const fmha_kv_cache* c, const fmha_opts* o)
 {
     auto al = [](size_t x) { return (x + 255) & ~size_t(255); };
@@ -63,7 +68,7 @@ PagedWs paged_ws(int B, int Hq, int Sq, const fmha_kv_cache* c, const fmha_opts*
     PagedWs w{};
     size_t off = 0;
     w.prefix_off = off;
-    off += split ? al((static_cast<size_t>(s.U) + 1) * 4) : 0;
+    off += split && needs_prefix(B, o->nvfp4_scale_in != nullptr) ? al((static_cast<size_t>(B) + 1) * 4) : 0;
     w.ctr_off = off;
     off += split ? al(static_cast<size_t>(s.U) * 8) : 0;
     w.lse_off = off;
@@ -154,7 +159,8 @@ int run_paged(const PagedArgs& a, bool split, const PagedWs& w, uint8_t* base, c
     p.cap = a.max_pages * a.c->page_size;
     p.Skv = p.cap;
     p.split = split ? 1 : 0;
-    p.prefix = split ? reinterpret_cast<const int32_t*>(base + w.prefix_off) : nullptr;
+    p.fixup = split && !a.nv_sg && nsm <= kMaxFixSlots ? 1 : 0;
+    p.prefix = split && needs_prefix(a.B, a.nv_sg != nullptr) ? reinterpret_cast<const int32_t*>(base + w.prefix_off) : nullptr;
     p.out = a.out_kind == FMHA_OUT_NVFP4 ? nullptr : a.out;
     p.out_f32 = a.out_kind == FMHA_OUT_F32 ? 1 : 0;
     p.lse = a.lse;
@@ -171,21 +177,23 @@ int run_paged(const PagedArgs& a, bool split, const PagedWs& w, uint8_t* base, c
     p.status = device_status_ptr();
     p.limit = wait_limit();
 
-    if (split) {
+    if (p.prefix) {
         FMHA_CHECK_CUDA(launch_pdl(tile_prefix_kernel<true>, dim3(1), dim3(1024), 0, st, p, const_cast<int32_t*>(p.prefix)));
         count_launch();
     }
     const bool epi = s.G > 1;   // as in the dense decode: the epilogue warpgroup pays with several columns
     const auto kernel = kernel_for<D, CAUSAL>(s.G);
     FMHA_CHECK_CUDA(set_smem_limit_once(reinterpret_cast<const void*>(kernel), C::kSmemBytes));
-    const unsigned grid = static_cast<unsigned>(split ? nsm : (s.U < nsm ? s.U : nsm));
+    // one CTA per SM, or fewer when even full tables have fewer key tiles (whole units: fewer units)
+    const long long tiles = split ? static_cast<long long>(s.U) * ((p.cap + kTileKV - 1) / kTileKV) : s.U;
+    const unsigned grid = static_cast<unsigned>(tiles < nsm ? tiles : nsm);
     timing_mark_begin(st);
     const cudaError_t e = launch_pdl(kernel, dim3(grid), dim3(epi ? decode_threads<true>() : decode_threads<false>()), C::kSmemBytes,
                                      st, qmap, kmap, vmap, p);
     timing_mark_end(st);
     FMHA_CHECK_CUDA(e);
     count_launch();
-    if (split) {
+    if (split && !p.fixup) {
         FMHA_CHECK_CUDA(launch_pdl(combine_kernel<true>, dim3(static_cast<unsigned>(s.U * s.G)), dim3(static_cast<unsigned>(D)), 0,
                                    st, p, static_cast<int>(grid)));
         count_launch();
