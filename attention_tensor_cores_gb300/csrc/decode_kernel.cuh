@@ -160,6 +160,7 @@ template <bool PAGED>
 struct Sched {
     const DecodeParams* p;
     const int* pre;     // paged split mode: exclusive prefix of the batch entries' tiles
+    const int* keys;    // and their keys, if in shared memory
     long long g, g1;    // split mode: current / end global tile
     int u;              // whole-unit mode: next unit
     int cta, nctas;
@@ -176,10 +177,11 @@ struct Sched {
     }
     __device__ int unit_keys(int u) const { return p->seqlens ? batch_keys<PAGED>(*p, u / p->Hkv) : p->Skv; }
 
-    __device__ void init(const DecodeParams* pp, int c, int n, const int* prefix)
+    __device__ void init(const DecodeParams* pp, int c, int n, const int* prefix, const int* lengths)
     {
         p = pp;
         pre = prefix;
+        keys = lengths;
         cta = c;
         nctas = n;
         if (p->split) {
@@ -210,7 +212,7 @@ struct Sched {
                 it.u = lo * p->Hkv + i;
                 it.t0 = r - i * nt;
                 it.t1 = static_cast<int>(min(static_cast<long long>(nt), g1 - g + it.t0));
-                it.n = batch_keys<true>(*p, lo);
+                it.n = keys ? keys[lo] : batch_keys<true>(*p, lo);
                 it.whole = (it.t0 == 0 && it.t1 == nt);
                 it.slot = it.u + cta;
                 g += it.t1 - it.t0;
@@ -416,7 +418,7 @@ __device__ int unit_partial_slots(const DecodeParams& p, const int* pre, int u, 
     return n;
 }
 
-constexpr int kMaxFixSlots = 512;
+constexpr int kMaxFixSlots = 160;   // at most one partial of a unit per SM
 constexpr int kFixChunk = 32;   // partials whose weights are in shared memory at once
 
 // Paged split mode finds the work split itself when it has up to this many batch entries: every CTA sums
@@ -468,7 +470,7 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
     __shared__ int fx_n;
     __shared__ int fx_slot[kMaxFixSlots];
     __shared__ float fx_w[kN][kFixChunk], fx_lse[kN];   // merge: per column, the partials' weights and the merged LSE
-    __shared__ int pre_sh[PAGED ? kInlineB + 1 : 1], pre_warp[PAGED ? 12 : 1];
+    __shared__ int pre_sh[PAGED ? kInlineB + 1 : 1], keys_sh[PAGED ? kInlineB : 1], pre_warp[PAGED ? 12 : 1];
 
     const int warp = threadIdx.x / 32;
     griddep_launch_dependents();
@@ -508,7 +510,7 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
     griddep_wait();   // the previous kernel of the stream has completed: global memory from here on
     if (blockIdx.x == 0 && threadIdx.x == 0 && p.nv_ts) *p.nv_ts = *p.nv_sg;   // single-pass NVFP4: report s_g
 
-    const int* pre = p.prefix;
+    const int *pre = p.prefix, *keys = nullptr;
     if constexpr (PAGED) {
         const int B = p.U / p.Hkv;
         if (blockIdx.x == 0)
@@ -519,7 +521,10 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
             const int per = (B + blockDim.x - 1) / blockDim.x;
             const int b0 = min(B, static_cast<int>(threadIdx.x) * per), b1 = min(B, b0 + per);
             int own = 0;
-            for (int b = b0; b < b1; ++b) own += (batch_keys<true>(p, b) + kTileKV - 1) / kTileKV;
+            for (int b = b0; b < b1; ++b) {
+                keys_sh[b] = batch_keys<true>(p, b);
+                own += (keys_sh[b] + kTileKV - 1) / kTileKV;
+            }
             int inc = own;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -532,11 +537,12 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
             for (int w = 0; w < warp; ++w) run += pre_warp[w];
             for (int b = b0; b < b1; ++b) {
                 pre_sh[b] = run;
-                run += (batch_keys<true>(p, b) + kTileKV - 1) / kTileKV;
+                run += (keys_sh[b] + kTileKV - 1) / kTileKV;
             }
             if (threadIdx.x == blockDim.x - 1) pre_sh[B] = run;
             __syncthreads();
             pre = pre_sh;
+            keys = keys_sh;
         }
         if (p.fixup)   // no combine kernel runs: entries without keys are written here
             for (int b = blockIdx.x; b < B; b += gridDim.x)
@@ -544,7 +550,7 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
     }
 
     Sched<PAGED> sched;
-    sched.init(&p, blockIdx.x, gridDim.x, pre);
+    sched.init(&p, blockIdx.x, gridDim.x, pre, keys);
     Item it;
 
     // The epilogue of one item, run by 128 threads: the epilogue warpgroup (named barrier 2) when a
@@ -697,38 +703,55 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
                         if (tid < D) write_final(unit_row0<PAGED>(p, it.u) + q, o, fx_lse[q], amax_m, tid);
                     }
                 } else {
-                    // Many partials (a long sequence over many CTAs): two round trips whatever their number up
-                    // to 32.  First the partials' LSEs, a warp per column and a lane per partial; then every
-                    // partial's O, four groups of lanes of a warp taking every fourth partial and eight lanes 32
-                    // columns of D, summed over the groups by shuffles at the end.
+                    // More partials (a long sequence over many CTAs): first their LSEs, a warp per column and a
+                    // lane per partial, all columns' loads in flight together; then their O, four groups of lanes
+                    // taking every fourth partial and eight lanes 32 columns of D, the groups' sums meeting in
+                    // shuffles at the end.
+                    constexpr int kCols = (NC + 3) / 4;
+                    auto load_lse = [&](int c, int i) {
+                        const int q = ew + 4 * c;
+                        return q < G && i < ns ? __ldcg(p.part_lse + static_cast<size_t>(fx_slot[i]) * kN + q) : -INFINITY;
+                    };
+                    float lv[kCols], mx[kCols], all[kCols];
+#pragma unroll
+                    for (int c = 0; c < kCols; ++c) mx[c] = lv[c] = load_lse(c, lane);
+                    for (int i = lane + kFixChunk; i < ns; i += kFixChunk)
+#pragma unroll
+                        for (int c = 0; c < kCols; ++c) mx[c] = fmaxf(mx[c], load_lse(c, i));
+#pragma unroll
+                    for (int c = 0; c < kCols; ++c) {
+                        mx[c] = redux_max(mx[c]);
+                        // partials without a visible key carry lse = -inf and weigh 0; all of them -> empty row
+                        all[c] = mx[c] > -INFINITY ? __expf(lv[c] - mx[c]) : 0.f;
+                    }
+                    for (int i = lane + kFixChunk; i < ns; i += kFixChunk)
+#pragma unroll
+                        for (int c = 0; c < kCols; ++c)
+                            if (mx[c] > -INFINITY) all[c] += __expf(load_lse(c, i) - mx[c]);
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+                        for (int c = 0; c < kCols; ++c) all[c] += __shfl_xor_sync(0xffffffffu, all[c], o);
+#pragma unroll
+                    for (int c = 0; c < kCols; ++c) {
+                        all[c] = mx[c] > -INFINITY ? mx[c] + __logf(all[c]) : -INFINITY;
+                        if (lane == 0 && ew + 4 * c < NC) fx_lse[ew + 4 * c] = all[c];
+                    }
                     const int d = ew * 32 + (lane & 7) * 4, first = lane >> 3;
                     float4 sum4[NC];
 #pragma unroll
                     for (int q = 0; q < NC; ++q) sum4[q] = make_float4(0.f, 0.f, 0.f, 0.f);
                     for (int c0 = 0; c0 < ns; c0 += kFixChunk) {
-                        const int nc = min(kFixChunk, ns - c0);
-                        if (c0) named_bar_sync(bar, 128);   // the previous chunk's weights have been used
-                        for (int q = ew; q < G; q += 4) {
-                            if (c0 == 0) {
-                                float mx = -INFINITY, sum = 0.f;
-                                for (int i = lane; i < ns; i += 32)
-                                    mx = fmaxf(mx, __ldcg(p.part_lse + static_cast<size_t>(fx_slot[i]) * kN + q));
-                                mx = redux_max(mx);
-                                // partials without a visible key carry lse = -inf and weigh 0; all of them -> empty row
-                                if (mx > -INFINITY)
-                                    for (int i = lane; i < ns; i += 32)
-                                        sum += __expf(__ldcg(p.part_lse + static_cast<size_t>(fx_slot[i]) * kN + q) - mx);
-                                sum = warp_sum(sum);
-                                if (lane == 0) fx_lse[q] = mx > -INFINITY ? mx + __logf(sum) : -INFINITY;
-                                __syncwarp();
-                            }
-                            const float all = fx_lse[q];
-                            if (lane < nc)
-                                fx_w[q][lane] = all > -INFINITY ? __expf(__ldcg(p.part_lse + static_cast<size_t>(fx_slot[c0 + lane]) * kN + q) - all) : 0.f;
+                        if (c0) named_bar_sync(bar, 128);   // the previous run's weights have been used
+#pragma unroll
+                        for (int c = 0; c < kCols; ++c) {
+                            const float x = c0 ? load_lse(c, c0 + lane) : lv[c];
+                            if (ew + 4 * c < NC) fx_w[ew + 4 * c][lane] = all[c] > -INFINITY ? __expf(x - all[c]) : 0.f;
                         }
                         named_bar_sync(bar, 128);
+                        const int nc = min(kFixChunk, ns - c0);
                         if (d < D) {
-#pragma unroll(NC == 1 ? 8 : 1)
+#pragma unroll(NC == 1 ? 8 : NC == 4 ? 4 : NC == 8 ? 2 : 1)
                             for (int i = first; i < nc; i += 4) {
                                 const float* src = p.part_o + static_cast<size_t>(fx_slot[c0 + i]) * kN * D + d;
                                 float4 v[NC];
@@ -737,7 +760,7 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
                                     v[q] = q < G ? __ldcg(reinterpret_cast<const float4*>(src + q * D)) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                                 for (int q = 0; q < NC; ++q) {
-                                    const float w = q < G ? fx_w[q][i] : 0.f;
+                                    const float w = fx_w[q][i];
                                     sum4[q].x = fmaf(w, v[q].x, sum4[q].x);
                                     sum4[q].y = fmaf(w, v[q].y, sum4[q].y);
                                     sum4[q].z = fmaf(w, v[q].z, sum4[q].z);
