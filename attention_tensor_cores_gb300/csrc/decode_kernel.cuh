@@ -118,27 +118,14 @@ struct DecodeParams {
     const int32_t* table;    // [B][max_pages] page of each run of `page` keys
     int max_pages, num_pages;
     int page;                // keys per page, a multiple of 8
+    uint32_t page_mul;       // j / page = j * page_mul >> page_shift for 0 <= j < 2^31
+    int page_shift;
     int box;                 // keys per TMA box: the largest power of two up to 128 dividing `page`
     int groups;              // D = 128: runs of 8 keys from one page to the next in the tensor map
     int cap;                 // max_pages * page: lengths are clamped to it
     int chunks;              // units per key/value head: its Gtot query rows in chunks of G
     int Gtot;
 };
-
-// Rows of a unit.  Dense: unit u = (b, kv-head) owns rows u * G .. u * G + G - 1.  Paged: a key/value
-// head with more than 16 query rows is cut into `chunks` units of at most G rows each.
-template <bool PAGED>
-__device__ __forceinline__ int unit_cols(const DecodeParams& p, int u)
-{
-    if constexpr (PAGED) return min(p.G, p.Gtot - (u % p.chunks) * p.G);
-    return p.G;
-}
-template <bool PAGED>
-__device__ __forceinline__ size_t unit_row0(const DecodeParams& p, int u)
-{
-    if constexpr (PAGED) return static_cast<size_t>(u / p.chunks) * p.Gtot + (u % p.chunks) * p.G;
-    return static_cast<size_t>(u) * p.G;
-}
 
 // Keys of batch entry b
 template <bool PAGED>
@@ -154,7 +141,33 @@ struct Item {
     int n;           // valid keys of the unit
     bool whole;      // covers every tile of the unit
     int slot;        // partial slot (u + cta)
+    int b, head, chunk;   // paged: batch entry, key/value head and chunk of its rows
 };
+
+template <bool PAGED>
+struct Sched;
+
+// Rows of a unit.  Dense: unit u = (b, kv-head) owns rows u * G .. u * G + G - 1.  Paged: a key/value
+// head with more than 16 query rows is cut into `chunks` units of at most G rows each.
+template <bool PAGED>
+__device__ __forceinline__ int unit_cols(const DecodeParams& p, const Item& it)
+{
+    if constexpr (PAGED) return min(p.G, p.Gtot - it.chunk * p.G);
+    return p.G;
+}
+template <bool PAGED>
+__device__ __forceinline__ size_t unit_row0(const DecodeParams& p, const Item& it)
+{
+    if constexpr (PAGED) return (static_cast<size_t>(it.b) * (p.Hkv / p.chunks) + it.head) * p.Gtot + it.chunk * p.G;
+    return static_cast<size_t>(it.u) * p.G;
+}
+// The unit's place in its batch entry
+__device__ __forceinline__ void place_unit(const DecodeParams& p, Item& it, int b, int i)
+{
+    it.b = b;
+    it.head = p.chunks == 1 ? i : i / p.chunks;
+    it.chunk = p.chunks == 1 ? 0 : i - it.head * p.chunks;
+}
 
 template <bool PAGED>
 struct Sched {
@@ -164,6 +177,7 @@ struct Sched {
     long long g, g1;    // split mode: current / end global tile
     int u;              // whole-unit mode: next unit
     int cta, nctas;
+    int b, i;           // paged split mode: batch entry and unit of it that tile g is in (first: i < 0)
 
     __device__ int unit_tiles(int u) const
     {
@@ -177,7 +191,7 @@ struct Sched {
     }
     __device__ int unit_keys(int u) const { return p->seqlens ? batch_keys<PAGED>(*p, u / p->Hkv) : p->Skv; }
 
-    __device__ void init(const DecodeParams* pp, int c, int n, const int* prefix, const int* lengths)
+    __device__ void init(const DecodeParams* pp, int c, int n, const int* prefix, const int* lengths, int first)
     {
         p = pp;
         pre = prefix;
@@ -188,6 +202,10 @@ struct Sched {
             const long long T = PAGED       ? static_cast<long long>(pre[p->U / p->Hkv]) * p->Hkv
                                 : p->prefix ? p->prefix[p->U]
                                             : static_cast<long long>(p->U) * p->tiles_uniform;
+            if constexpr (PAGED) {
+                b = first;
+                i = -1;
+            }
             g = (static_cast<long long>(c) * T) / n;
             g1 = (static_cast<long long>(c + 1) * T) / n;
         } else {
@@ -200,22 +218,27 @@ struct Sched {
         if (p->split) {
             if (g >= g1) return false;
             if constexpr (PAGED) {
-                // the last batch entry that starts at or before tile g (one without tiles ends there too)
-                int lo = 0, hi = p->U / p->Hkv - 1;
-                while (lo < hi) {
-                    const int mid = (lo + hi + 1) >> 1;
-                    if (static_cast<long long>(pre[mid]) * p->Hkv <= g) lo = mid; else hi = mid - 1;
+                // on to the batch entry that holds tile g (b >= the one before, entries may have no tiles)
+                while (static_cast<long long>(pre[b + 1]) * p->Hkv <= g) {
+                    ++b;
+                    i = 0;
                 }
-                const int nt = pre[lo + 1] - pre[lo];
-                const int r = static_cast<int>(g - static_cast<long long>(pre[lo]) * p->Hkv);   // < Hkv * nt < 2^31
-                const int i = r / nt;
-                it.u = lo * p->Hkv + i;
-                it.t0 = r - i * nt;
+                const int nt = pre[b + 1] - pre[b];
+                if (i < 0) {   // first item: the only one that may start inside a unit
+                    const int r = static_cast<int>(g - static_cast<long long>(pre[b]) * p->Hkv);   // < Hkv * nt < 2^31
+                    i = r / nt;
+                    it.t0 = r - i * nt;
+                } else {
+                    it.t0 = 0;
+                }
+                it.u = b * p->Hkv + i;
                 it.t1 = static_cast<int>(min(static_cast<long long>(nt), g1 - g + it.t0));
-                it.n = keys ? keys[lo] : batch_keys<true>(*p, lo);
+                it.n = keys ? keys[b] : batch_keys<true>(*p, b);
                 it.whole = (it.t0 == 0 && it.t1 == nt);
                 it.slot = it.u + cta;
+                place_unit(*p, it, b, i);
                 g += it.t1 - it.t0;
+                ++i;
                 return true;
             }
             int uu;
@@ -248,6 +271,7 @@ struct Sched {
         it.n = unit_keys(u);
         it.whole = true;
         it.slot = 0;
+        if constexpr (PAGED) place_unit(*p, it, u / p->Hkv, u % p->Hkv);
         u += nctas;
         return true;
     }
@@ -511,6 +535,7 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
     if (blockIdx.x == 0 && threadIdx.x == 0 && p.nv_ts) *p.nv_ts = *p.nv_sg;   // single-pass NVFP4: report s_g
 
     const int *pre = p.prefix, *keys = nullptr;
+    int first_b = 0;
     if constexpr (PAGED) {
         const int B = p.U / p.Hkv;
         if (blockIdx.x == 0)
@@ -544,13 +569,21 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
             pre = pre_sh;
             keys = keys_sh;
         }
+        if (p.split) {
+            // the batch entry that the CTA's first tile is in: its owner among the threads says so
+            const long long first = static_cast<long long>(blockIdx.x) * (static_cast<long long>(pre[B]) * p.Hkv) / gridDim.x;
+            for (int b = threadIdx.x; b < B; b += blockDim.x)
+                if (static_cast<long long>(pre[b]) * p.Hkv <= first && first < static_cast<long long>(pre[b + 1]) * p.Hkv) pre_warp[0] = b;
+            __syncthreads();
+            first_b = pre[B] > 0 ? pre_warp[0] : 0;
+        }
         if (p.fixup)   // no combine kernel runs: entries without keys are written here
             for (int b = blockIdx.x; b < B; b += gridDim.x)
                 if (pre[b + 1] == pre[b]) write_empty_entry(p, b);
     }
 
     Sched<PAGED> sched;
-    sched.init(&p, blockIdx.x, gridDim.x, pre, keys);
+    sched.init(&p, blockIdx.x, gridDim.x, pre, keys, first_b);
     Item it;
 
     // The epilogue of one item, run by 128 threads: the epilogue warpgroup (named barrier 2) when a
@@ -562,19 +595,36 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
     auto run_epilogue = [&](const Item& it, bool empty, const float (&m)[NC], const float (&l)[NC],
                             const float (&acc)[NC], int tid, int ew, int bar, bool slots_ready) {
         const int lane = static_cast<int>(lane_id());
-        const int G = unit_cols<PAGED>(p, it.u);
+        const int G = unit_cols<PAGED>(p, it);
         const float nv_sg = p.nv_sg ? *p.nv_sg : 0.f;
-        // final output of one row at column d; the |O| max goes to amax_acc
-        auto write_final = [&](size_t row, float o, float lse_v, float& amax_acc, int d) {
-            if (p.o_stage) p.o_stage[row * D + d] = o;
-            if (p.amax_bits) amax_acc = fmaxf(amax_acc, fabsf(o));
-            if (p.out) {
-                if (p.out_f32)
-                    static_cast<float*>(p.out)[row * D + d] = o;
-                else
-                    static_cast<uint16_t*>(p.out)[row * D + d] = float_to_bf16_bits(o);
+        const size_t row0 = unit_row0<PAGED>(p, it);
+        // final output of the unit's rows at column d < D; returns the |O| max when it is wanted.  The
+        // choices are made once, not per row: the rows' stores then go out back to back.
+        auto write_rows = [&](const float (&o)[NC], int d) {
+            float am = 0.f;
+            if (p.o_stage) {
+                float* dst = p.o_stage + row0 * D + d;
+#pragma unroll
+                for (int q = 0; q < NC; ++q)
+                    if (q < G) dst[q * D] = o[q];
             }
-            if (d == 0 && p.lse) p.lse[row] = lse_v;
+            if (p.amax_bits) {
+#pragma unroll
+                for (int q = 0; q < NC; ++q)
+                    if (q < G) am = fmaxf(am, fabsf(o[q]));
+            }
+            if (p.out && p.out_f32) {
+                float* dst = static_cast<float*>(p.out) + row0 * D + d;
+#pragma unroll
+                for (int q = 0; q < NC; ++q)
+                    if (q < G) dst[q * D] = o[q];
+            } else if (p.out) {
+                uint16_t* dst = static_cast<uint16_t*>(p.out) + row0 * D + d;
+#pragma unroll
+                for (int q = 0; q < NC; ++q)
+                    if (q < G) dst[q * D] = float_to_bf16_bits(o[q]);
+            }
+            return am;
         };
         // ---- epilogue: L = sum over the 128 key lanes, O = acc · (1 / L), lse = ln2 * (m + log2 L)
         if (!empty) {
@@ -618,22 +668,27 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
         // short units)
         const bool final_here = it.whole && !(p.split && p.nv_codes);
         float local_amax = 0.f;
-        if (tid < D) {
+        float o[NC];
 #pragma unroll
-            for (int q = 0; q < NC; ++q) {
-                if (q >= G) break;
-                const float o = col_inv[q] > 0.f ? acc[q] * col_inv[q] : 0.f;   // 0: no visible key in this range
-                const float lse_v = col_lse[q];
-                const size_t row = unit_row0<PAGED>(p, it.u) + q;
-                if (final_here) {
-                    write_final(row, o, lse_v, local_amax, tid);
-                    // single-pass NVFP4: a warp holds 32 consecutive columns of the row
-                    if (p.nv_codes) nvfp4_encode_lanes(o, nv_sg, tid, p.nv_codes + row * (D / 2), p.nv_scales + row * (D / 16));
-                } else {
-                    p.part_o[(static_cast<size_t>(it.slot) * kN + q) * D + tid] = o;
-                    if (tid == 0) p.part_lse[static_cast<size_t>(it.slot) * kN + q] = lse_v;
-                }
+        for (int q = 0; q < NC; ++q) o[q] = col_inv[q] > 0.f ? acc[q] * col_inv[q] : 0.f;   // 0: no visible key in this range
+        if (final_here) {
+            if (tid < D) {
+                local_amax = write_rows(o, tid);
+                if (p.nv_codes)   // single-pass NVFP4: a warp holds 32 consecutive columns of the row
+#pragma unroll
+                    for (int q = 0; q < NC; ++q)
+                        if (q < G)
+                            nvfp4_encode_lanes(o[q], nv_sg, tid, p.nv_codes + (row0 + q) * (D / 2), p.nv_scales + (row0 + q) * (D / 16));
             }
+            if (tid < G && p.lse) p.lse[row0 + tid] = col_lse[tid];
+        } else {
+            if (tid < D) {
+                float* dst = p.part_o + static_cast<size_t>(it.slot) * kN * D + tid;
+#pragma unroll
+                for (int q = 0; q < NC; ++q)
+                    if (q < G) dst[q * D] = o[q];
+            }
+            if (tid < G) p.part_lse[static_cast<size_t>(it.slot) * kN + tid] = col_lse[tid];
         }
         if (p.amax_bits && final_here) {
             const float wm = warp_max(local_amax);
@@ -670,14 +725,14 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
                     // (threads q < G) column q's partial LSEs, all in flight at once, so the merge
                     // costs one L2 round trip whatever the number of columns (a round per few
                     // columns was one dependent trip each, slow while the other CTAs stream)
-                    float ov[NC][4];
+                    float ov[4][NC];
 #pragma unroll
-                    for (int q = 0; q < NC; ++q)
+                    for (int i = 0; i < 4; ++i) {
+                        const bool use = i < ns && tid < D;
+                        const float* src = p.part_o + static_cast<size_t>(fx_slot[i < ns ? i : 0]) * kN * D + tid;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const bool use = q < G && i < ns && tid < D;
-                            ov[q][i] = use ? __ldcg(p.part_o + (static_cast<size_t>(fx_slot[i < ns ? i : 0]) * kN + q) * D + tid) : 0.f;
-                        }
+                        for (int q = 0; q < NC; ++q) ov[i][q] = use && q < G ? __ldcg(src + q * D) : 0.f;
+                    }
                     if (tid < G) {
                         float lv[4];
 #pragma unroll
@@ -696,12 +751,11 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
                     named_bar_sync(bar, 128);
 #pragma unroll
                     for (int q = 0; q < NC; ++q) {
-                        if (q >= G) break;
-                        float o = 0.f;
+                        o[q] = 0.f;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) o = fmaf(fx_w[q][i], ov[q][i], o);
-                        if (tid < D) write_final(unit_row0<PAGED>(p, it.u) + q, o, fx_lse[q], amax_m, tid);
+                        for (int i = 0; i < 4; ++i) o[q] = fmaf(fx_w[q][i], ov[i][q], o[q]);
                     }
+                    if (tid < D) amax_m = write_rows(o, tid);
                 } else {
                     // More partials (a long sequence over many CTAs): first their LSEs, a warp per column and a
                     // lane per partial, all columns' loads in flight together; then their O, four groups of lanes
@@ -729,9 +783,9 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
                         for (int c = 0; c < kCols; ++c)
                             if (mx[c] > -INFINITY) all[c] += __expf(load_lse(c, i) - mx[c]);
 #pragma unroll
-                    for (int o = 16; o > 0; o >>= 1)
+                    for (int x = 16; x > 0; x >>= 1)
 #pragma unroll
-                        for (int c = 0; c < kCols; ++c) all[c] += __shfl_xor_sync(0xffffffffu, all[c], o);
+                        for (int c = 0; c < kCols; ++c) all[c] += __shfl_xor_sync(0xffffffffu, all[c], x);
 #pragma unroll
                     for (int c = 0; c < kCols; ++c) {
                         all[c] = mx[c] > -INFINITY ? mx[c] + __logf(all[c]) : -INFINITY;
@@ -771,18 +825,18 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
                     }
 #pragma unroll
                     for (int q = 0; q < NC; ++q) {
-                        if (q >= G) break;
-                        float o[4] = {sum4[q].x, sum4[q].y, sum4[q].z, sum4[q].w};
+                        float x[4] = {sum4[q].x, sum4[q].y, sum4[q].z, sum4[q].w};
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            o[x] += __shfl_xor_sync(0xffffffffu, o[x], 8);
-                            o[x] += __shfl_xor_sync(0xffffffffu, o[x], 16);
+                        for (int k = 0; k < 4; ++k) {
+                            x[k] += __shfl_xor_sync(0xffffffffu, x[k], 8);
+                            x[k] += __shfl_xor_sync(0xffffffffu, x[k], 16);
                         }
                         // the four lanes of a column group hold the same sums: each writes one column
-                        const float mine = first == 0 ? o[0] : first == 1 ? o[1] : first == 2 ? o[2] : o[3];
-                        if (d < D) write_final(unit_row0<PAGED>(p, it.u) + q, mine, fx_lse[q], amax_m, d + first);
+                        o[q] = first == 0 ? x[0] : first == 1 ? x[1] : first == 2 ? x[2] : x[3];
                     }
+                    if (d < D) amax_m = write_rows(o, d + first);
                 }
+                if (tid < G && p.lse) p.lse[row0 + tid] = fx_lse[tid];
                 if (p.amax_bits) {
                     const float wm = warp_max(amax_m);
                     if (lane == 0 && wm > 0.f) atomicMax(p.amax_bits, __float_as_uint(wm));
@@ -834,14 +888,14 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
             };
             while (sched.next(it)) {
                 if (it.t1 <= it.t0) continue;
-                const int b = it.u / p.Hkv, head = (it.u % p.Hkv) / p.chunks;
-                const int32_t* row = p.table + static_cast<size_t>(b) * p.max_pages;
+                const int head = it.head;
+                const int32_t* row = p.table + static_cast<size_t>(it.b) * p.max_pages;
                 // page and first key in it of this lane's box of tile t (-1: it has none)
                 int page = 0, off = -1;
                 auto look_up = [&](int t) {
                     const int j = t * kTileKV + i * p.box;
                     if (i < boxes && j < it.n) {
-                        const int s = j / p.page;
+                        const int s = static_cast<int>((static_cast<unsigned long long>(j) * p.page_mul) >> p.page_shift);   // j / page
                         page = row[s];
                         off = j - s * p.page;
                     } else {
@@ -852,7 +906,7 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
                 if (claim(&q_empty[qr.idx], &q_full[qr.idx], qr.phase, C::kQBytes)) {
                     if (lane < C::kAtoms)
                         tma_load_3d(smem + C::kOffQ + qr.idx * C::kQBytes + lane * (kN * 128), &qmap, &q_full[qr.idx], lane * 64,
-                                    (it.u % p.chunks) * p.G, it.u / p.chunks);
+                                    it.chunk * p.G, it.b * (p.Hkv / p.chunks) + head);
                     ++qcnt[qr.idx];
                 }
                 qr.advance();
@@ -1015,14 +1069,14 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
         const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
         Ring sr(2), pr(2), orr(2), vr(S), hr(2);
         while (sched.next(it)) {
-            const int G = unit_cols<PAGED>(p, it.u);
+            const int G = unit_cols<PAGED>(p, it);
             float m[NC], l[NC], acc[NC], alpha_prev[NC];
             // keys visible to column q: 0 .. lim[q] - 1 (causal: query q % Sq sees keys up to
             // (q % Sq) + n - Sq; otherwise all n)
             int lim[NC];
 #pragma unroll
             for (int q = 0; q < NC; ++q)
-                lim[q] = CAUSAL ? it.n - p.Sq + 1 + (((PAGED ? (it.u % p.chunks) * p.G : 0) + q) % p.Sq) : it.n;
+                lim[q] = CAUSAL ? it.n - p.Sq + 1 + (((PAGED ? it.chunk * p.G : 0) + q) % p.Sq) : it.n;
 #pragma unroll
             for (int q = 0; q < NC; ++q) {
                 m[q] = q < G ? -INFINITY : INFINITY;   // a column without a query: P = 0, never the largest
@@ -1252,7 +1306,12 @@ __global__ void combine_kernel(const __grid_constant__ DecodeParams p, int nctas
     const int row = blockIdx.x;
     const int u = row / p.G;
     const int q = row % p.G;
-    if (PAGED && q >= unit_cols<PAGED>(p, u)) return;   // the last chunk of a head may have fewer rows
+    Item it{};
+    it.u = u;
+    if constexpr (PAGED) {
+        place_unit(p, it, u / p.Hkv, u % p.Hkv);
+        if (q >= unit_cols<PAGED>(p, it)) return;   // the last chunk of a head may have fewer rows
+    }
     const int d = threadIdx.x;
     const int D = p.D;
     if (threadIdx.x < 32) {
@@ -1309,7 +1368,7 @@ __global__ void combine_kernel(const __grid_constant__ DecodeParams p, int nctas
     const float lse_v = lse_sh;
 #pragma unroll 4
     for (int i = 0; i < ns; ++i) o = fmaf(weights[i], p.part_o[(static_cast<size_t>(slots[i]) * kN + q) * D + d], o);
-    const size_t r = unit_row0<PAGED>(p, u) + q;
+    const size_t r = unit_row0<PAGED>(p, it) + q;
     if (p.o_stage) p.o_stage[r * D + d] = o;
     if (p.out) {
         if (p.out_f32)
