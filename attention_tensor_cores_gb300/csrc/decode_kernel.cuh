@@ -33,6 +33,7 @@
 #pragma once
 #include <cuda_runtime.h>
 
+#include "fastdiv.cuh"
 #include "internal.h"
 #include "nvfp4_dev.cuh"
 #include "ptx.cuh"
@@ -118,8 +119,7 @@ struct DecodeParams {
     const int32_t* table;    // [B][max_pages] page of each run of `page` keys
     int max_pages, num_pages;
     int page;                // keys per page, a multiple of 8
-    uint32_t page_mul;       // j / page = j * page_mul >> page_shift for 0 <= j < 2^31
-    int page_shift;
+    FastDiv by_page;
     int box;                 // keys per TMA box: the largest power of two up to 128 dividing `page`
     int groups;              // D = 128: runs of 8 keys from one page to the next in the tensor map
     int cap;                 // max_pages * page: lengths are clamped to it
@@ -895,7 +895,7 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
                 auto look_up = [&](int t) {
                     const int j = t * kTileKV + i * p.box;
                     if (i < boxes && j < it.n) {
-                        const int s = static_cast<int>((static_cast<unsigned long long>(j) * p.page_mul) >> p.page_shift);   // j / page
+                        const int s = p.by_page.div(j);
                         page = row[s];
                         off = j - s * p.page;
                     } else {

@@ -10,13 +10,15 @@
 //   token t, request b, position pos = ctx_b + t - cu_b:  slot = table[b][pos / P] * P + pos % P
 //
 // taken(a) that falls on a page given back in this call is found through roff and the finished request's
-// table row, not through the stack, so no thread reads what another one writes.  The lengths and the
-// stack height may be updated in place: every CTA keeps them in shared memory before any is written.
+// table row, not through the stack, so no thread reads what another one writes, except that the lengths
+// and the stack height may be updated in place: a CTA has them in shared memory before it writes them, and
+// a launch of several CTAs leaves them to a second launch when they are.
 //
 // Bound: launch latency and a chain of dependent loads (lengths, table or stack entry) for a decoding
 // step; 12 bytes written per token for prompts.
 #include <cuda_runtime.h>
 
+#include "fastdiv.cuh"
 #include "paged.h"
 #include "ptx.cuh"
 
@@ -41,23 +43,63 @@ struct PageTableParams {
     int T;
     int32_t* free_count_out;
     int* status;
+    FastDiv by_page;
+    int top;      // the largest power of two below B
+    int parts;    // kTables, kLengths or both
 };
 
-// last b with start[b] <= x (start non-decreasing, start[0] = 0): the request that item x belongs to
-__device__ __forceinline__ int owner(const int* start, int B, int x)
+// What a launch writes: the tables and slots, or what may be updated in place (lengths and stack height).
+enum : int { kTables = 1, kLengths = 2 };
+
+// last b with start[b] <= x (start non-decreasing, start[0] = 0): the request that item x belongs to.  top: the
+// largest power of two below B (0 for B = 1).
+__device__ __forceinline__ int owner(const int* start, int B, int top, int x)
 {
-    int lo = 0, hi = B - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (start[mid] <= x) lo = mid; else hi = mid - 1;
-    }
-    return lo;
+    int b = 0;
+    for (int s = top; s > 0; s >>= 1)
+        if (b + s < B && start[b + s] <= x) b += s;
+    return b;
 }
 
-struct Sums {
+struct Sums {   // new tokens, pages taken, pages given back
     long long add, need, back;
+
+    __device__ __forceinline__ Sums operator+(const Sums& o) const { return {add + o.add, need + o.need, back + o.back}; }
+    __device__ __forceinline__ Sums operator-(const Sums& o) const { return {add - o.add, need - o.need, back - o.back}; }
 };
 
+// inclusive sums over the lanes of a warp
+__device__ __forceinline__ Sums warp_scan(Sums v, int lane)
+{
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const Sums u{__shfl_up_sync(0xffffffffu, v.add, o), __shfl_up_sync(0xffffffffu, v.need, o), __shfl_up_sync(0xffffffffu, v.back, o)};
+        if (lane >= o) v = v + u;
+    }
+    return v;
+}
+
+// What request b asks for; sets `bad` for lengths that cannot be.
+__device__ __forceinline__ Sums request(const PageTableParams& p, int c, int a, bool& bad)
+{
+    Sums r{0, 0, 0};
+    const long long room = static_cast<long long>(p.max_pages) * p.page;   // below 2^31
+    if (c < 0 || c > room || (a > 0 && static_cast<long long>(c) + a > room)) {
+        bad = true;
+        return r;
+    }
+    const int held = p.by_page.up(c);
+    if (a < 0) {
+        r.back = held;
+    } else {
+        r.add = a;
+        r.need = p.by_page.up(c + a) - held;
+    }
+    return r;
+}
+
+// RUN: tokens (and pages) a lane takes of 32 * RUN consecutive ones of its warp, their loads in flight together
+template <int RUN>
 __global__ void __launch_bounds__(1024) page_table_kernel(const __grid_constant__ PageTableParams p)
 {
     extern __shared__ int sh[];
@@ -78,41 +120,20 @@ __global__ void __launch_bounds__(1024) page_table_kernel(const __grid_constant_
     bool bad = false;
     Sums own{0, 0, 0};
     for (int b = b0; b < b1; ++b) {
-        const int c = p.ctx[b], a = p.add[b];
-        const long long held = (static_cast<long long>(c) + P - 1) / P;
-        if (c < 0 || held > p.max_pages) bad = true;
-        if (a < 0) {
-            own.back += held;
-        } else {
-            const long long after = (static_cast<long long>(c) + a + P - 1) / P;
-            if (after > p.max_pages) bad = true;
-            own.add += a;
-            own.need += after - held;
-        }
+        const int c = p.ctx[b];
+        s_ctx[b] = c;
+        own = own + request(p, c, p.add[b], bad);
     }
     if (tid == 0) s_n = *p.free_count;
-    Sums inc = own;
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, inc.add, o), y = __shfl_up_sync(0xffffffffu, inc.need, o),
-                        z = __shfl_up_sync(0xffffffffu, inc.back, o);
-        if (lane >= o) {
-            inc.add += x;
-            inc.need += y;
-            inc.back += z;
-        }
-    }
+    const Sums inc = warp_scan(own, lane);
     if (lane == 31) warp_sums[warp] = inc;
     bad = __syncthreads_or(bad);
-    if (tid == 0) {
-        Sums run{0, 0, 0};
-        for (int w = 0; w < nw; ++w) {
-            const Sums v = warp_sums[w];
-            warp_sums[w] = run;
-            run.add += v.add;
-            run.need += v.need;
-            run.back += v.back;
-        }
-        total = run;
+    if (warp == 0) {
+        const Sums mine = lane < nw ? warp_sums[lane] : Sums{0, 0, 0};
+        const Sums all = warp_scan(mine, lane);
+        __syncwarp();
+        if (lane < nw) warp_sums[lane] = all - mine;
+        if (lane == 31) total = all;
     }
     __syncthreads();
     const Sums tot = total;
@@ -120,89 +141,106 @@ __global__ void __launch_bounds__(1024) page_table_kernel(const __grid_constant_
     // all or nothing: without room for every request, or with a length that cannot be, nothing changes
     bad = bad || n < 0 || n + tot.back > p.num_pages || tot.need > n + tot.back || tot.add > p.T;
     if (!bad) {
-        Sums at = warp_sums[warp];
-        at.add += inc.add - own.add;
-        at.need += inc.need - own.need;
-        at.back += inc.back - own.back;
+        Sums at = warp_sums[warp] + inc - own;
         for (int b = b0; b < b1; ++b) {
-            const int c = p.ctx[b], a = p.add[b];
-            const int held = static_cast<int>((static_cast<long long>(c) + P - 1) / P);
-            s_ctx[b] = c;
             s_cu[b] = static_cast<int>(at.add);
             s_aoff[b] = static_cast<int>(at.need);
             s_roff[b] = static_cast<int>(at.back);
-            if (a < 0) {
-                at.back += held;
-            } else {
-                at.add += a;
-                at.need += static_cast<int>((static_cast<long long>(c) + a + P - 1) / P) - held;
-            }
+            if (b + 1 < b1) at = at + request(p, s_ctx[b], p.add[b], bad);
         }
-    } else {
-        for (int b = b0; b < b1; ++b) s_ctx[b] = p.ctx[b];
     }
-    // every CTA has read the lengths and the stack height: from here on they may be overwritten
-    cluster_sync();
+    // the lengths and the stack height have been read: from here on they may be overwritten
+    __syncthreads();
 
     const int first = blockIdx.x * blockDim.x + tid, step = gridDim.x * blockDim.x;
     if (bad) {
-        for (int b = first; b <= B; b += step) {
-            p.cu[b] = 0;
-            if (b < B) p.seqlens[b] = s_ctx[b];
+        if (p.parts & kTables) {
+            for (int b = first; b <= B; b += step) p.cu[b] = 0;
+            for (int t = first; t < p.T; t += step) {
+                p.positions[t] = 0;
+                p.slots[t] = -1;
+            }
+            if (first == 0) atomicExch(p.status, kDevBadPage);
         }
-        for (int t = first; t < p.T; t += step) {
-            p.positions[t] = 0;
-            p.slots[t] = -1;
-        }
-        if (first == 0) {
-            *p.free_count_out = n;
-            atomicExch(p.status, kDevBadPage);
+        if (p.parts & kLengths) {
+            for (int b = first; b < B; b += step) p.seqlens[b] = s_ctx[b];
+            if (first == 0) *p.free_count_out = n;
         }
         return;
     }
     const int taken_n = static_cast<int>(tot.need), given_n = static_cast<int>(tot.back), tokens = static_cast<int>(tot.add);
-    auto given = [&](int r) {
-        const int b = owner(s_roff, B, r);
-        return p.table[static_cast<size_t>(b) * p.max_pages + (r - s_roff[b])];
+    const auto row = [&](int b) { return p.table + static_cast<size_t>(b) * p.max_pages; };
+    // where the r-th page given back, and the page of taken(a), are to be read
+    const auto given = [&](int r) {
+        const int b = owner(s_roff, B, p.top, r);
+        return row(b) + (r - s_roff[b]);
     };
-    auto taken = [&](int a) {
+    const auto taken = [&](int a) {
         const int i = n + given_n - 1 - a;
-        return i < n ? p.free_pages[i] : given(i - n);
+        return i < n ? p.free_pages + i : given(i - n);
     };
-    auto held_of = [&](int b) { return static_cast<int>((static_cast<unsigned>(s_ctx[b]) + P - 1) / P); };
-    for (int b = first; b <= B; b += step) {
-        p.cu[b] = b < B ? s_cu[b] : tokens;
-        if (b < B) {
+    const auto fine = [&](int page) { return page >= 0 && page < p.num_pages; };
+
+    if (p.parts & kTables) {
+        // a warp's 32 * RUN consecutive tokens, pages taken and pages given back, lane by lane: first all their
+        // pages are looked up, then all is written
+        const int most = max(max(p.T, taken_n), given_n);
+        for (int x0 = (first & ~31) * RUN + lane; x0 < most; x0 += step * RUN) {
+            int pos[RUN], page[RUN], at[RUN], new_page[RUN], old_page[RUN];
+            int bt = x0 < tokens ? owner(s_cu, B, p.top, x0) : 0, ba = x0 < taken_n ? owner(s_aoff, B, p.top, x0) : 0;
+#pragma unroll
+            for (int k = 0; k < RUN; ++k) {
+                const int x = x0 + 32 * k;
+                pos[k] = page[k] = at[k] = new_page[k] = old_page[k] = 0;
+                if (x < tokens) {
+                    while (bt + 1 < B && s_cu[bt + 1] <= x) ++bt;
+                    pos[k] = s_ctx[bt] + (x - s_cu[bt]);
+                    const int i = p.by_page.div(pos[k]), held = p.by_page.up(s_ctx[bt]);
+                    page[k] = *(i < held ? row(bt) + i : taken(s_aoff[bt] + i - held));
+                }
+                if (x < taken_n) {
+                    while (ba + 1 < B && s_aoff[ba + 1] <= x) ++ba;
+                    at[k] = ba;
+                    new_page[k] = *taken(x);
+                }
+                if (x < given_n) old_page[k] = *given(x);
+            }
+#pragma unroll
+            for (int k = 0; k < RUN; ++k) {
+                const int x = x0 + 32 * k;
+                if (x < p.T) {
+                    const bool ok = x < tokens && fine(page[k]);
+                    if (x < tokens && !ok) atomicExch(p.status, kDevBadPage);
+                    p.positions[x] = pos[k];
+                    p.slots[x] = ok ? static_cast<long long>(page[k]) * P + (pos[k] - p.by_page.div(pos[k]) * P) : -1;
+                }
+                if (x < taken_n) row(at[k])[p.by_page.up(s_ctx[at[k]]) + (x - s_aoff[at[k]])] = new_page[k];
+                if (x < given_n) {
+                    p.free_pages[n + x] = old_page[k];
+                    if (!fine(old_page[k])) atomicExch(p.status, kDevBadPage);
+                }
+            }
+        }
+        for (int b = first; b <= B; b += step) p.cu[b] = b < B ? s_cu[b] : tokens;
+    }
+    if (p.parts & kLengths) {
+        for (int b = first; b < B; b += step) {
             const bool done = (b + 1 < B ? s_roff[b + 1] : given_n) > s_roff[b];
             p.seqlens[b] = done ? 0 : s_ctx[b] + ((b + 1 < B ? s_cu[b + 1] : tokens) - s_cu[b]);
         }
+        if (first == 0) *p.free_count_out = n + given_n - taken_n;
     }
-    for (int r = first; r < given_n; r += step) {
-        const int page = given(r);
-        p.free_pages[n + r] = page;
-        if (page < 0 || page >= p.num_pages) atomicExch(p.status, kDevBadPage);
-    }
-    for (int a = first; a < taken_n; a += step) {
-        const int b = owner(s_aoff, B, a);
-        p.table[static_cast<size_t>(b) * p.max_pages + held_of(b) + (a - s_aoff[b])] = taken(a);
-    }
-    if (first == 0) *p.free_count_out = n + given_n - taken_n;
-    for (int t = first; t < p.T; t += step) {
-        int pos = 0;
-        long long slot = -1;
-        if (t < tokens) {
-            const int b = owner(s_cu, B, t);
-            pos = s_ctx[b] + (t - s_cu[b]);
-            const int i = pos / P, held = held_of(b);
-            const int page = i < held ? p.table[static_cast<size_t>(b) * p.max_pages + i] : taken(s_aoff[b] + i - held);
-            if (page >= 0 && page < p.num_pages)
-                slot = static_cast<long long>(page) * P + (pos - i * P);
-            else
-                atomicExch(p.status, kDevBadPage);
-        }
-        p.positions[t] = pos;
-        p.slots[t] = slot;
-    }
+}
+
+template <int RUN>
+int launch_table(PageTableParams& p, int parts, int ctas, int threads, cudaStream_t st)
+{
+    p.parts = parts;
+    FMHA_CHECK_CUDA(set_smem_limit_once(reinterpret_cast<const void*>(page_table_kernel<RUN>), kMaxRequests * 16));
+    FMHA_CHECK_CUDA(launch_pdl(page_table_kernel<RUN>, dim3(static_cast<unsigned>(ctas)), dim3(static_cast<unsigned>(threads)),
+                               static_cast<size_t>(p.B) * 16, st, p));
+    count_launch();
+    return FMHA_OK;
 }
 
 }  // namespace
@@ -229,12 +267,19 @@ extern "C" int fmha_page_table(const int32_t* ctx_lens, const int32_t* new_lens,
         return set_error(FMHA_ERR_UNSUPPORTED, "fmha_page_table: max_pages * page_size past 2^31, or T or num_pages past 2^30");
     int* status = device_status_ptr();
     if (!status) return set_error(FMHA_ERR_CUDA, "no CUDA device");
-    const PageTableParams p{ctx_lens, new_lens, B,         page_size, num_pages, free_pages, free_count,     block_table,
-                            max_pages, seqlens, cu_new,    positions, slots,     T,          free_count_out, status};
+    PageTableParams p{ctx_lens, new_lens, B, page_size, num_pages, free_pages, free_count, block_table, max_pages, seqlens, cu_new,
+                      positions, slots, T, free_count_out, status, FastDiv(static_cast<uint32_t>(page_size)), 0, 0};
+    while ((p.top ? 2 * p.top : 1) < B) p.top = p.top ? 2 * p.top : 1;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const int smem = B * 16;
-    FMHA_CHECK_CUDA(set_smem_limit_once(reinterpret_cast<const void*>(page_table_kernel), kMaxRequests * 16));
-    FMHA_CHECK_CUDA(launch_pdl(page_table_kernel, dim3(1), dim3(1024), static_cast<size_t>(smem), st, p));
-    count_launch();
-    return FMHA_OK;
+    // Up to 2048 tokens a lane takes one item, beyond that four at once.  Enough CTAs for the tokens and, as
+    // requests that end give back many pages, eight items per request; all of them sum the lengths.  An update
+    // in place has one CTA, or beyond 2048 tokens or requests a launch of its own after the others have read.
+    const bool in_place = seqlens == ctx_lens || free_count_out == free_count;
+    const int most = T > B ? T : B;
+    if (in_place && most <= 2048) return launch_table<1>(p, kTables | kLengths, 1, most <= 256 ? 256 : 1024, st);
+    const int parts = in_place ? kTables : kTables | kLengths, limit = 4 * num_sms();
+    const int items = T <= 2048 ? (T > 8 * B ? T : 8 * B) : (T > 8 * B ? T : 8 * B) / 4;
+    const int ctas = items <= 256 ? 1 : (items + 255) / 256 < limit ? (items + 255) / 256 : limit;
+    const int rc = T <= 2048 ? launch_table<1>(p, parts, ctas, 256, st) : launch_table<4>(p, parts, ctas, 256, st);
+    return rc || !in_place ? rc : launch_table<1>(p, kLengths, 1, 1024, st);
 }

@@ -154,12 +154,7 @@ int run_paged(const PagedArgs& a, bool split, const PagedWs& w, uint8_t* base, c
     p.max_pages = a.max_pages;
     p.num_pages = a.c->num_pages;
     p.page = a.c->page_size;
-    // with 2^s >= page, mul = floor(2^(31 + s) / page) + 1 is at most 1 / page * 2^s too large per 2^(31 + s), which
-    // a numerator below 2^31 cannot bring up to a whole
-    int sh = 0;
-    while ((1LL << sh) < p.page) ++sh;
-    p.page_shift = 31 + sh;
-    p.page_mul = static_cast<uint32_t>((1ULL << (31 + sh)) / p.page + 1);
+    p.by_page = FastDiv(static_cast<uint32_t>(p.page));
     p.box = box;
     p.groups = static_cast<int>(page_groups(a.c));
     p.cap = a.max_pages * a.c->page_size;

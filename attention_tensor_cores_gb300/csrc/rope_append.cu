@@ -10,6 +10,7 @@
 // Bound: HBM (every element read once and written once; a decoding step is latency-bound).
 #include <cuda_runtime.h>
 
+#include "fastdiv.cuh"
 #include "paged.h"
 #include "ptx.cuh"
 
@@ -33,6 +34,8 @@ struct AppendParams {
     int page;
     int T, Hq, Hkv, Sq;
     int* status;
+    int q_sets, kv_sets;               // sets of heads of a token, of queries and of keys (or values)
+    FastDiv by_sets, by_page, by_sq;   // all of a token's sets, page and Sq
 };
 
 // Sixteen features of a head as two runs of eight: thread l of the D / 16 threads of a head holds the
@@ -50,125 +53,197 @@ __device__ __forceinline__ Runs runs_of(int l, int R)
     return {16 * l, 16 * l + 8};
 }
 
-__device__ __forceinline__ void unpack8(const uint4& u, float* f)
+__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// Eight BF16 as four pairs of FP32, and back
+__device__ __forceinline__ void unpack8(const uint4& u, uint64_t (&f)[4])
 {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i) f[i] = f32x2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
 }
 
-__device__ __forceinline__ uint4 pack8(const float* f)
+__device__ __forceinline__ uint4 pack8(const uint64_t (&f)[4])
 {
-    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        f32x2_split(f[i], lo, hi);
+        w[i] = pack_bf16x2(lo, hi);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <int D, bool PAIRS>
-__global__ void __launch_bounds__(256) rope_append_kernel(const __grid_constant__ AppendParams p)
+__device__ __forceinline__ uint64_t swap2(uint64_t v)
+{
+    float lo, hi;
+    f32x2_split(v, lo, hi);
+    return f32x2(hi, lo);
+}
+
+// A group of D / 16 threads takes up to HEADS consecutive heads of one kind (queries, keys or values) of a
+// token: their loads are in flight together, and the token's slot, position and angles are read once for
+// them.  With the weights drawn into the angles, w the head's and c, s the angle's cosine and sine, a pair is
+//   y_i = (x_i (w_i c) + x_j (-w_j s)) / rms     y_j = (x_j (w_j c) + x_i (w_i s)) / rms
+// three packed operations for two outputs.
+template <int D, bool PAIRS, int HEADS>
+__global__ void __launch_bounds__(128, 5) rope_append_kernel(const __grid_constant__ AppendParams p)
 {
     constexpr int L = D / 16;   // threads per head
     griddep_launch_dependents();
     griddep_wait();
-    const int H = p.Hq + 2 * p.Hkv;
-    const long long item = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) / L;
+    const int item = static_cast<int>((static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) / L);   // below 2^31
     const int l = threadIdx.x % L;
-    const bool live = item < static_cast<long long>(p.T) * H;
-    const int t = live ? static_cast<int>(item / H) : 0, h = live ? static_cast<int>(item % H) : 0;
-    const long long slot = live ? p.slots[t] : -1;
-    const int pos = live && p.R ? p.positions[t] : 0;
-    bool store = slot >= 0;
-    if (store && (slot >= p.num_slots || (p.R && (pos < 0 || pos >= p.max_pos)))) {
-        store = false;
+    const uint32_t group = ((1u << L) - 1u) << (threadIdx.x & 31 & ~(L - 1));   // the lanes of this head
+    const int t = p.by_sets.div(item), set = item - t * static_cast<int>(p.by_sets.d);
+    if (t >= p.T) return;
+    const int64_t slot = p.slots[t];
+    const int pos = p.R ? p.positions[t] : 0;
+    const int kind = set < p.q_sets ? 0 : set < p.q_sets + p.kv_sets ? 1 : 2;
+    const int h0 = (kind == 0 ? set : kind == 1 ? set - p.q_sets : set - p.q_sets - p.kv_sets) * HEADS;
+    const int heads = min(HEADS, (kind == 0 ? p.Hq : p.Hkv) - h0);
+    const Runs r = kind == 2 ? Runs{16 * l, 16 * l + 8} : runs_of<PAIRS>(l, p.R);
+
+    const uint16_t* x = (kind == 0 ? p.q + t * p.q_stride : kind == 1 ? p.k + t * p.k_stride : p.v + t * p.v_stride) + h0 * D;
+    uint4 u[HEADS][2];
+#pragma unroll
+    for (int k = 0; k < HEADS; ++k)
+        if (k < heads) {
+            u[k][0] = *reinterpret_cast<const uint4*>(x + k * D + r.a);
+            u[k][1] = *reinterpret_cast<const uint4*>(x + k * D + r.b);
+        }
+
+    if (slot < 0) return;
+    if (slot >= p.num_slots || (p.R && (pos < 0 || pos >= p.max_pos))) {
         atomicExch(p.status, kDevBadPage);
+        return;
     }
-    const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
-    const Runs r = is_v ? Runs{16 * l, 16 * l + 8} : runs_of<PAIRS>(l, p.R);
-    uint4 ua = make_uint4(0, 0, 0, 0), ub = ua;
-    if (store) {
-        const uint16_t* x = is_q ? p.q + t * p.q_stride + static_cast<int64_t>(h) * D
-                            : is_v ? p.v + t * p.v_stride + static_cast<int64_t>(h - p.Hq - p.Hkv) * D
-                                   : p.k + t * p.k_stride + static_cast<int64_t>(h - p.Hq) * D;
-        ua = *reinterpret_cast<const uint4*>(x + r.a);
-        ub = *reinterpret_cast<const uint4*>(x + r.b);
-    }
-    if (!is_v) {
-        float a[8], b[8];
-        unpack8(ua, a);
-        unpack8(ub, b);
-        const uint16_t* w = is_q ? p.wq : p.wk;
-        float ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss += a[i] * a[i] + b[i] * b[i];
-#pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (w) {
-            const float inv = rsqrtf(ss / D + p.eps);
-            float wa[8], wb[8];
-            unpack8(*reinterpret_cast<const uint4*>(w + r.a), wa);
-            unpack8(*reinterpret_cast<const uint4*>(w + r.b), wb);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                a[i] = a[i] * inv * wa[i];
-                b[i] = b[i] * inv * wb[i];
-            }
-        }
-        if (store && l < p.R / 16) {
-            // the thread's eight angles: features 8l .. 8l + 7 of either half, or its eight neighbouring pairs
-            const float* cs = p.cos_sin + static_cast<int64_t>(pos) * p.R + 8 * l;
-            float c[8], s[8];
-#pragma unroll
-            for (int i = 0; i < 8; i += 4) {
-                *reinterpret_cast<float4*>(c + i) = *reinterpret_cast<const float4*>(cs + i);
-                *reinterpret_cast<float4*>(s + i) = *reinterpret_cast<const float4*>(cs + p.R / 2 + i);
-            }
-            if (PAIRS) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float x0 = a[2 * i], x1 = a[2 * i + 1], z0 = b[2 * i], z1 = b[2 * i + 1];
-                    a[2 * i] = x0 * c[i] - x1 * s[i];
-                    a[2 * i + 1] = x1 * c[i] + x0 * s[i];
-                    b[2 * i] = z0 * c[4 + i] - z1 * s[4 + i];
-                    b[2 * i + 1] = z1 * c[4 + i] + z0 * s[4 + i];
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float x0 = a[i], x1 = b[i];
-                    a[i] = x0 * c[i] - x1 * s[i];
-                    b[i] = x1 * c[i] + x0 * s[i];
-                }
-            }
-        }
-        ua = pack8(a);
-        ub = pack8(b);
-    } else {
-        // a warp may hold heads of both kinds: take part in the norm's shuffles
-        float ss = 0.f;
-#pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    }
-    if (!store) return;
     uint16_t* y;
-    if (is_q) {
-        y = p.q_out + ((static_cast<int64_t>(t / p.Sq) * p.Hq + h) * p.Sq + t % p.Sq) * D;
+    int64_t step;   // from a head to the next
+    if (kind == 0) {
+        const int n = p.by_sq.div(t);
+        step = static_cast<int64_t>(p.Sq) * D;
+        y = p.q_out + (static_cast<int64_t>(n) * p.Hq + h0) * step + (t - n * p.Sq) * D;
     } else {
-        const int head = is_v ? h - p.Hq - p.Hkv : h - p.Hq;
-        const int64_t page = slot / p.page;
-        y = (is_v ? p.vc : p.kc) + page * p.page_stride + head * p.head_stride + (slot - page * p.page) * p.token_stride;
+        const int64_t page = p.num_slots < (1LL << 31) ? p.by_page.div(static_cast<int>(slot)) : slot / p.page;
+        step = p.head_stride;
+        y = (kind == 1 ? p.kc : p.vc) + page * p.page_stride + (slot - page * p.page) * p.token_stride + h0 * step;
     }
-    *reinterpret_cast<uint4*>(y + r.a) = ua;
-    *reinterpret_cast<uint4*>(y + r.b) = ub;
+    if (kind == 2) {
+#pragma unroll
+        for (int k = 0; k < HEADS; ++k)
+            if (k < heads) {
+                *reinterpret_cast<uint4*>(y + k * step + r.a) = u[k][0];
+                *reinterpret_cast<uint4*>(y + k * step + r.b) = u[k][1];
+            }
+        return;
+    }
+
+    const uint16_t* w = kind == 0 ? p.wq : p.wk;
+    const bool turn = l < p.R / 16;
+    uint64_t pa[4], pb[4], qa[4], qb[4];   // what x_i and its partner are multiplied with, both runs
+    if (w) {
+        unpack8(*reinterpret_cast<const uint4*>(w + r.a), pa);
+        unpack8(*reinterpret_cast<const uint4*>(w + r.b), pb);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pa[i] = pb[i] = f32x2(1.f, 1.f);
+    }
+    if (turn) {
+        // the thread's eight angles: features 8l .. 8l + 7 of either half, or its eight neighbouring pairs
+        const float* cs = p.cos_sin + static_cast<int64_t>(pos) * p.R + 8 * l;
+        const float4 c0 = *reinterpret_cast<const float4*>(cs), c1 = *reinterpret_cast<const float4*>(cs + 4);
+        const float4 s0 = *reinterpret_cast<const float4*>(cs + p.R / 2), s1 = *reinterpret_cast<const float4*>(cs + p.R / 2 + 4);
+        const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+        const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (PAIRS) {   // angle i turns the i-th pair of run a, angle 4 + i that of run b
+                qa[i] = fmul2(swap2(pa[i]), f32x2(-s[i], s[i]));
+                qb[i] = fmul2(swap2(pb[i]), f32x2(-s[4 + i], s[4 + i]));
+                pa[i] = fmul2(pa[i], f32x2(c[i], c[i]));
+                pb[i] = fmul2(pb[i], f32x2(c[4 + i], c[4 + i]));
+            } else {
+                qa[i] = fmul2(pb[i], f32x2(-s[2 * i], -s[2 * i + 1]));
+                qb[i] = fmul2(pa[i], f32x2(s[2 * i], s[2 * i + 1]));
+                pa[i] = fmul2(pa[i], f32x2(c[2 * i], c[2 * i + 1]));
+                pb[i] = fmul2(pb[i], f32x2(c[2 * i], c[2 * i + 1]));
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < HEADS; ++k) {
+        if (k >= heads) break;
+        uint64_t a[4], b[4];
+        unpack8(u[k][0], a);
+        unpack8(u[k][1], b);
+        float inv = 1.f;
+        if (w) {
+            uint64_t s0 = fmul2(a[0], a[0]), s1 = fmul2(b[0], b[0]);
+#pragma unroll
+            for (int i = 1; i < 4; ++i) {
+                s0 = ffma2(a[i], a[i], s0);
+                s1 = ffma2(b[i], b[i], s1);
+            }
+            float lo, hi;
+            f32x2_split(fadd2(s0, s1), lo, hi);
+            float ss = lo + hi;
+#pragma unroll
+            for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(group, ss, o);
+            inv = rsqrtf(ss * (1.f / D) + p.eps);
+        }
+        const uint64_t inv2 = f32x2(inv, inv);
+        uint64_t ya[4], yb[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            ya[i] = fmul2(a[i], pa[i]);
+            yb[i] = fmul2(b[i], pb[i]);
+        }
+        if (turn) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                ya[i] = ffma2(PAIRS ? swap2(a[i]) : b[i], qa[i], ya[i]);
+                yb[i] = ffma2(PAIRS ? swap2(b[i]) : a[i], qb[i], yb[i]);
+            }
+        }
+        if (w) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                ya[i] = fmul2(ya[i], inv2);
+                yb[i] = fmul2(yb[i], inv2);
+            }
+        }
+        *reinterpret_cast<uint4*>(y + k * step + r.a) = pack8(ya);
+        *reinterpret_cast<uint4*>(y + k * step + r.b) = pack8(yb);
+    }
 }
 
-template <int D, bool PAIRS>
-int run_append(const AppendParams& p, cudaStream_t st)
+template <int D, bool PAIRS, int HEADS>
+int launch_append(AppendParams& p, cudaStream_t st)
 {
-    const long long threads = static_cast<long long>(p.T) * (p.Hq + 2 * p.Hkv) * (D / 16);
-    FMHA_CHECK_CUDA(launch_pdl(rope_append_kernel<D, PAIRS>, dim3(static_cast<unsigned>((threads + 255) / 256)), dim3(256), 0, st, p));
+    p.q_sets = (p.Hq + HEADS - 1) / HEADS;
+    p.kv_sets = (p.Hkv + HEADS - 1) / HEADS;
+    const int sets = p.q_sets + 2 * p.kv_sets;
+    p.by_sets = FastDiv(static_cast<uint32_t>(sets));
+    const long long threads = static_cast<long long>(p.T) * sets * (D / 16);
+    FMHA_CHECK_CUDA(launch_pdl(rope_append_kernel<D, PAIRS, HEADS>, dim3(static_cast<unsigned>((threads + 127) / 128)), dim3(128), 0, st, p));
     count_launch();
     return FMHA_OK;
+}
+
+// Four heads per group of threads once the threads of one head each would fill the GPU several times; below
+// that one head each, which is the shorter chain.
+template <int D, bool PAIRS>
+int run_append(AppendParams& p, cudaStream_t st)
+{
+    const long long threads = static_cast<long long>(p.T) * (p.Hq + 2 * p.Hkv) * (D / 16);
+    return threads > 4LL * 2048 * num_sms() ? launch_append<D, PAIRS, 4>(p, st) : launch_append<D, PAIRS, 1>(p, st);
 }
 
 }  // namespace
@@ -197,7 +272,7 @@ extern "C" int fmha_rope_append(const void* q, int64_t q_stride, const void* k, 
                          "fmha_rope_append: tensors 16-byte, positions 4-byte, slots 8-byte aligned");
     if (q_stride % 8 != 0 || k_stride % 8 != 0 || v_stride % 8 != 0 || q_stride < 0 || k_stride < 0 || v_stride < 0)
         return set_error(FMHA_ERR_INVALID, "fmha_rope_append: token strides must be non-negative multiples of 8 elements");
-    if (static_cast<long long>(T) * (Hq + 2LL * cache->Hkv) >= (1LL << 31))
+    if (static_cast<long long>(T) * (Hq + 2LL * cache->Hkv) >= (1LL << 31) - 256)
         return set_error(FMHA_ERR_UNSUPPORTED, "fmha_rope_append: more than 2^31 heads");
     int* status = device_status_ptr();
     if (!status) return set_error(FMHA_ERR_CUDA, "no CUDA device");
@@ -230,6 +305,8 @@ extern "C" int fmha_rope_append(const void* q, int64_t q_stride, const void* k, 
     p.Hkv = cache->Hkv;
     p.Sq = Sq;
     p.status = status;
+    p.by_page = FastDiv(static_cast<uint32_t>(cache->page_size));
+    p.by_sq = FastDiv(static_cast<uint32_t>(Sq));
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (cache->D == 64) return interleaved ? run_append<64, true>(p, st) : run_append<64, false>(p, st);
     return interleaved ? run_append<128, true>(p, st) : run_append<128, false>(p, st);
