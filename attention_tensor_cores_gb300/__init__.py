@@ -297,17 +297,28 @@ def _need(cond, what: str):
         raise FmhaError(FMHA_ERR_INVALID, what)
 
 
-def _need_current(t):
-    import torch
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise FmhaError(FMHA_ERR_INVALID, "tensors must be on the current CUDA device")
+_ext = None
 
 
-def _need_like(dev, **ts):
-    """Each name=(tensor, dtype): a contiguous tensor of that type on device `dev`."""
-    for name, (t, dt) in ts.items():
-        if t.dtype != dt or t.device != dev or not t.is_contiguous():
-            raise FmhaError(FMHA_ERR_INVALID, f"{name} must be a contiguous {dt} tensor on {dev}")
+def _native():
+    """The native binding of the functions below (built with libfmha.so); raises if absent."""
+    global _ext
+    if _ext is None:
+        lib = load()
+        import torch  # noqa: F401  (its libraries first)
+        try:
+            from . import _binding as ext
+        except ImportError as e:
+            raise FmhaError(FMHA_ERR_CUDA, f"_binding.so not built for this torch: run attention_tensor_cores_gb300/build.py ({e})")
+        ext.bind(FmhaError, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib.fmha_page_table, lib.fmha_rope_append, lib.fmha_fwd_paged, lib.fmha_last_error, lib.fmha_error_string)))
+        _ext = ext
+    return _ext
+
+
+def _need(cond, what: str):
+    if not cond:
+        raise FmhaError(FMHA_ERR_INVALID, what)
 
 
 def make_kv_cache(k, v) -> fmha_kv_cache:
@@ -336,51 +347,15 @@ def fmha_page_table(ctx_lens, new_lens, page_size: int, free_pages, free_count, 
     """Gives pages of the stack free_pages [num_pages] to requests whose tokens outgrow theirs, takes back
     those of requests with new_lens < 0, and writes block_table [B, max_pages], seqlens [B], cu_new [B + 1],
     positions [T], slots [T] and free_count_out [1]; slots is int64, all others int32."""
-    import torch
-    i32, dev = torch.int32, free_pages.device
-    _need_current(free_pages)
-    _need_like(dev, ctx_lens=(ctx_lens, i32), new_lens=(new_lens, i32), free_pages=(free_pages, i32), free_count=(free_count, i32),
-               block_table=(block_table, i32), seqlens=(seqlens, i32), cu_new=(cu_new, i32), positions=(positions, i32),
-               slots=(slots, torch.int64), free_count_out=(free_count_out, i32))
-    B, T = ctx_lens.numel(), slots.numel()
-    _need(new_lens.numel() == B and seqlens.numel() == B and cu_new.numel() == B + 1 and positions.numel() == T
-          and block_table.dim() == 2 and block_table.shape[0] == B and free_count.numel() == 1 and free_count_out.numel() == 1,
-          "need new_lens [B], seqlens [B], cu_new [B + 1], block_table [B, max_pages], positions [T], free counts [1]")
-    rc = load().fmha_page_table(_ptr(ctx_lens), _ptr(new_lens), B, page_size, _ptr(free_pages), _ptr(free_count), free_pages.numel(),
-                                _ptr(block_table), block_table.shape[1], _ptr(seqlens), _ptr(cu_new), _ptr(positions), _ptr(slots),
-                                T, _ptr(free_count_out), _stream(stream))
-    _check(rc, "fmha_page_table")
+    (_ext or _native()).page_table(ctx_lens, new_lens, page_size, free_pages, free_count, block_table, seqlens, cu_new, positions,
+                                    slots, free_count_out, stream)
 
 
 def fmha_rope_append(q, k, v, q_weight, k_weight, eps: float, cos_sin, positions, slots, q_out, cache: fmha_kv_cache,
                      interleaved: bool = False, stream=None):
     """Norm (weights [D] or None), rotation (cos_sin FP32 [max_pos, rope_dim] or None) and store: q [T, Hq, D],
     k and v [T, Hkv, D] may be slices of one projection; q_out [T / Sq, Hq, Sq, D] or [T, Hq, D]."""
-    import torch
-    bf16, dev = torch.bfloat16, slots.device
-    T, Hq, D = q.shape
-    _need_current(slots)
-    for t, H in ((q, Hq), (k, cache.Hkv), (v, cache.Hkv)):
-        _need(t.dtype == bf16 and t.device == dev and tuple(t.shape) == (T, H, cache.D),
-              "q must be BF16 [T, Hq, D], k and v [T, Hkv, D], on the device of slots")
-        _need(t.numel() == 0 or (t.stride(2) == 1 and (H == 1 or t.stride(1) == D)), "q, k and v must have contiguous heads")
-    _need_like(dev, q_out=(q_out, bf16), slots=(slots, torch.int64))
-    for w in (q_weight, k_weight):
-        if w is not None:
-            _need_like(dev, weight=(w, bf16))
-            _need(w.numel() == D, "weights must have D values")
-    rope_dim = max_pos = 0
-    if cos_sin is not None:
-        _need_like(dev, cos_sin=(cos_sin, torch.float32), positions=(positions, torch.int32))
-        _need(cos_sin.dim() == 2 and positions.numel() == T, "need cos_sin [max_pos, rope_dim] and positions [T]")
-        max_pos, rope_dim = cos_sin.shape
-    Sq = q_out.shape[2] if q_out.dim() == 4 else 1
-    _need(slots.numel() == T and q_out.numel() == T * Hq * D and q_out.dim() in (3, 4) and q_out.shape[1] == Hq,
-          "need slots [T] and q_out [T / Sq, Hq, Sq, D] or [T, Hq, D]")
-    rc = load().fmha_rope_append(_ptr(q), q.stride(0), _ptr(k), k.stride(0), _ptr(v), v.stride(0), _ptr(q_weight), _ptr(k_weight),
-                                 eps, _ptr(cos_sin), max_pos, rope_dim, int(interleaved), _ptr(positions), _ptr(slots), _ptr(q_out),
-                                 cache, T, Hq, Sq, _stream(stream))
-    _check(rc, "fmha_rope_append")
+    (_ext or _native()).rope_append(q, k, v, q_weight, k_weight, eps, cos_sin, positions, slots, q_out, cache, interleaved, stream)
 
 
 def fmha_paged_workspace_size(B, Hq, Sq, cache: fmha_kv_cache, opts: fmha_opts | None = None) -> int:
@@ -390,20 +365,4 @@ def fmha_paged_workspace_size(B, Hq, Sq, cache: fmha_kv_cache, opts: fmha_opts |
 def fmha_fwd_paged(q, cache: fmha_kv_cache, block_table, seqlens, out, lse, scale: float, opts: fmha_opts | None = None, stream=None):
     """Attention of q [B, Hq, Sq, D] over the first seqlens[b] tokens of each request's pages, block_table
     int32 [B, max_pages]; out per opts.out_kind, lse FP32 [B, Hq, Sq] or None (see make_opts, make_kv_cache)."""
-    import torch
-    dev = q.device
-    _need_current(q)
-    kind = FMHA_OUT_BF16 if opts is None else opts.out_kind
-    dtype, size = {FMHA_OUT_F32: (torch.float32, 1), FMHA_OUT_NVFP4: (torch.uint8, 2)}.get(kind, (torch.bfloat16, 1))
-    _need_like(dev, out=(out, dtype))
-    _need(out.numel() * size == q.numel(), "out must have q's size (NVFP4: a byte for two values)")
-    if lse is not None:
-        _need_like(dev, lse=(lse, torch.float32))
-        _need(lse.numel() * cache.D == q.numel(), "lse must be [B, Hq, Sq]")
-    _need_like(dev, q=(q, torch.bfloat16), block_table=(block_table, torch.int32), seqlens=(seqlens, torch.int32))
-    B, Hq, Sq, D = q.shape
-    _need(D == cache.D and block_table.dim() == 2 and block_table.shape[0] == B and seqlens.numel() == B,
-          "need q [B, Hq, Sq, D] with the cache's D, block_table [B, max_pages] and seqlens [B]")
-    rc = load().fmha_fwd_paged(_ptr(q), cache, _ptr(block_table), block_table.shape[1], _ptr(seqlens), _ptr(out), _ptr(lse), B, Hq, Sq,
-                               scale, _stream(stream), opts)
-    _check(rc, "fmha_fwd_paged")
+    (_ext or _native()).fwd_paged(q, cache, block_table, seqlens, out, lse, scale, opts, stream)
