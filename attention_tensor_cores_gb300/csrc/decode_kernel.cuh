@@ -125,6 +125,7 @@ struct DecodeParams {
     int cap;                 // max_pages * page: lengths are clamped to it
     int chunks;              // units per key/value head: its Gtot query rows in chunks of G
     int Gtot;
+    int ctas;                // of the grid
 };
 
 // Keys of batch entry b
@@ -191,7 +192,7 @@ struct Sched {
     }
     __device__ int unit_keys(int u) const { return p->seqlens ? batch_keys<PAGED>(*p, u / p->Hkv) : p->Skv; }
 
-    __device__ void init(const DecodeParams* pp, int c, int n, const int* prefix, const int* lengths, int first)
+    __device__ void init(const DecodeParams* pp, int c, int n, const int* prefix, const int* lengths, int first, const long long* range)
     {
         p = pp;
         pre = prefix;
@@ -199,13 +200,14 @@ struct Sched {
         cta = c;
         nctas = n;
         if (p->split) {
-            const long long T = PAGED       ? static_cast<long long>(pre[p->U / p->Hkv]) * p->Hkv
-                                : p->prefix ? p->prefix[p->U]
-                                            : static_cast<long long>(p->U) * p->tiles_uniform;
             if constexpr (PAGED) {
                 b = first;
                 i = -1;
+                g = range[0];
+                g1 = range[1];
+                return;
             }
+            const long long T = p->prefix ? p->prefix[p->U] : static_cast<long long>(p->U) * p->tiles_uniform;
             g = (static_cast<long long>(c) * T) / n;
             g1 = (static_cast<long long>(c + 1) * T) / n;
         } else {
@@ -427,6 +429,33 @@ __device__ __forceinline__ void unit_range(const DecodeParams& p, const int* pre
     }
 }
 
+// Paged work split.  The line of T tiles is cut for P CTAs at c T / P, P as many as leave each kMinPiece tiles or
+// as there are units with keys; a cut less than kMinPiece tiles from an end of its unit moves there.  A piece of
+// a unit costs its publication and a share of the merge, several tiles' time, so short units stay whole.
+constexpr int kMinPiece = 4;
+
+__device__ __forceinline__ int paged_ctas(long long T, long long units, int n)
+{
+    return static_cast<int>(max(1ll, min(static_cast<long long>(n), max(T / kMinPiece, units))));
+}
+
+// the cut at x as the unit of tiles [s, e) sees it (s or e when it is not inside)
+__device__ __forceinline__ long long unit_cut(long long x, long long s, long long e)
+{
+    if (x <= s) return s;
+    if (x >= e) return e;
+    return x - s <= e - x ? (x - s < kMinPiece ? s : x) : (e - x < kMinPiece ? e : x);
+}
+
+// Whether CTA c of P has a piece of the unit of tiles [s, s + tiles) of T
+template <bool PAGED>
+__device__ __forceinline__ bool has_piece(int c, int P, long long T, long long s, int tiles)
+{
+    const long long x = (static_cast<long long>(c) * T) / P, y = (static_cast<long long>(c + 1) * T) / P;
+    if constexpr (PAGED) return unit_cut(x, s, s + tiles) < unit_cut(y, s, s + tiles);
+    return x != y;
+}
+
 template <bool PAGED>
 __device__ int unit_partial_slots(const DecodeParams& p, const int* pre, int u, int P, int* slots, int cap)
 {
@@ -434,11 +463,12 @@ __device__ int unit_partial_slots(const DecodeParams& p, const int* pre, int u, 
     long long Tu, T;
     unit_range<PAGED>(p, pre, u, tiles, Tu, T);
     if (tiles <= 0) return 0;
-    const int c0 = static_cast<int>(min((((Tu + 1) * P) - 1) / T, static_cast<long long>(P - 1)));
-    const int c1 = static_cast<int>(min((((Tu + tiles) * P) - 1) / T, static_cast<long long>(P - 1)));
+    int c0 = static_cast<int>(min((((Tu + 1) * P) - 1) / T, static_cast<long long>(P - 1)));
+    int c1 = static_cast<int>(min((((Tu + tiles) * P) - 1) / T, static_cast<long long>(P - 1)));
+    if constexpr (PAGED) c0 = max(c0 - 1, 0), c1 = min(c1 + 1, P - 1);   // a moved cut
     int n = 0;
     for (int c = c0; c <= c1 && n < cap; ++c)
-        if ((static_cast<long long>(c) * T) / P != (static_cast<long long>(c + 1) * T) / P) slots[n++] = u + c;
+        if (has_piece<PAGED>(c, P, T, Tu, tiles)) slots[n++] = u + c;
     return n;
 }
 
@@ -535,7 +565,8 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
     if (blockIdx.x == 0 && threadIdx.x == 0 && p.nv_ts) *p.nv_ts = *p.nv_sg;   // single-pass NVFP4: report s_g
 
     const int *pre = p.prefix, *keys = nullptr;
-    int first_b = 0;
+    int first_b = 0, P = static_cast<int>(gridDim.x);   // P: CTAs that the tiles are split over
+    __shared__ long long range_sh[2];   // paged split mode: the CTA's tiles
     if constexpr (PAGED) {
         const int B = p.U / p.Hkv;
         if (blockIdx.x == 0)
@@ -570,12 +601,40 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
             keys = keys_sh;
         }
         if (p.split) {
-            // the batch entry that the CTA's first tile is in: its owner among the threads says so
-            const long long first = static_cast<long long>(blockIdx.x) * (static_cast<long long>(pre[B]) * p.Hkv) / gridDim.x;
-            for (int b = threadIdx.x; b < B; b += blockDim.x)
-                if (static_cast<long long>(pre[b]) * p.Hkv <= first && first < static_cast<long long>(pre[b + 1]) * p.Hkv) pre_warp[0] = b;
+            // the CTA's range of tiles and the batch entry it starts in: the threads that own the entries with
+            // its two cuts say so
+            const long long T = static_cast<long long>(pre[B]) * p.Hkv;
+            const int c = static_cast<int>(blockIdx.x);
+            if (p.prefix) {
+                P = p.prefix[B + 1];
+            } else {
+                int with_keys = 0;
+                for (int b = threadIdx.x; b < B; b += blockDim.x) with_keys += pre[b + 1] > pre[b] ? 1 : 0;
+                with_keys = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(with_keys)));
+                if ((threadIdx.x & 31) == 0) pre_warp[warp] = with_keys;
+                __syncthreads();
+                with_keys = 0;
+                for (int w = 0; w < static_cast<int>(blockDim.x) / 32; ++w) with_keys += pre_warp[w];
+                P = paged_ctas(T, static_cast<long long>(with_keys) * p.Hkv, P);
+            }
+            if (threadIdx.x < 2) range_sh[threadIdx.x] = c < P ? T : 0;   // the cut behind the last tile has no owner
             __syncthreads();
-            first_b = pre[B] > 0 ? pre_warp[0] : 0;
+            if (c < P) {
+                const long long cut[2] = {static_cast<long long>(c) * T / P, static_cast<long long>(c + 1) * T / P};
+                for (int b = threadIdx.x; b < B; b += blockDim.x) {
+                    const int nt = pre[b + 1] - pre[b];
+                    const long long s0 = static_cast<long long>(pre[b]) * p.Hkv, end = s0 + static_cast<long long>(nt) * p.Hkv;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        if (s0 <= cut[k] && cut[k] < end) {
+                            const long long s = s0 + static_cast<long long>(static_cast<int>(cut[k] - s0) / nt) * nt;
+                            range_sh[k] = unit_cut(cut[k], s, s + nt);
+                            if (k == 0) pre_warp[0] = b;
+                        }
+                }
+            }
+            __syncthreads();
+            first_b = T > 0 && c < P ? pre_warp[0] : 0;
         }
         if (p.fixup)   // no combine kernel runs: entries without keys are written here
             for (int b = blockIdx.x; b < B; b += gridDim.x)
@@ -583,7 +642,7 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
     }
 
     Sched<PAGED> sched;
-    sched.init(&p, blockIdx.x, gridDim.x, pre, keys, first_b);
+    sched.init(&p, blockIdx.x, gridDim.x, pre, keys, first_b, range_sh);
     Item it;
 
     // The epilogue of one item, run by 128 threads: the epilogue warpgroup (named barrier 2) when a
@@ -702,7 +761,7 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
             // fence waits for the stores instead of 128.
             named_bar_sync(bar, 128);
             if (tid == 0) {
-                const int n = slots_ready ? fx_n : unit_partial_slots<PAGED>(p, pre, it.u, static_cast<int>(gridDim.x), fx_slot, kMaxFixSlots);
+                const int n = slots_ready ? fx_n : unit_partial_slots<PAGED>(p, pre, it.u, P, fx_slot, kMaxFixSlots);
                 fx_n = n;
                 __threadfence();
                 const int arrived = n > 0 ? arrive_unit(p.unit_ctr + it.u, p.gen, n) : 0;
@@ -1228,7 +1287,7 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
             // a partial's slots (64-bit divisions) while the softmax warps still stream the item, off
             // the path from its last tile to its arrival count
             const bool partial = p.fixup && !(it.whole && !(p.split && p.nv_codes)) && it.t1 > it.t0;
-            if (partial && tid == 0) fx_n = unit_partial_slots<PAGED>(p, pre, it.u, static_cast<int>(gridDim.x), fx_slot, kMaxFixSlots);
+            if (partial && tid == 0) fx_n = unit_partial_slots<PAGED>(p, pre, it.u, P, fx_slot, kMaxFixSlots);
             mbar_wait(&ep_full[hr.idx], hr.phase, wc);
             tc_fence_after();
             __syncwarp();   // tcgen05.ld is warp-collective
@@ -1272,6 +1331,9 @@ __global__ void __launch_bounds__(1024) tile_prefix_kernel(const __grid_constant
     const int per = (U + 1023) / 1024;
     const int b0 = threadIdx.x * per;
     int s = 0;
+    int with_keys = 0;
+    if constexpr (PAGED)
+        for (int u = b0; u < min(U, b0 + per); ++u) with_keys += batch_keys<PAGED>(p, u) > 0 ? 1 : 0;
     for (int u = b0; u < min(U, b0 + per); ++u) s += (batch_keys<PAGED>(p, u / per_entry) + kTileKV - 1) / kTileKV;
     part[threadIdx.x] = s;
     __syncthreads();
@@ -1287,6 +1349,17 @@ __global__ void __launch_bounds__(1024) tile_prefix_kernel(const __grid_constant
         run += (batch_keys<PAGED>(p, u / per_entry) + kTileKV - 1) / kTileKV;
     }
     if (threadIdx.x == 1023) prefix[U] = part[1023];
+    if constexpr (PAGED) {   // and the CTAs that the tiles are split over
+        const long long total = part[1023];
+        __syncthreads();
+        part[threadIdx.x] = with_keys;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            long long n = 0;
+            for (int i = 0; i < 1024; ++i) n += part[i];
+            prefix[U + 1] = paged_ctas(total * p.Hkv, n * p.Hkv, p.ctas);
+        }
+    }
 }
 
 // Merges the partial results of units whose tiles were split over several CTAs, and writes the
@@ -1320,25 +1393,23 @@ __global__ void combine_kernel(const __grid_constant__ DecodeParams p, int nctas
         unit_range<PAGED>(p, p.prefix, u, tiles, Tu, T);
         int cnt = 0;
         if (tiles > 0) {
-            const long long P = nctas;
-            const int c0 = static_cast<int>(min((((Tu + 1) * P) - 1) / T, P - 1));
-            const int c1 = static_cast<int>(min((((Tu + tiles) * P) - 1) / T, P - 1));
-            if (c0 == c1 && !p.nv_codes) {
-                cnt = -1;   // one CTA held the whole unit and wrote it
-            } else {
-                for (int cw = c0; cw <= c1; cw += 32) {
-                    const int c = cw + static_cast<int>(threadIdx.x);
-                    // CTAs with an empty tile range (possible when T < P) hold no partial
-                    const bool ok = c <= c1 && (c * T) / P != ((c + 1) * T) / P;
-                    const unsigned m = __ballot_sync(0xffffffffu, ok);
-                    if (ok) {
-                        const int idx = cnt + __popc(m & ((1u << threadIdx.x) - 1u));
-                        if (idx < kMaxPartsD) slots[idx] = u + c;
-                    }
-                    cnt += __popc(m);
+            const long long P = PAGED ? p.prefix[p.U / p.Hkv + 1] : nctas;
+            int c0 = static_cast<int>(min((((Tu + 1) * P) - 1) / T, P - 1));
+            int c1 = static_cast<int>(min((((Tu + tiles) * P) - 1) / T, P - 1));
+            if constexpr (PAGED) c0 = max(c0 - 1, 0), c1 = min(c1 + 1, static_cast<int>(P) - 1);   // a moved cut
+            for (int cw = c0; cw <= c1; cw += 32) {
+                const int c = cw + static_cast<int>(threadIdx.x);
+                // CTAs with an empty tile range (possible when T < P) hold no partial
+                const bool ok = c <= c1 && has_piece<PAGED>(c, static_cast<int>(P), T, Tu, tiles);
+                const unsigned m = __ballot_sync(0xffffffffu, ok);
+                if (ok) {
+                    const int idx = cnt + __popc(m & ((1u << threadIdx.x) - 1u));
+                    if (idx < kMaxPartsD) slots[idx] = u + c;
                 }
-                cnt = min(cnt, kMaxPartsD);
+                cnt += __popc(m);
             }
+            cnt = min(cnt, kMaxPartsD);
+            if (cnt == 1 && !p.nv_codes) cnt = -1;   // one CTA held the whole unit and wrote it
         }
         __syncwarp();
         // LSE of the merged row and each partial's weight exp(lse_i - lse), once per block

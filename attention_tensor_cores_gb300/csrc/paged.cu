@@ -68,7 +68,7 @@ PagedWs paged_ws(int B, int Hq, int Sq, const fmha_kv_cache* c, const fmha_opts*
     PagedWs w{};
     size_t off = 0;
     w.prefix_off = off;
-    off += split && needs_prefix(B, o->nvfp4_scale_in != nullptr) ? al((static_cast<size_t>(B) + 1) * 4) : 0;
+    off += split && needs_prefix(B, o->nvfp4_scale_in != nullptr) ? al((static_cast<size_t>(B) + 2) * 4) : 0;
     w.ctr_off = off;
     off += split ? al(static_cast<size_t>(s.U) * 8) : 0;
     w.lse_off = off;
@@ -178,6 +178,10 @@ int run_paged(const PagedArgs& a, bool split, const PagedWs& w, uint8_t* base, c
     p.status = device_status_ptr();
     p.limit = wait_limit();
 
+    // one CTA per SM, or fewer when even full tables have fewer key tiles (whole units: fewer units)
+    const long long tiles = split ? static_cast<long long>(s.U) * ((p.cap + kTileKV - 1) / kTileKV) : s.U;
+    const unsigned grid = static_cast<unsigned>(tiles < nsm ? tiles : nsm);
+    p.ctas = static_cast<int>(grid);
     if (p.prefix) {
         FMHA_CHECK_CUDA(launch_pdl(tile_prefix_kernel<true>, dim3(1), dim3(1024), 0, st, p, const_cast<int32_t*>(p.prefix)));
         count_launch();
@@ -185,9 +189,6 @@ int run_paged(const PagedArgs& a, bool split, const PagedWs& w, uint8_t* base, c
     const bool epi = s.G > 1;   // as in the dense decode: the epilogue warpgroup pays with several columns
     const auto kernel = kernel_for<D, CAUSAL>(s.G);
     FMHA_CHECK_CUDA(set_smem_limit_once(reinterpret_cast<const void*>(kernel), C::kSmemBytes));
-    // one CTA per SM, or fewer when even full tables have fewer key tiles (whole units: fewer units)
-    const long long tiles = split ? static_cast<long long>(s.U) * ((p.cap + kTileKV - 1) / kTileKV) : s.U;
-    const unsigned grid = static_cast<unsigned>(tiles < nsm ? tiles : nsm);
     timing_mark_begin(st);
     const cudaError_t e = launch_pdl(kernel, dim3(grid), dim3(epi ? decode_threads<true>() : decode_threads<false>()), C::kSmemBytes,
                                      st, qmap, kmap, vmap, p);
