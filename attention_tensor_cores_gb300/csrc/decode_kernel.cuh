@@ -33,6 +33,8 @@
 #pragma once
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "fastdiv.cuh"
 #include "internal.h"
 #include "nvfp4_dev.cuh"
@@ -145,6 +147,39 @@ struct Item {
     int b, head, chunk;   // paged: batch entry, key/value head and chunk of its rows
 };
 
+// Paged work split.  The line of T tiles (below 2^31) is cut for P CTAs at c T / P, P as many as leave each
+// kMinPiece tiles or as there are units with keys; a cut less than kMinPiece tiles from an end of its unit moves
+// there.  A piece of a unit costs its publication and a share of the merge, several tiles' time, so short units
+// stay whole.
+constexpr int kMinPiece = 4;
+
+struct Line {
+    int T = 0, P = 1, q = 0, r = 0;   // T = q P + r
+
+    __device__ void init(int tiles, int ctas)
+    {
+        T = tiles;
+        P = ctas;
+        q = T / P;
+        r = T - q * P;
+    }
+    // floor(c T / P); P <= 2^15
+    __device__ int cut(int c) const { return c * q + c * r / P; }
+};
+
+__device__ __forceinline__ int paged_ctas(int T, long long units, int n)
+{
+    return static_cast<int>(max(1ll, min(static_cast<long long>(n), max(static_cast<long long>(T / kMinPiece), units))));
+}
+
+// the cut at x as the unit of tiles [s, e) sees it (s or e when it is not inside)
+__device__ __forceinline__ int unit_cut(int x, int s, int e)
+{
+    if (x <= s) return s;
+    if (x >= e) return e;
+    return x - s <= e - x ? (x - s < kMinPiece ? s : x) : (e - x < kMinPiece ? e : x);
+}
+
 template <bool PAGED>
 struct Sched;
 
@@ -175,7 +210,8 @@ struct Sched {
     const DecodeParams* p;
     const int* pre;     // paged split mode: exclusive prefix of the batch entries' tiles
     const int* keys;    // and their keys, if in shared memory
-    long long g, g1;    // split mode: current / end global tile
+    using Pos = std::conditional_t<PAGED, int, long long>;
+    Pos g, g1;          // split mode: current / end global tile
     int u;              // whole-unit mode: next unit
     int cta, nctas;
     int b, i;           // paged split mode: batch entry and unit of it that tile g is in (first: i < 0)
@@ -192,7 +228,7 @@ struct Sched {
     }
     __device__ int unit_keys(int u) const { return p->seqlens ? batch_keys<PAGED>(*p, u / p->Hkv) : p->Skv; }
 
-    __device__ void init(const DecodeParams* pp, int c, int n, const int* prefix, const int* lengths, int first, const long long* range)
+    __device__ void init(const DecodeParams* pp, int c, int n, const int* prefix, const int* lengths, int first, const int* range)
     {
         p = pp;
         pre = prefix;
@@ -221,20 +257,20 @@ struct Sched {
             if (g >= g1) return false;
             if constexpr (PAGED) {
                 // on to the batch entry that holds tile g (b >= the one before, entries may have no tiles)
-                while (static_cast<long long>(pre[b + 1]) * p->Hkv <= g) {
+                while (pre[b + 1] * p->Hkv <= g) {
                     ++b;
                     i = 0;
                 }
                 const int nt = pre[b + 1] - pre[b];
                 if (i < 0) {   // first item: the only one that may start inside a unit
-                    const int r = static_cast<int>(g - static_cast<long long>(pre[b]) * p->Hkv);   // < Hkv * nt < 2^31
+                    const int r = g - pre[b] * p->Hkv;
                     i = r / nt;
                     it.t0 = r - i * nt;
                 } else {
                     it.t0 = 0;
                 }
                 it.u = b * p->Hkv + i;
-                it.t1 = static_cast<int>(min(static_cast<long long>(nt), g1 - g + it.t0));
+                it.t1 = min(nt, g1 - g + it.t0);
                 it.n = keys ? keys[b] : batch_keys<true>(*p, b);
                 it.whole = (it.t0 == 0 && it.t1 == nt);
                 it.slot = it.u + cta;
@@ -259,7 +295,7 @@ struct Sched {
             const int nt = unit_tiles(uu);
             it.u = uu;
             it.t0 = static_cast<int>(g - s);
-            it.t1 = static_cast<int>(min(static_cast<long long>(nt), g1 - s));
+            it.t1 = static_cast<int>(min(static_cast<long long>(nt), static_cast<long long>(g1) - s));
             it.n = unit_keys(uu);
             it.whole = (it.t0 == 0 && it.t1 == nt);
             it.slot = uu + cta;
@@ -410,15 +446,11 @@ __device__ __forceinline__ float warp_sum(float v)
 // Stream-K: the CTAs holding partials of unit u are c0..c1 of P, skipping CTAs whose tile range is
 // empty (possible when there are fewer tiles than CTAs).  Fills slots[] (partial slots u + c, at
 // most cap) and returns how many there are; 0 for a unit without tiles.
-template <bool PAGED>
-__device__ __forceinline__ void unit_range(const DecodeParams& p, const int* pre, int u, int& tiles, long long& Tu, long long& T)
+__device__ int unit_partial_slots(const DecodeParams& p, int u, int P, int* slots, int cap)
 {
-    if constexpr (PAGED) {
-        const int b = u / p.Hkv;
-        tiles = pre[b + 1] - pre[b];
-        Tu = static_cast<long long>(pre[b]) * p.Hkv + static_cast<long long>(u - b * p.Hkv) * tiles;
-        T = static_cast<long long>(pre[p.U / p.Hkv]) * p.Hkv;
-    } else if (p.prefix) {
+    int tiles;
+    long long Tu, T;
+    if (p.prefix) {
         tiles = p.prefix[u + 1] - p.prefix[u];
         Tu = p.prefix[u];
         T = p.prefix[p.U];
@@ -427,48 +459,32 @@ __device__ __forceinline__ void unit_range(const DecodeParams& p, const int* pre
         Tu = static_cast<long long>(u) * tiles;
         T = static_cast<long long>(p.U) * tiles;
     }
-}
-
-// Paged work split.  The line of T tiles is cut for P CTAs at c T / P, P as many as leave each kMinPiece tiles or
-// as there are units with keys; a cut less than kMinPiece tiles from an end of its unit moves there.  A piece of
-// a unit costs its publication and a share of the merge, several tiles' time, so short units stay whole.
-constexpr int kMinPiece = 4;
-
-__device__ __forceinline__ int paged_ctas(long long T, long long units, int n)
-{
-    return static_cast<int>(max(1ll, min(static_cast<long long>(n), max(T / kMinPiece, units))));
-}
-
-// the cut at x as the unit of tiles [s, e) sees it (s or e when it is not inside)
-__device__ __forceinline__ long long unit_cut(long long x, long long s, long long e)
-{
-    if (x <= s) return s;
-    if (x >= e) return e;
-    return x - s <= e - x ? (x - s < kMinPiece ? s : x) : (e - x < kMinPiece ? e : x);
-}
-
-// Whether CTA c of P has a piece of the unit of tiles [s, s + tiles) of T
-template <bool PAGED>
-__device__ __forceinline__ bool has_piece(int c, int P, long long T, long long s, int tiles)
-{
-    const long long x = (static_cast<long long>(c) * T) / P, y = (static_cast<long long>(c + 1) * T) / P;
-    if constexpr (PAGED) return unit_cut(x, s, s + tiles) < unit_cut(y, s, s + tiles);
-    return x != y;
-}
-
-template <bool PAGED>
-__device__ int unit_partial_slots(const DecodeParams& p, const int* pre, int u, int P, int* slots, int cap)
-{
-    int tiles;
-    long long Tu, T;
-    unit_range<PAGED>(p, pre, u, tiles, Tu, T);
     if (tiles <= 0) return 0;
-    int c0 = static_cast<int>(min((((Tu + 1) * P) - 1) / T, static_cast<long long>(P - 1)));
-    int c1 = static_cast<int>(min((((Tu + tiles) * P) - 1) / T, static_cast<long long>(P - 1)));
-    if constexpr (PAGED) c0 = max(c0 - 1, 0), c1 = min(c1 + 1, P - 1);   // a moved cut
+    const int c0 = static_cast<int>(min((((Tu + 1) * P) - 1) / T, static_cast<long long>(P - 1)));
+    const int c1 = static_cast<int>(min((((Tu + tiles) * P) - 1) / T, static_cast<long long>(P - 1)));
     int n = 0;
     for (int c = c0; c <= c1 && n < cap; ++c)
-        if (has_piece<PAGED>(c, P, T, Tu, tiles)) slots[n++] = u + c;
+        if ((static_cast<long long>(c) * T) / P != (static_cast<long long>(c + 1) * T) / P) slots[n++] = u + c;
+    return n;
+}
+
+// Same for the paged split: the CTAs with a piece of unit i of batch entry b.
+__device__ int paged_partial_slots(const DecodeParams& p, const int* pre, const Line& line, int b, int i, int* slots, int cap)
+{
+    const int tiles = pre[b + 1] - pre[b];
+    if (tiles <= 0) return 0;
+    const int s = pre[b] * p.Hkv + i * tiles, e = s + tiles;
+    // the CTA whose cut is the last at or before s, and one before it, as a cut behind s may have moved back
+    int c = min(static_cast<int>(static_cast<float>(s) * (static_cast<float>(line.P) / static_cast<float>(line.T))), line.P - 1);
+    while (c > 0 && line.cut(c) > s) --c;
+    while (c + 1 < line.P && line.cut(c + 1) <= s) ++c;
+    c = max(c - 1, 0);
+    int n = 0, lo = unit_cut(line.cut(c), s, e);
+    for (; c < line.P && lo < e && n < cap; ++c) {
+        const int hi = unit_cut(line.cut(c + 1), s, e);
+        if (lo < hi) slots[n++] = b * p.Hkv + i + c;
+        lo = hi;
+    }
     return n;
 }
 
@@ -512,7 +528,10 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
 
     __shared__ uint64_t q_full[2], q_empty[2], k_full[S], k_empty[S], v_full[S], v_empty[S];
-    __shared__ uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2], o_full[2], o_empty[2], mma_done;
+    // S, P and O of a tile alternate between two buffers without barriers for "empty": the MMA warp issues
+    // QK(k), PV(k - 1), QK(k + 1), .. and PV(k) waits for P(k), by when the softmax has read S(k) and O(k - 2);
+    // it stores P(k) after it has read O(k - 2), by when PV(k - 2) has read P(k - 2).
+    __shared__ uint64_t s_full[2], p_full[2], o_full[2], mma_done;
     __shared__ uint64_t ep_full[2], ep_empty[2];   // softmax -> epilogue handoff
     __shared__ float ep_m[2][kN];                  // the columns' reference maxima
     __shared__ uint32_t tmem_slot;
@@ -524,7 +543,8 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
     __shared__ int fx_n;
     __shared__ int fx_slot[kMaxFixSlots];
     __shared__ float fx_w[kN][kFixChunk], fx_lse[kN];   // merge: per column, the partials' weights and the merged LSE
-    __shared__ int pre_sh[PAGED ? kInlineB + 1 : 1], keys_sh[PAGED ? kInlineB : 1], pre_warp[PAGED ? 12 : 1];
+    __shared__ int pre_sh[PAGED ? kInlineB + 1 : 1], keys_sh[PAGED ? kInlineB : 1], range_sh[3];
+    __shared__ int2 sums_sh[PAGED ? 12 : 1];
 
     const int warp = threadIdx.x / 32;
     griddep_launch_dependents();
@@ -536,11 +556,8 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
             mbar_init(&q_full[i], 1);
             mbar_init(&q_empty[i], 1);
             mbar_init(&s_full[i], 1);
-            mbar_init(&s_empty[i], 4);   // one arrival per warp
             mbar_init(&p_full[i], 4);   // one arrival per warp
-            mbar_init(&p_empty[i], 1);
             mbar_init(&o_full[i], 1);
-            mbar_init(&o_empty[i], 4);   // one arrival per warp
             mbar_init(&ep_full[i], 4);   // one arrival per warp
             mbar_init(&ep_empty[i], 4);   // one arrival per warp
         }
@@ -565,85 +582,90 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
     if (blockIdx.x == 0 && threadIdx.x == 0 && p.nv_ts) *p.nv_ts = *p.nv_sg;   // single-pass NVFP4: report s_g
 
     const int *pre = p.prefix, *keys = nullptr;
-    int first_b = 0, P = static_cast<int>(gridDim.x);   // P: CTAs that the tiles are split over
-    __shared__ long long range_sh[2];   // paged split mode: the CTA's tiles
+    int first_b = 0;
+    Line line;
     if constexpr (PAGED) {
-        const int B = p.U / p.Hkv;
-        if (blockIdx.x == 0)
-            for (int b = threadIdx.x; b < B; b += blockDim.x)
-                if (p.seqlens[b] < 0 || p.seqlens[b] > p.cap) atomicExch(p.status, kDevBadPage);
+        // The CTA's range of tiles (range_sh) and the batch entry that it starts in: whoever has the entry that
+        // one of its two cuts falls in says so.
+        const int B = p.U / p.Hkv, c = static_cast<int>(blockIdx.x), lane = static_cast<int>(threadIdx.x) & 31;
+        auto owns = [&](int b, int start, int nt, const int (&cut)[2]) {
+            const int s0 = start * p.Hkv;
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                if (s0 <= cut[k] && cut[k] < s0 + nt * p.Hkv) {
+                    const int s = s0 + (cut[k] - s0) / nt * nt;
+                    range_sh[k] = unit_cut(cut[k], s, s + nt);
+                    if (k == 0) range_sh[2] = b;
+                }
+        };
         if (p.split && !p.prefix) {
             // a run of entries per thread, then a scan over the threads
             const int per = (B + blockDim.x - 1) / blockDim.x;
             const int b0 = min(B, static_cast<int>(threadIdx.x) * per), b1 = min(B, b0 + per);
-            int own = 0;
+            int own = 0, with_keys = 0;
             for (int b = b0; b < b1; ++b) {
-                keys_sh[b] = batch_keys<true>(p, b);
-                own += (keys_sh[b] + kTileKV - 1) / kTileKV;
+                const int n = batch_keys<true>(p, b);
+                keys_sh[b] = n;
+                own += (n + kTileKV - 1) / kTileKV;
+                with_keys += n > 0 ? 1 : 0;
             }
             int inc = own;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int v = __shfl_up_sync(0xffffffffu, inc, o);
-                if ((threadIdx.x & 31) >= o) inc += v;
+                if (lane >= o) inc += v;
             }
-            if ((threadIdx.x & 31) == 31) pre_warp[warp] = inc;
+            with_keys = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(with_keys)));
+            if (lane == 31) sums_sh[warp] = make_int2(inc, with_keys);
             __syncthreads();
-            int run = inc - own;
-            for (int w = 0; w < warp; ++w) run += pre_warp[w];
+            int before = 0, total = 0;
+            with_keys = 0;
+#pragma unroll
+            for (int w = 0; w < decode_threads<EPI>() / 32; ++w) {
+                const int2 v = sums_sh[w];
+                before += w < warp ? v.x : 0;
+                total += v.x;
+                with_keys += v.y;
+            }
+            line.init(total * p.Hkv, paged_ctas(total * p.Hkv, static_cast<long long>(with_keys) * p.Hkv, static_cast<int>(gridDim.x)));
+            const int cut[2] = {line.cut(c), line.cut(c + 1)};
+            int run = before + inc - own;
             for (int b = b0; b < b1; ++b) {
+                const int nt = (keys_sh[b] + kTileKV - 1) / kTileKV;
                 pre_sh[b] = run;
-                run += (keys_sh[b] + kTileKV - 1) / kTileKV;
+                if (c < line.P) owns(b, run, nt, cut);
+                run += nt;
             }
-            if (threadIdx.x == blockDim.x - 1) pre_sh[B] = run;
-            __syncthreads();
+            if (threadIdx.x == 0) pre_sh[B] = total;
             pre = pre_sh;
             keys = keys_sh;
+        } else if (p.split) {
+            line.init(pre[B] * p.Hkv, pre[B + 1]);
+            const int cut[2] = {line.cut(c), line.cut(c + 1)};
+            if (c < line.P)
+                for (int b = threadIdx.x; b < B; b += blockDim.x) owns(b, pre[b], pre[b + 1] - pre[b], cut);
         }
         if (p.split) {
-            // the CTA's range of tiles and the batch entry it starts in: the threads that own the entries with
-            // its two cuts say so
-            const long long T = static_cast<long long>(pre[B]) * p.Hkv;
-            const int c = static_cast<int>(blockIdx.x);
-            if (p.prefix) {
-                P = p.prefix[B + 1];
-            } else {
-                int with_keys = 0;
-                for (int b = threadIdx.x; b < B; b += blockDim.x) with_keys += pre[b + 1] > pre[b] ? 1 : 0;
-                with_keys = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(with_keys)));
-                if ((threadIdx.x & 31) == 0) pre_warp[warp] = with_keys;
-                __syncthreads();
-                with_keys = 0;
-                for (int w = 0; w < static_cast<int>(blockDim.x) / 32; ++w) with_keys += pre_warp[w];
-                P = paged_ctas(T, static_cast<long long>(with_keys) * p.Hkv, P);
-            }
-            if (threadIdx.x < 2) range_sh[threadIdx.x] = c < P ? T : 0;   // the cut behind the last tile has no owner
-            __syncthreads();
-            if (c < P) {
-                const long long cut[2] = {static_cast<long long>(c) * T / P, static_cast<long long>(c + 1) * T / P};
-                for (int b = threadIdx.x; b < B; b += blockDim.x) {
-                    const int nt = pre[b + 1] - pre[b];
-                    const long long s0 = static_cast<long long>(pre[b]) * p.Hkv, end = s0 + static_cast<long long>(nt) * p.Hkv;
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        if (s0 <= cut[k] && cut[k] < end) {
-                            const long long s = s0 + static_cast<long long>(static_cast<int>(cut[k] - s0) / nt) * nt;
-                            range_sh[k] = unit_cut(cut[k], s, s + nt);
-                            if (k == 0) pre_warp[0] = b;
-                        }
-                }
+            if (threadIdx.x == 0) {   // cuts that no entry has
+                if (c >= line.P || line.T == 0)
+                    range_sh[0] = range_sh[1] = range_sh[2] = 0;
+                else if (c + 1 == line.P)
+                    range_sh[1] = line.T;
             }
             __syncthreads();
-            first_b = T > 0 && c < P ? pre_warp[0] : 0;
+            first_b = range_sh[2];
         }
-        if (p.fixup)   // no combine kernel runs: entries without keys are written here
-            for (int b = blockIdx.x; b < B; b += gridDim.x)
-                if (pre[b + 1] == pre[b]) write_empty_entry(p, b);
     }
 
     Sched<PAGED> sched;
     sched.init(&p, blockIdx.x, gridDim.x, pre, keys, first_b, range_sh);
     Item it;
+
+    // fills fx_slot with the slots of the unit's partials
+    auto partial_slots = [&](const Item& it) {
+        if constexpr (PAGED) return paged_partial_slots(p, pre, line, it.b, it.head * p.chunks + it.chunk, fx_slot, kMaxFixSlots);
+        return unit_partial_slots(p, it.u, static_cast<int>(gridDim.x), fx_slot, kMaxFixSlots);
+    };
 
     // The epilogue of one item, run by 128 threads: the epilogue warpgroup (named barrier 2) when a
     // unit has several query columns, else the softmax warps themselves (barrier 1), for which the
@@ -691,17 +713,29 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
                 const float s = warp_sum(l[0]);
                 if (lane == 0) red_sum[ew][0] = s;
             } else {
-                // all columns' butterflies interleaved: five rounds of independent shuffles
+                // butterflies over the lanes in which each round halves the columns a lane carries: the lane keeps
+                // those whose bit matches its own and gives the others away (16 shuffles for 16 columns, not 80)
                 float v[NC];
 #pragma unroll
                 for (int q = 0; q < NC; ++q) v[q] = l[q];
+                int n = NC, col = 0;
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1)
+                for (int o = 16; o > 0; o >>= 1) {
+                    const bool up = lane & o;
+                    if (n > 1) {
+                        n >>= 1;
+                        col += up ? n : 0;
 #pragma unroll
-                    for (int q = 0; q < NC; ++q) v[q] += __shfl_xor_sync(0xffffffffu, v[q], o);
-                if (lane == 0)
-#pragma unroll
-                    for (int q = 0; q < NC; ++q) red_sum[ew][q] = v[q];
+                        for (int q = 0; q < NC / 2; ++q)
+                            if (q < n) {
+                                const float give = up ? v[q] : v[q + n], keep = up ? v[q + n] : v[q];
+                                v[q] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+                            }
+                    } else {
+                        v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+                    }
+                }
+                if ((lane & (32 / NC - 1)) == 0) red_sum[ew][col] = v[0];
             }
         }
         // red_sum is complete, and every thread is past its reads of the previous item's
@@ -761,7 +795,7 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
             // fence waits for the stores instead of 128.
             named_bar_sync(bar, 128);
             if (tid == 0) {
-                const int n = slots_ready ? fx_n : unit_partial_slots<PAGED>(p, pre, it.u, P, fx_slot, kMaxFixSlots);
+                const int n = slots_ready ? fx_n : partial_slots(it);
                 fx_n = n;
                 __threadfence();
                 const int arrived = n > 0 ? arrive_unit(p.unit_ctr + it.u, p.gen, n) : 0;
@@ -1064,7 +1098,6 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
             auto pv = [&]() {
                 mbar_wait(&p_full[pr.idx], pr.phase, wc);
                 mbar_wait(&v_full[vr.idx], vr.phase, wc);
-                mbar_wait(&o_empty[orr.idx], orr.phase ^ 1, wc);
                 tc_fence_after();
                 if (!aborted(wc)) {
                     const uint32_t sV = smem_u32(smem + C::kOffV + vr.idx * C::kKVBytes);
@@ -1078,7 +1111,6 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
                     }
                     mma_commit(&o_full[orr.idx]);
                     mma_commit(&v_empty[vr.idx]);
-                    mma_commit(&p_empty[pr.idx]);
                 }
                 pr.advance();
                 vr.advance();
@@ -1093,7 +1125,6 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
                 const uint32_t sQ = smem_u32(smem + C::kOffQ + qr.idx * C::kQBytes);
                 for (int t = it.t0; t < it.t1; ++t) {
                     mbar_wait(&k_full[kr.idx], kr.phase, wc);
-                    mbar_wait(&s_empty[sr.idx], sr.phase ^ 1, wc);
                     tc_fence_after();
                     if (!aborted(wc)) {
                         const uint32_t sK = smem_u32(smem + C::kOffK + kr.idx * C::kKVBytes);
@@ -1150,9 +1181,6 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
                 uint32_t ov[NC];
                 tmem_ld<NC>(tmem + lane_base + 32 + orr.idx * 16, ov);
                 tmem_ld_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&o_empty[orr.idx]);
                 orr.advance();
                 if (moved_prev) {
 #pragma unroll
@@ -1168,9 +1196,6 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
                 uint32_t sv[NC];
                 tmem_ld<NC>(tmem + lane_base + sr.idx * 16, sv);
                 tmem_ld_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s_empty[sr.idx]);
                 sr.advance();
 
                 const int kv = t * kTileKV + tid;
@@ -1226,12 +1251,12 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
                 }
                 vr.advance();
                 // rows of P beyond NC keep what they held: they only reach columns of O that nobody reads
-                mbar_wait(&p_empty[pr.idx], pr.phase ^ 1, wc);
                 uint8_t* sP = smem + C::kOffP + pr.idx * C::kPBytes;
 #pragma unroll
                 for (int q = 0; q < NC; ++q)
                     *reinterpret_cast<uint16_t*>(sP + sw128_offset(q, tid, kN * 128)) = float_to_bf16_bits(pv[q]);
                 fence_proxy_async_smem();
+                tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[pr.idx]);
                 pr.advance();
@@ -1287,7 +1312,7 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
             // a partial's slots (64-bit divisions) while the softmax warps still stream the item, off
             // the path from its last tile to its arrival count
             const bool partial = p.fixup && !(it.whole && !(p.split && p.nv_codes)) && it.t1 > it.t0;
-            if (partial && tid == 0) fx_n = unit_partial_slots<PAGED>(p, pre, it.u, P, fx_slot, kMaxFixSlots);
+            if (partial && tid == 0) fx_n = partial_slots(it);
             mbar_wait(&ep_full[hr.idx], hr.phase, wc);
             tc_fence_after();
             __syncwarp();   // tcgen05.ld is warp-collective
@@ -1317,6 +1342,15 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
     tc_fence_before();
     __syncthreads();
     if (warp == mma_warp<EPI>()) tmem_dealloc(tmem, C::kTmemCols);
+    if constexpr (PAGED) {
+        const int B = p.U / p.Hkv;
+        if (blockIdx.x == 0)
+            for (int b = threadIdx.x; b < B; b += blockDim.x)
+                if (p.seqlens[b] < 0 || p.seqlens[b] > p.cap) atomicExch(p.status, kDevBadPage);
+        if (p.fixup)   // no combine kernel runs: entries without keys are written here
+            for (int b = blockIdx.x; b < B; b += gridDim.x)
+                if (pre[b + 1] == pre[b]) write_empty_entry(p, b);
+    }
 }
 
 // Exclusive prefix of per-unit tile counts (ragged keys), one block.
@@ -1350,7 +1384,7 @@ __global__ void __launch_bounds__(1024) tile_prefix_kernel(const __grid_constant
     }
     if (threadIdx.x == 1023) prefix[U] = part[1023];
     if constexpr (PAGED) {   // and the CTAs that the tiles are split over
-        const long long total = part[1023];
+        const int total = part[1023];
         __syncthreads();
         part[threadIdx.x] = with_keys;
         __syncthreads();
@@ -1388,28 +1422,49 @@ __global__ void combine_kernel(const __grid_constant__ DecodeParams p, int nctas
     const int d = threadIdx.x;
     const int D = p.D;
     if (threadIdx.x < 32) {
-        int tiles;
-        long long Tu, T;
-        unit_range<PAGED>(p, p.prefix, u, tiles, Tu, T);
         int cnt = 0;
-        if (tiles > 0) {
-            const long long P = PAGED ? p.prefix[p.U / p.Hkv + 1] : nctas;
-            int c0 = static_cast<int>(min((((Tu + 1) * P) - 1) / T, P - 1));
-            int c1 = static_cast<int>(min((((Tu + tiles) * P) - 1) / T, P - 1));
-            if constexpr (PAGED) c0 = max(c0 - 1, 0), c1 = min(c1 + 1, static_cast<int>(P) - 1);   // a moved cut
-            for (int cw = c0; cw <= c1; cw += 32) {
-                const int c = cw + static_cast<int>(threadIdx.x);
-                // CTAs with an empty tile range (possible when T < P) hold no partial
-                const bool ok = c <= c1 && has_piece<PAGED>(c, static_cast<int>(P), T, Tu, tiles);
-                const unsigned m = __ballot_sync(0xffffffffu, ok);
-                if (ok) {
-                    const int idx = cnt + __popc(m & ((1u << threadIdx.x) - 1u));
-                    if (idx < kMaxPartsD) slots[idx] = u + c;
-                }
-                cnt += __popc(m);
+        if constexpr (PAGED) {
+            if (threadIdx.x == 0) {
+                const int B = p.U / p.Hkv;
+                Line line;
+                line.init(p.prefix[B] * p.Hkv, p.prefix[B + 1]);
+                cnt = paged_partial_slots(p, p.prefix, line, it.b, it.head * p.chunks + it.chunk, slots, kMaxPartsD);
             }
-            cnt = min(cnt, kMaxPartsD);
+            cnt = __shfl_sync(0xffffffffu, cnt, 0);
             if (cnt == 1 && !p.nv_codes) cnt = -1;   // one CTA held the whole unit and wrote it
+        } else {
+            int tiles;
+            long long Tu, T;
+            if (p.prefix) {
+                tiles = p.prefix[u + 1] - p.prefix[u];
+                Tu = p.prefix[u];
+                T = p.prefix[p.U];
+            } else {
+                tiles = p.tiles_uniform;
+                Tu = static_cast<long long>(u) * tiles;
+                T = static_cast<long long>(p.U) * tiles;
+            }
+            if (tiles > 0) {
+                const long long P = nctas;
+                const int c0 = static_cast<int>(min((((Tu + 1) * P) - 1) / T, P - 1));
+                const int c1 = static_cast<int>(min((((Tu + tiles) * P) - 1) / T, P - 1));
+                if (c0 == c1 && !p.nv_codes) {
+                    cnt = -1;   // one CTA held the whole unit and wrote it
+                } else {
+                    for (int cw = c0; cw <= c1; cw += 32) {
+                        const int c = cw + static_cast<int>(threadIdx.x);
+                        // CTAs with an empty tile range (possible when T < P) hold no partial
+                        const bool ok = c <= c1 && (c * T) / P != ((c + 1) * T) / P;
+                        const unsigned m = __ballot_sync(0xffffffffu, ok);
+                        if (ok) {
+                            const int idx = cnt + __popc(m & ((1u << threadIdx.x) - 1u));
+                            if (idx < kMaxPartsD) slots[idx] = u + c;
+                        }
+                        cnt += __popc(m);
+                    }
+                    cnt = min(cnt, kMaxPartsD);
+                }
+            }
         }
         __syncwarp();
         // LSE of the merged row and each partial's weight exp(lse_i - lse), once per block
