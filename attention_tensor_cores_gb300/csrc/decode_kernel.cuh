@@ -338,12 +338,40 @@ __device__ __forceinline__ void tma_load_4d_hint(void* dst, const CUtensorMap* m
         : "memory");
 }
 
-// Byte offset of element (row r, column k) of a K-major operand made of 128-byte-swizzled
-// atoms of 64 columns, `atom_bytes` apart.
-__device__ __forceinline__ uint32_t sw128_offset(int r, int k, uint32_t atom_bytes)
+// P^T of a tile is an MN-major operand with the 32-byte swizzle: 16 columns of a key in a row of 32 bytes, so
+// that the thread with the key stores them with at most two 16-byte stores (K-major rows of keys took one
+// 2-byte store per column); rows 4..7 of each 8 have their 16-byte halves exchanged.  Atoms of 8 keys are 256
+// bytes apart.
+__device__ __forceinline__ uint64_t sdesc_sw32(uint32_t saddr, uint32_t sbo_bytes)
 {
-    const int a = k >> 6, kk = k & 63;
-    return a * atom_bytes + r * 128 + ((((kk >> 3) ^ (r & 7)) & 7) << 4) + ((kk & 7) << 1);
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFF) >> 4);
+    d |= static_cast<uint64_t>(1) << 16;   // one atom spans all 16 columns: no stride between atoms along them
+    d |= static_cast<uint64_t>((sbo_bytes >> 4) & 0x3FFF) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(6) << 61;
+    return d;
+}
+
+// Row `key` of P^T, rounded to BF16 (the operand type of the MMA; half a step, 2^-9 to 2^-8 of a weight)
+template <int NC>
+__device__ __forceinline__ void store_p(uint8_t* sP, int key, const float (&pv)[NC])
+{
+    uint8_t* row = sP + key * 32 + ((key >> 2) & 1) * 16;   // columns 0..7; 8..15 are in the other half
+    if constexpr (NC == 1) {
+        *reinterpret_cast<uint16_t*>(row) = float_to_bf16_bits(pv[0]);
+    } else {
+        uint32_t w[NC / 2];
+#pragma unroll
+        for (int i = 0; i < NC / 2; ++i) w[i] = pack_bf16x2(pv[2 * i], pv[2 * i + 1]);
+        if constexpr (NC == 4) {
+            *reinterpret_cast<uint2*>(row) = make_uint2(w[0], w[1]);
+        } else {
+            *reinterpret_cast<uint4*>(row) = make_uint4(w[0], w[1], w[2], w[3]);
+            if constexpr (NC == 16)
+                *reinterpret_cast<uint4*>(sP + key * 32 + (((key >> 2) & 1) ^ 1) * 16) = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+    }
 }
 
 
@@ -1091,7 +1119,7 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
         // ------------------------------------------------ MMA issuer
         if (lane_id() == 0) {
             constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kN, false, false);
-            constexpr uint32_t idesc_pv = idesc_bf16_f32(128, kN, true, false);
+            constexpr uint32_t idesc_pv = idesc_bf16_f32(128, kN, true, true);
             using L = TileLayout<D, PAGED>;
             constexpr uint32_t lbo_v = (D >= 128) ? L::kHalf : 0u;   // D = 64: M rows 64..127 repeat 0..63
             Ring qr(2), kr(S), vr(S), sr(2), pr(2), orr(2);
@@ -1106,7 +1134,7 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
 #pragma unroll
                     for (int ks = 0; ks < kTileKV / 16; ++ks) {
                         const uint64_t da = sdesc_sw128(sV + ks * 2 * L::kGroup, lbo_v, L::kGroup);
-                        const uint64_t db = sdesc_sw128(sP + (ks >> 2) * (kN * 128) + (ks & 3) * 32, 16, 1024);
+                        const uint64_t db = sdesc_sw32(sP + ks * 512, 256);
                         mma_ss(dO, da, db, idesc_pv, ks > 0 ? 1u : 0u);
                     }
                     mma_commit(&o_full[orr.idx]);
@@ -1252,9 +1280,7 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
                 vr.advance();
                 // rows of P beyond NC keep what they held: they only reach columns of O that nobody reads
                 uint8_t* sP = smem + C::kOffP + pr.idx * C::kPBytes;
-#pragma unroll
-                for (int q = 0; q < NC; ++q)
-                    *reinterpret_cast<uint16_t*>(sP + sw128_offset(q, tid, kN * 128)) = float_to_bf16_bits(pv[q]);
+                store_p<NC>(sP, tid, pv);
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
