@@ -156,6 +156,7 @@ int run_paged(const PagedArgs& a, bool split, const PagedWs& w, uint8_t* base, c
     p.page = a.c->page_size;
     p.by_page = FastDiv(static_cast<uint32_t>(p.page));
     p.box = box;
+    while ((1 << p.box_log2) < box) ++p.box_log2;
     p.groups = static_cast<int>(page_groups(a.c));
     p.cap = a.max_pages * a.c->page_size;
     p.Skv = p.cap;
