@@ -72,6 +72,20 @@ def test_batches(B, most, add, P, done):
     run(ctx, new.tolist(), P, spare=int(rng.integers(0, 50)), pad=int(rng.integers(0, 700)), seed=B)
 
 
+@pytest.mark.parametrize("B, add", [(9, 700), (3000, 1)])
+def test_in_place_with_many_tokens_or_requests(B, add):
+    """More than 2048 of either: the lengths and the height are updated by a second launch."""
+    rng = np.random.default_rng(B)
+    ctx, new = rng.integers(0, 200, B).tolist(), rng.integers(add, add + 2, B)
+    new[::4] = -1
+    table, free, n, T = setup(ctx, new.tolist(), 16, 3, 11, B)
+    s = Step(ctx, new.tolist(), table, free, n, T)
+    s.seqlens, s.n_out = s.ctx, s.n
+    s.call(16)
+    assert F.fmha_check_status() == 0
+    s.same(page_table_ref(ctx, new, 16, free, n, table, T))
+
+
 def test_no_requests_and_no_tokens():
     s = Step([], [], np.zeros((0, 4), np.int32), np.arange(6), 6, 3)
     s.call(16)

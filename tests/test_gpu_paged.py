@@ -287,3 +287,16 @@ def test_refuses_wrong_shapes():
             F.fmha_fwd_paged(**args(**bad))
     with pytest.raises(F.FmhaError):
         F.fmha_fwd_paged(**args(opts=F.make_opts(workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))))
+
+
+@pytest.mark.parametrize("seed", range(60))
+def test_random_shapes(seed):
+    rng = np.random.default_rng(1000 + seed)
+    pick = lambda *a: a[int(rng.integers(len(a)))]   # noqa: E731
+    Sq, group, Hkv, D = pick(1, 1, 2, 3, 4, 7), pick(1, 2, 3, 4, 5, 8, 16), pick(1, 2, 3), pick(64, 128)
+    B = pick(1, 2, 5, 17, 60)
+    most = int(np.exp(rng.uniform(0, np.log(6000 // B + 2))))
+    lens = rng.integers(0, most + 1, B)
+    lens[rng.integers(B)] = most
+    p = Problem(lens.tolist(), Hkv * group, Hkv, Sq, D, pick(8, 16, 32, 40, 64, 128, 160), pick("hnd", "nhd", "kv"), seed)
+    check(p, bool(rng.integers(2)), kinds=(pick(F.FMHA_OUT_BF16, F.FMHA_OUT_F32),))
