@@ -611,12 +611,11 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
     if (blockIdx.x == 0 && threadIdx.x == 0 && p.nv_ts) *p.nv_ts = *p.nv_sg;   // single-pass NVFP4: report s_g
 
     const int *pre = p.prefix, *keys = nullptr;
-    int first_b = 0;
+    int range[2] = {0, 0}, first_b = 0;   // paged split mode: the CTA's tiles and the batch entry it starts in
     Line line;
     if constexpr (PAGED) {
-        // The CTA's range of tiles (range_sh) and the batch entry that it starts in: whoever has the entry that
-        // one of its two cuts falls in says so.
         const int B = p.U / p.Hkv, c = static_cast<int>(blockIdx.x), lane = static_cast<int>(threadIdx.x) & 31;
+        // whoever has the entry that one of the CTA's two cuts falls in says so
         auto owns = [&](int b, int start, int nt, const int (&cut)[2]) {
             const int s0 = start * p.Hkv;
 #pragma unroll
@@ -627,7 +626,39 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
                     if (k == 0) range_sh[2] = b;
                 }
         };
-        if (p.split && !p.prefix) {
+        if (p.split && !p.prefix && B <= 32) {
+            // a lane per entry, the same in every warp: no barrier (all write the same to shared memory)
+            const int n = lane < B ? batch_keys<true>(p, lane) : 0, nt = (n + kTileKV - 1) / kTileKV;
+            int inc = nt;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += v;
+            }
+            const int T = __shfl_sync(0xffffffffu, inc, 31) * p.Hkv, start = inc - nt;
+            line.init(T, paged_ctas(T, static_cast<long long>(__popc(__ballot_sync(0xffffffffu, n > 0))) * p.Hkv, static_cast<int>(gridDim.x)));
+            keys_sh[lane] = n;
+            pre_sh[lane] = start;
+            if (lane == 31) pre_sh[32] = inc;
+            __syncwarp();
+            pre = pre_sh;
+            keys = keys_sh;
+            if (c < line.P && T > 0) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int cut = line.cut(c + k);
+                    const unsigned has = __ballot_sync(0xffffffffu, start * p.Hkv <= cut && cut < inc * p.Hkv);
+                    if (has) {
+                        const int b = __ffs(has) - 1, s0 = pre_sh[b] * p.Hkv, tiles = pre_sh[b + 1] - pre_sh[b];
+                        const int s = s0 + (cut - s0) / tiles * tiles;
+                        range[k] = unit_cut(cut, s, s + tiles);
+                        if (k == 0) first_b = b;
+                    } else {
+                        range[k] = T;   // the cut behind the last tile
+                    }
+                }
+            }
+        } else if (p.split && !p.prefix) {
             // a run of entries per thread, then a scan over the threads
             const int per = (B + blockDim.x - 1) / blockDim.x;
             const int b0 = min(B, static_cast<int>(threadIdx.x) * per), b1 = min(B, b0 + per);
@@ -674,7 +705,7 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
             if (c < line.P)
                 for (int b = threadIdx.x; b < B; b += blockDim.x) owns(b, pre[b], pre[b + 1] - pre[b], cut);
         }
-        if (p.split) {
+        if (p.split && (p.prefix || B > 32)) {
             if (threadIdx.x == 0) {   // cuts that no entry has
                 if (c >= line.P || line.T == 0)
                     range_sh[0] = range_sh[1] = range_sh[2] = 0;
@@ -682,12 +713,14 @@ __global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
                     range_sh[1] = line.T;
             }
             __syncthreads();
+            range[0] = range_sh[0];
+            range[1] = range_sh[1];
             first_b = range_sh[2];
         }
     }
 
     Sched<PAGED> sched;
-    sched.init(&p, blockIdx.x, gridDim.x, pre, keys, first_b, range_sh);
+    sched.init(&p, blockIdx.x, gridDim.x, pre, keys, first_b, range);
     Item it;
 
     // fills fx_slot with the slots of the unit's partials
