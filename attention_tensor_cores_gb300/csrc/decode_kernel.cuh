@@ -10,9 +10,10 @@
 //  * Swap-AB.  With G <= 16 query rows per key/value head (G = (Hq/Hkv) * Sq), the products are
 //    taken transposed so that the 128 keys of a tile fill the MMA's M dimension:
 //      S^T[kv][q] = K[kv][:] . Q[q][:]      (A = K tile, K-major; B = Q rows, K-major; N = 16)
-//      O^T[d][q]  = V^T[d][kv] . P^T[kv][q]  (A = V tile read MN-major; B = P, K-major; N = 16)
+//      O^T[d][q]  = V^T[d][kv] . P^T[kv][q]  (A = V tile and B = P^T, both read MN-major; N = 16)
 //    Thread t of the softmax warpgroup owns TMEM lane t: key t of the tile for S, feature d = t
-//    for O.  Reductions over keys are warp shuffles plus a 4-warp shared-memory step.
+//    for O.  Reductions over keys are warp shuffles plus a 4-warp shared-memory step.  The softmax
+//    computes NC = 1, 4, 8 or 16 of the 16 columns, the smallest that holds a unit's rows.
 //  * The per-tile PV product goes to a fresh TMEM buffer (no accumulate) and the softmax threads
 //    fold it into register accumulators with the rescale factor: acc = alpha * acc + O_tile.
 //    O is never read-modify-written in TMEM, so there is no ordering hazard between the rescale
@@ -20,14 +21,17 @@
 //  * Work split ("stream-K" over keys): the key tiles of all units (b, kv-head) are laid end to
 //    end and CTA c of P takes tiles [c*T/P, (c+1)*T/P).  Each maximal run inside one unit is a
 //    work item; an item that covers a whole unit writes the final O and LSE, otherwise it writes
-//    a normalised partial (O_i, lse_i) to slot u + c of the workspace and the combine kernel
-//    merges them: lse = log sum_i exp(lse_i), O = sum_i exp(lse_i - lse) O_i.  Ragged batches
-//    balance by construction.  With num_splits == 1 each CTA takes whole units instead.
-//  * Roles (decode_kernel<D, CAUSAL, EPI>): warps 0-3 softmax.  EPI (units of several query
-//    columns): warps 4-7 epilogue, warp 8 TMA producer, warp 9 MMA issuer, warps 10-11 only complete
+//    a normalised partial (O_i, lse_i) to slot u + c of the workspace, and the CTA that completes
+//    the unit (or the combine kernel) merges them: lse = log sum_i exp(lse_i),
+//    O = sum_i exp(lse_i - lse) O_i.  Ragged batches balance by construction.  With
+//    num_splits == 1 each CTA takes whole units instead.
+//  * Paged keys and values (PAGED): the producer gathers a tile page by page (see the producer), and
+//    the work split comes from the requests' lengths inside the kernel (see Line).
+//  * Roles (decode_kernel<D, CAUSAL, NC, PAGED>): warps 0-3 softmax.  EPI (see
+//    has_epilogue_warps): warps 4-7 epilogue, warp 8 TMA producer, warp 9 MMA issuer, warps 10-11 only complete
 //    their warpgroup; at the end of a work item the softmax warps hand its accumulators to the
 //    epilogue warps (Tensor Memory, two buffers) and go on with the next item while the epilogue
-//    normalises, stores and merges.  !EPI (one column): warp 4 producer, warp 5 MMA, and the softmax
+//    normalises, stores and merges.  !EPI: warp 4 producer, warp 5 MMA, and the softmax
 //    warps run each item's short epilogue themselves.  Every wait is bounded; a timeout flips the
 //    CTA into a drain mode (no new TMA/MMA, loops run out) and sets the device status word.
 #pragma once
@@ -60,6 +64,12 @@ constexpr int kN = 16;          // query rows per unit, padded (MMA N)
 // softmax warps run each item's epilogue themselves and warps 4 and 5 are the producer and the MMA.
 template <bool EPI>
 constexpr int decode_threads() { return EPI ? 384 : 192; }
+// Several columns: publishing a partial costs several tiles' streaming time, which the extra warps take off the
+// softmax.  One dense column: it is short, and the handoff measured 1 % slower.  One paged column keeps them, as
+// lengths differ and most CTAs publish: B8 Hkv16 0..2000 keys D64 21.3 -> 20.4 us, B32 Hkv8 0..500 18.6 -> 17.3,
+// B8 Hkv32 4096 keys (HBM-bound) 83.3 both ways.
+template <int NC, bool PAGED>
+constexpr bool has_epilogue_warps() { return NC > 1 || PAGED; }
 template <bool EPI>
 constexpr int tma_warp() { return EPI ? 8 : 4; }
 template <bool EPI>
@@ -380,9 +390,11 @@ __device__ __forceinline__ void store_p(uint8_t* sP, int key, const float (&pv)[
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N])
 {
-    static_assert(N == 1 || N == 4 || N == 8 || N == 16 || N == 32, "column counts in use");
+    static_assert(N == 1 || N == 2 || N == 4 || N == 8 || N == 16 || N == 32, "column counts in use");
     if constexpr (N == 1)
         asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r[0]) : "r"(taddr));
+    else if constexpr (N == 2)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(taddr));
     else if constexpr (N == 4)
         asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(taddr));
@@ -399,8 +411,10 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N])
 template <int N>
 __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[N])
 {
-    static_assert(N == 8 || N == 16 || N == 32, "column counts in use");
-    if constexpr (N == 8)
+    static_assert(N == 2 || N == 8 || N == 16 || N == 32, "column counts in use");
+    if constexpr (N == 2)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(taddr), "r"(r[0]), "r"(r[1]) : "memory");
+    else if constexpr (N == 8)
         asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
                      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                      : "memory");
@@ -546,13 +560,13 @@ __device__ __forceinline__ void write_empty_entry(const DecodeParams& p, int b)
 inline int decode_columns(int G) { return G <= 1 ? 1 : G <= 4 ? 4 : G <= 8 ? 8 : 16; }
 
 template <int D, bool CAUSAL, int NC, bool PAGED = false>
-__global__ void __launch_bounds__(decode_threads<(NC > 1)>(), 1)
+__global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()>(), 1)
     decode_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap, const __grid_constant__ DecodeParams p)
 {
     using C = DecodeCfg<D>;
     constexpr int S = C::kStages;
-    constexpr bool EPI = NC > 1;
+    constexpr bool EPI = has_epilogue_warps<NC, PAGED>();
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
 

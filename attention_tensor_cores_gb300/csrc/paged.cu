@@ -187,11 +187,10 @@ int run_paged(const PagedArgs& a, bool split, const PagedWs& w, uint8_t* base, c
         FMHA_CHECK_CUDA(launch_pdl(tile_prefix_kernel<true>, dim3(1), dim3(1024), 0, st, p, const_cast<int32_t*>(p.prefix)));
         count_launch();
     }
-    const bool epi = s.G > 1;   // as in the dense decode: the epilogue warpgroup pays with several columns
     const auto kernel = kernel_for<D, CAUSAL>(s.G);
     FMHA_CHECK_CUDA(set_smem_limit_once(reinterpret_cast<const void*>(kernel), C::kSmemBytes));
     timing_mark_begin(st);
-    const cudaError_t e = launch_pdl(kernel, dim3(grid), dim3(epi ? decode_threads<true>() : decode_threads<false>()), C::kSmemBytes,
+    const cudaError_t e = launch_pdl(kernel, dim3(grid), dim3(decode_threads<true>()), C::kSmemBytes,
                                      st, qmap, kmap, vmap, p);
     timing_mark_end(st);
     FMHA_CHECK_CUDA(e);
