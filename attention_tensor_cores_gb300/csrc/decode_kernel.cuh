@@ -1306,7 +1306,8 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
                 }
                 // Keys at or beyond n in a partial tile: their V rows may hold anything (NaN in
                 // padded memory) and P = 0 does not cancel NaN in the MMA, so zero those rows.
-                // Whole 128-byte rows are zeroed, which the swizzle only permutes within.
+                // Whole 128-byte rows are zeroed, which the swizzle only permutes within, each thread its own in
+                // an order that keeps a warp's stores on different banks.
                 if ((t + 1) * kTileKV > it.n) {
                     mbar_wait(&v_full[vr.idx], vr.phase, wc);
                     if (!valid) {
@@ -1315,7 +1316,7 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
                         for (int a = 0; a < C::kAtoms; ++a)
 #pragma unroll
                             for (int i = 0; i < 8; ++i)
-                                reinterpret_cast<uint4*>(rowp + a * TileLayout<D, PAGED>::kHalf)[i] = make_uint4(0, 0, 0, 0);
+                                reinterpret_cast<uint4*>(rowp + a * TileLayout<D, PAGED>::kHalf)[i ^ (tid & 7)] = make_uint4(0, 0, 0, 0);
                     }
                 }
                 vr.advance();
