@@ -50,11 +50,11 @@ typedef enum {
     FMHA_ERR_WORKSPACE = 3,   /* workspace missing or smaller than fmha_workspace_size() */
     FMHA_ERR_CUDA = 4,        /* a CUDA runtime/driver call or kernel launch failed */
     FMHA_ERR_TIMEOUT = 5,     /* a kernel's bounded wait expired (see fmha_check_status) */
-    FMHA_ERR_PAGES = 7,       /* a paged-cache call met data out of bounds on the device: a length, page,
-                                 slot or position, or too few free pages (see fmha_check_status) */
-    FMHA_ERR_RACE = 6         /* a split-KV merge counter never settled: calls sharing one
+    FMHA_ERR_RACE = 6,        /* a split-KV merge counter never settled: calls sharing one
                                  workspace (or the allocation-free scratch) overlapped on the
                                  GPU, so some output rows may be unmerged (see fmha_check_status) */
+    FMHA_ERR_PAGES = 7        /* a paged-cache call met data out of bounds on the device: a length, page,
+                                 slot or position, or too few free pages (see fmha_check_status) */
 } fmha_status;
 
 typedef enum {

@@ -300,3 +300,18 @@ def test_random_shapes(seed):
     lens[rng.integers(B)] = most
     p = Problem(lens.tolist(), Hkv * group, Hkv, Sq, D, pick(8, 16, 32, 40, 64, 128, 160), pick("hnd", "nhd", "kv"), seed)
     check(p, bool(rng.integers(2)), kinds=(pick(F.FMHA_OUT_BF16, F.FMHA_OUT_F32),))
+
+
+@pytest.mark.parametrize("Hq, Hkv, D", [(4, 4, 128), (16, 2, 64)])
+def test_forced_timeout_is_reported(Hq, Hkv, D):
+    """With a wait limit of one cycle the kernel drains and reports; the next call is right."""
+    p = Problem([900, 0, 333], Hq, Hkv, 1, D, 16, seed=8)
+    assert F.fmha_check_status() == 0
+    F.fmha_set_wait_limit(1)
+    try:
+        p.run()
+        rc = F.fmha_check_status()
+    finally:
+        F.fmha_set_wait_limit(0)
+    assert rc == F.FMHA_ERR_TIMEOUT
+    check(p)
