@@ -13,6 +13,7 @@
 #include <string>
 
 #include "internal.h"
+#include "paged.h"
 
 namespace atc_gb300 {
 
@@ -35,7 +36,6 @@ int cuda_error(cudaError_t e, const char* what)
 // expires.  Its address is looked up once per device and passed to kernels as a pointer.
 static __device__ int g_status_word;
 static constexpr int kDevMergeLost = 6;   // the value the split-KV merge leaves (ptx.cuh)
-static constexpr int kDevBadPage = 7;     // the value the paged-cache kernels leave
 static constexpr int kMaxDevices = 64;
 static std::atomic<int*> g_status_addr[kMaxDevices];
 static std::atomic<int> g_num_sms[kMaxDevices];

@@ -42,6 +42,7 @@
 #include "fastdiv.cuh"
 #include "internal.h"
 #include "nvfp4_dev.cuh"
+#include "paged.h"
 #include "ptx.cuh"
 
 namespace atc_gb300 {
@@ -89,7 +90,7 @@ struct DecodeCfg {
     static constexpr int kStages = (D == 64) ? 4 : 3;      // K and V ring depth
     static constexpr int kQBytes = kAtoms * kN * 128;      // one Q buffer
     static constexpr int kKVBytes = kAtoms * kTileKV * 128;
-    static constexpr int kPBytes = 2 * kN * 128;           // P^T: 16 rows x 128 keys
+    static constexpr int kPBytes = 2 * kN * 128;           // P^T: 128 keys x 16 columns
     static constexpr int kOffQ = 0;
     static constexpr int kOffK = kOffQ + 2 * kQBytes;
     static constexpr int kOffV = kOffK + kStages * kKVBytes;
@@ -174,7 +175,7 @@ struct Line {
         q = T / P;
         r = T - q * P;
     }
-    // floor(c T / P); P <= 2^15
+    // floor(c T / P) of c <= P (c r stays small: P is at most the number of SMs)
     __device__ int cut(int c) const { return c * q + c * r / P; }
 };
 
@@ -326,9 +327,6 @@ struct Sched {
     }
 };
 
-// Status word value of a page index outside the pool or a length outside its table row
-constexpr int kDevBadPage = 7;
-
 __device__ __forceinline__ void tma_load_5d_hint(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z, int w, int v,
                                                  uint64_t policy)
 {
@@ -384,7 +382,6 @@ __device__ __forceinline__ void store_p(uint8_t* sP, int key, const float (&pv)[
         }
     }
 }
-
 
 // Tensor Memory loads and stores of N consecutive columns of this warp's 32 lanes
 template <int N>
@@ -743,10 +740,9 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
         return unit_partial_slots(p, it.u, static_cast<int>(gridDim.x), fx_slot, kMaxFixSlots);
     };
 
-    // The epilogue of one item, run by 128 threads: the epilogue warpgroup (named barrier 2) when a
-    // unit has several query columns, else the softmax warps themselves (barrier 1), for which the
-    // epilogue is short and an extra warpgroup's handoff measured slower.  tid: O^T row (Tensor
-    // Memory lane) and output column, ew: warp within the group.
+    // The epilogue of one item, run by 128 threads: the epilogue warpgroup (named barrier 2) or, without
+    // one, the softmax warps themselves (barrier 1).  tid: O^T row (Tensor Memory lane) and output
+    // column, ew: warp within the group.
     // slots_ready: fx_n / fx_slot already hold this item's partial slots (the epilogue warpgroup finds
     // them while it waits for the item)
     auto run_epilogue = [&](const Item& it, bool empty, const float (&m)[NC], const float (&l)[NC],

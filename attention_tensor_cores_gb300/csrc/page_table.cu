@@ -26,7 +26,6 @@ namespace atc_gb300 {
 namespace {
 
 constexpr int kMaxRequests = 8192;   // 16 bytes of shared memory each
-constexpr int kDevBadPage = 7;
 
 struct PageTableParams {
     const int32_t* ctx;

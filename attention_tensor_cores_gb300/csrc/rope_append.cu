@@ -17,8 +17,6 @@
 namespace atc_gb300 {
 namespace {
 
-constexpr int kDevBadPage = 7;
-
 struct AppendParams {
     const uint16_t *q, *k, *v;
     int64_t q_stride, k_stride, v_stride;   // elements between tokens
