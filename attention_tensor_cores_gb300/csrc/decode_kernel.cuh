@@ -166,23 +166,22 @@ struct Item {
 constexpr int kMinPiece = 4;
 
 struct Line {
-    int T = 0, P = 1, q = 0, r = 0;   // T = q P + r
+    int T = 0, P = 1;
 
-    __device__ void init(int tiles, int ctas)
+    // floor(c T / P) of c <= P, P at most the number of SMs (below 512)
+    __device__ int cut(int c) const
     {
-        T = tiles;
-        P = ctas;
-        q = T / P;
-        r = T - q * P;
+        if (T < (1 << 23)) return static_cast<int>(static_cast<unsigned>(c) * static_cast<unsigned>(T) / static_cast<unsigned>(P));
+        return static_cast<int>(static_cast<long long>(c) * T / P);
     }
-    // floor(c T / P) of c <= P (c r stays small: P is at most the number of SMs)
-    __device__ int cut(int c) const { return c * q + c * r / P; }
 };
 
-__device__ __forceinline__ int paged_ctas(int T, long long units, int n)
-{
-    return static_cast<int>(max(1ll, min(static_cast<long long>(n), max(static_cast<long long>(T / kMinPiece), units))));
-}
+__device__ __forceinline__ int paged_ctas(int T, int units, int n) { return max(1, min(n, max(T / kMinPiece, units))); }
+
+// Where a CTA's range of tiles begins: tile g, the first of item (b, i, t0)
+struct Start {
+    int g = 0, b = 0, i = 0, t0 = 0;
+};
 
 // the cut at x as the unit of tiles [s, e) sees it (s or e when it is not inside)
 __device__ __forceinline__ int unit_cut(int x, int s, int e)
@@ -226,7 +225,7 @@ struct Sched {
     Pos g, g1;          // split mode: current / end global tile
     int u;              // whole-unit mode: next unit
     int cta, nctas;
-    int b, i;           // paged split mode: batch entry and unit of it that tile g is in (first: i < 0)
+    int b, i, t0;       // paged split mode: batch entry, unit of it and tile of that which tile g is
 
     __device__ int unit_tiles(int u) const
     {
@@ -240,7 +239,7 @@ struct Sched {
     }
     __device__ int unit_keys(int u) const { return p->seqlens ? batch_keys<PAGED>(*p, u / p->Hkv) : p->Skv; }
 
-    __device__ void init(const DecodeParams* pp, int c, int n, const int* prefix, const int* lengths, int first, const int* range)
+    __device__ void init(const DecodeParams* pp, int c, int n, const int* prefix, const int* lengths, const Start& start, int end)
     {
         p = pp;
         pre = prefix;
@@ -249,10 +248,11 @@ struct Sched {
         nctas = n;
         if (p->split) {
             if constexpr (PAGED) {
-                b = first;
-                i = -1;
-                g = range[0];
-                g1 = range[1];
+                b = start.b;
+                i = start.i;
+                t0 = start.t0;
+                g = start.g;
+                g1 = end;
                 return;
             }
             const long long T = p->prefix ? p->prefix[p->U] : static_cast<long long>(p->U) * p->tiles_uniform;
@@ -268,19 +268,14 @@ struct Sched {
         if (p->split) {
             if (g >= g1) return false;
             if constexpr (PAGED) {
-                // on to the batch entry that holds tile g (b >= the one before, entries may have no tiles)
+                // on to the batch entry that holds tile g (entries may have no tiles)
                 while (pre[b + 1] * p->Hkv <= g) {
                     ++b;
                     i = 0;
                 }
                 const int nt = pre[b + 1] - pre[b];
-                if (i < 0) {   // first item: the only one that may start inside a unit
-                    const int r = g - pre[b] * p->Hkv;
-                    i = r / nt;
-                    it.t0 = r - i * nt;
-                } else {
-                    it.t0 = 0;
-                }
+                it.t0 = t0;   // only a first item may start inside its unit
+                t0 = 0;
                 it.u = b * p->Hkv + i;
                 it.t1 = min(nt, g1 - g + it.t0);
                 it.n = keys ? keys[b] : batch_keys<true>(*p, b);
@@ -583,8 +578,10 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
     __shared__ int fx_n;
     __shared__ int fx_slot[kMaxFixSlots];
     __shared__ float fx_w[kN][kFixChunk], fx_lse[kN];   // merge: per column, the partials' weights and the merged LSE
-    __shared__ int pre_sh[PAGED ? kInlineB + 1 : 1], keys_sh[PAGED ? kInlineB : 1], range_sh[3];
+    __shared__ int pre_sh[PAGED ? kInlineB + 1 : 1], keys_sh[PAGED ? kInlineB : 1];
     __shared__ int2 sums_sh[PAGED ? 12 : 1];
+    __shared__ int4 start_raw[2];
+    Start* start_sh = reinterpret_cast<Start*>(start_raw);
 
     const int warp = threadIdx.x / 32;
     griddep_launch_dependents();
@@ -614,6 +611,13 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
         tmem_alloc(&tmem_slot, C::kTmemCols);
         tmem_relinquish();
     }
+    if constexpr (PAGED) {
+        if (threadIdx.x == tma_warp<EPI>() * 32) {
+            tma_prefetch_desc(&qmap);
+            tma_prefetch_desc(&kmap);
+            tma_prefetch_desc(&vmap);
+        }
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -622,20 +626,27 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
     if (blockIdx.x == 0 && threadIdx.x == 0 && p.nv_ts) *p.nv_ts = *p.nv_sg;   // single-pass NVFP4: report s_g
 
     const int *pre = p.prefix, *keys = nullptr;
-    int range[2] = {0, 0}, first_b = 0;   // paged split mode: the CTA's tiles and the batch entry it starts in
+    Start first;        // paged split mode: the CTA's range of tiles
+    int end = 0;
     Line line;
     if constexpr (PAGED) {
         const int B = p.U / p.Hkv, c = static_cast<int>(blockIdx.x), lane = static_cast<int>(threadIdx.x) & 31;
+        // the CTA's cut at x, in batch entry b of nt tiles a unit whose first tile is s0
+        auto start_at = [&](int x, int b, int s0, int nt) {
+            Start r;
+            const int i = static_cast<int>(static_cast<unsigned>(x - s0) / static_cast<unsigned>(nt)), s = s0 + i * nt;
+            r.g = unit_cut(x, s, s + nt);
+            r.b = b;
+            r.i = r.g == s + nt ? i + 1 : i;
+            r.t0 = r.g == s + nt ? 0 : r.g - s;
+            return r;
+        };
         // whoever has the entry that one of the CTA's two cuts falls in says so
         auto owns = [&](int b, int start, int nt, const int (&cut)[2]) {
             const int s0 = start * p.Hkv;
 #pragma unroll
             for (int k = 0; k < 2; ++k)
-                if (s0 <= cut[k] && cut[k] < s0 + nt * p.Hkv) {
-                    const int s = s0 + (cut[k] - s0) / nt * nt;
-                    range_sh[k] = unit_cut(cut[k], s, s + nt);
-                    if (k == 0) range_sh[2] = b;
-                }
+                if (s0 <= cut[k] && cut[k] < s0 + nt * p.Hkv) start_sh[k] = start_at(cut[k], b, s0, nt);
         };
         if (p.split && !p.prefix && B <= 32) {
             // a lane per entry, the same in every warp: no barrier (all write the same to shared memory)
@@ -646,28 +657,29 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
                 const int v = __shfl_up_sync(0xffffffffu, inc, o);
                 if (lane >= o) inc += v;
             }
-            const int T = __shfl_sync(0xffffffffu, inc, 31) * p.Hkv, start = inc - nt;
-            line.init(T, paged_ctas(T, static_cast<long long>(__popc(__ballot_sync(0xffffffffu, n > 0))) * p.Hkv, static_cast<int>(gridDim.x)));
+            const int start = inc - nt;
+            line.T = __shfl_sync(0xffffffffu, inc, 31) * p.Hkv;
+            line.P = paged_ctas(line.T, __popc(__ballot_sync(0xffffffffu, n > 0)) * p.Hkv, static_cast<int>(gridDim.x));
             keys_sh[lane] = n;
             pre_sh[lane] = start;
             if (lane == 31) pre_sh[32] = inc;
             __syncwarp();
             pre = pre_sh;
             keys = keys_sh;
-            if (c < line.P && T > 0) {
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int cut = line.cut(c + k);
-                    const unsigned has = __ballot_sync(0xffffffffu, start * p.Hkv <= cut && cut < inc * p.Hkv);
-                    if (has) {
-                        const int b = __ffs(has) - 1, s0 = pre_sh[b] * p.Hkv, tiles = pre_sh[b + 1] - pre_sh[b];
-                        const int s = s0 + (cut - s0) / tiles * tiles;
-                        range[k] = unit_cut(cut, s, s + tiles);
-                        if (k == 0) first_b = b;
-                    } else {
-                        range[k] = T;   // the cut behind the last tile
-                    }
-                }
+            if (c < line.P && line.T > 0) {
+                // even lanes look at the CTA's first cut, odd lanes at the next CTA's
+                const int cut = line.cut(c + (lane & 1)), cut0 = __shfl_sync(0xffffffffu, cut, 0), cut1 = __shfl_sync(0xffffffffu, cut, 1);
+                const unsigned has0 = __ballot_sync(0xffffffffu, start * p.Hkv <= cut0 && cut0 < inc * p.Hkv);
+                const unsigned has1 = __ballot_sync(0xffffffffu, start * p.Hkv <= cut1 && cut1 < inc * p.Hkv);
+                const int b = max(__ffs(lane & 1 ? has1 : has0) - 1, 0);
+                const int s0 = __shfl_sync(0xffffffffu, start, b) * p.Hkv, tiles = __shfl_sync(0xffffffffu, nt, b);
+                const Start mine = start_at(cut, b, s0, max(tiles, 1));
+                first.g = __shfl_sync(0xffffffffu, mine.g, 0);
+                first.b = __shfl_sync(0xffffffffu, mine.b, 0);
+                first.i = __shfl_sync(0xffffffffu, mine.i, 0);
+                first.t0 = __shfl_sync(0xffffffffu, mine.t0, 0);
+                end = __shfl_sync(0xffffffffu, mine.g, 1);
+                if (!has1) end = line.T;   // the cut behind the last tile
             }
         } else if (p.split && !p.prefix) {
             // a run of entries per thread, then a scan over the threads
@@ -698,7 +710,8 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
                 total += v.x;
                 with_keys += v.y;
             }
-            line.init(total * p.Hkv, paged_ctas(total * p.Hkv, static_cast<long long>(with_keys) * p.Hkv, static_cast<int>(gridDim.x)));
+            line.T = total * p.Hkv;
+            line.P = paged_ctas(line.T, with_keys * p.Hkv, static_cast<int>(gridDim.x));
             const int cut[2] = {line.cut(c), line.cut(c + 1)};
             int run = before + inc - own;
             for (int b = b0; b < b1; ++b) {
@@ -711,7 +724,8 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
             pre = pre_sh;
             keys = keys_sh;
         } else if (p.split) {
-            line.init(pre[B] * p.Hkv, pre[B + 1]);
+            line.T = pre[B] * p.Hkv;
+            line.P = pre[B + 1];
             const int cut[2] = {line.cut(c), line.cut(c + 1)};
             if (c < line.P)
                 for (int b = threadIdx.x; b < B; b += blockDim.x) owns(b, pre[b], pre[b + 1] - pre[b], cut);
@@ -719,19 +733,18 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
         if (p.split && (p.prefix || B > 32)) {
             if (threadIdx.x == 0) {   // cuts that no entry has
                 if (c >= line.P || line.T == 0)
-                    range_sh[0] = range_sh[1] = range_sh[2] = 0;
+                    start_sh[0] = start_sh[1] = Start{};
                 else if (c + 1 == line.P)
-                    range_sh[1] = line.T;
+                    start_sh[1].g = line.T;
             }
             __syncthreads();
-            range[0] = range_sh[0];
-            range[1] = range_sh[1];
-            first_b = range_sh[2];
+            first = start_sh[0];
+            end = start_sh[1].g;
         }
     }
 
     Sched<PAGED> sched;
-    sched.init(&p, blockIdx.x, gridDim.x, pre, keys, first_b, range);
+    sched.init(&p, blockIdx.x, gridDim.x, pre, keys, first, end);
     Item it;
 
     // fills fx_slot with the slots of the unit's partials
@@ -1023,11 +1036,6 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
             // and issues it, for K and for V.  A page outside the pool loads zeros (the tensor map's fill) and
             // sets the status.  One elected thread issuing every box measured 25 % slower than a lane per box.
             const int lane = static_cast<int>(lane_id());
-            if (lane == 0) {
-                tma_prefetch_desc(&qmap);
-                tma_prefetch_desc(&kmap);
-                tma_prefetch_desc(&vmap);
-            }
             const uint64_t pol = policy_evict_first();
             Ring qr(2), kr(S), vr(S);
             uint32_t kcnt[S], vcnt[S], qcnt[2] = {0, 0};
@@ -1453,7 +1461,7 @@ __global__ void __launch_bounds__(1024) tile_prefix_kernel(const __grid_constant
         part[threadIdx.x] = with_keys;
         __syncthreads();
         if (threadIdx.x == 0) {
-            long long n = 0;
+            int n = 0;
             for (int i = 0; i < 1024; ++i) n += part[i];
             prefix[U + 1] = paged_ctas(total * p.Hkv, n * p.Hkv, p.ctas);
         }
@@ -1491,7 +1499,8 @@ __global__ void combine_kernel(const __grid_constant__ DecodeParams p, int nctas
             if (threadIdx.x == 0) {
                 const int B = p.U / p.Hkv;
                 Line line;
-                line.init(p.prefix[B] * p.Hkv, p.prefix[B + 1]);
+                line.T = p.prefix[B] * p.Hkv;
+                line.P = p.prefix[B + 1];
                 cnt = paged_partial_slots(p, p.prefix, line, it.b, it.head * p.chunks + it.chunk, slots, kMaxPartsD);
             }
             cnt = __shfl_sync(0xffffffffu, cnt, 0);
