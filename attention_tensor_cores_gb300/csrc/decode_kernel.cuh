@@ -1027,90 +1027,90 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
     // Each setmaxnreg dominates only its own role's code and is executed by whole warpgroups.
     if (warp >= tma_warp<EPI>()) {
         if constexpr (EPI) setmaxnreg_dec<kRegsCtl>();
-      if (warp == tma_warp<EPI>()) {
-        // ------------------------------------------------ TMA producer
+      if (PAGED && (warp == tma_warp<EPI>() || warp == tma_warp<EPI>() + 2)) {
+        // ------------------------------------------------ paged TMA producers: one warp for K, one for Q and V
+        // A tile is filled in boxes of p.box keys, each inside one page, up to the request's length (rows behind
+        // it keep what the buffer held: their scores are masked and their V rows zeroed).  Lane i of the warp
+        // looks up the page of box i, a tile ahead (up to four ahead measured the same or slower), and issues
+        // it.  A page outside the pool loads zeros (the tensor map's fill) and sets the status.  A box takes
+        // its warp some 100 cycles, whoever issues it (one elected thread: twice that), hence two warps: in pages
+        // of 16, B1 500 keys 9.2 -> 8.0 us, B8 Hkv16 0..2000 keys D64 19.8 -> 16.0.
         if constexpr (PAGED) {
-            // A tile is filled in boxes of p.box keys, each inside one page, up to the request's length (rows
-            // behind it keep what the buffer held: their scores are masked and their V rows zeroed).  Lane i
-            // of the warp looks up the page of box i, a tile ahead (up to four ahead measured the same or slower),
-            // and issues it, for K and for V.  A page outside the pool loads zeros (the tensor map's fill) and
-            // sets the status.  One elected thread issuing every box measured 25 % slower than a lane per box.
-            const int lane = static_cast<int>(lane_id());
-            const uint64_t pol = policy_evict_first();
-            Ring qr(2), kr(S), vr(S);
-            uint32_t kcnt[S], vcnt[S], qcnt[2] = {0, 0};
-            for (int i = 0; i < S; ++i) kcnt[i] = vcnt[i] = 0;
-            const int i = lane, boxes = kTileKV >> p.box_log2;
             using L = TileLayout<D, PAGED>;
-            auto load_box = [&](uint8_t* tile, const CUtensorMap* map, uint64_t* bar, int page, int off, int head) {
-                uint8_t* dst = tile + i * (p.box / 8) * L::kGroup;
-                if constexpr (L::kInter)
-                    tma_load_5d_hint(dst, map, bar, 0, 0, 0, page * p.groups + off / 8, head, pol);
-                else
-                    tma_load_4d_hint(dst, map, bar, 0, off, head, page, pol);
-            };
+            const int lane = static_cast<int>(lane_id()), boxes = kTileKV >> p.box_log2;
+            const bool is_k = warp == tma_warp<EPI>();
+            const CUtensorMap* map = is_k ? &kmap : &vmap;
+            uint64_t *full = is_k ? k_full : v_full, *empty = is_k ? k_empty : v_empty;
+            uint8_t* ring = smem + (is_k ? C::kOffK : C::kOffV);
+            const uint64_t pol = policy_evict_first();
+            Ring qr(2), r(S);
+            uint32_t cnt[S], qcnt[2] = {0, 0};
+            for (int n = 0; n < S; ++n) cnt[n] = 0;
             // lane 0 waits for the buffer and announces `bytes`; the warp goes on unless the CTA has aborted
-            auto claim = [&](uint64_t* empty, uint64_t* full, uint32_t phase, uint32_t bytes) {
+            auto claim = [&](uint64_t* free, uint64_t* filled, uint32_t phase, uint32_t bytes) {
                 int go = 0;
                 if (lane == 0) {
-                    mbar_wait(empty, phase ^ 1, wc);
+                    mbar_wait(free, phase ^ 1, wc);
                     go = aborted(wc) ? 0 : 1;
-                    if (go) mbar_arrive_expect_tx(full, bytes);
+                    if (go) mbar_arrive_expect_tx(filled, bytes);
                 }
                 return __shfl_sync(0xffffffffu, go, 0) != 0;
             };
             while (sched.next(it)) {
                 if (it.t1 <= it.t0) continue;
-                const int head = it.head;
                 const int32_t* row = p.table + static_cast<size_t>(it.b) * p.max_pages;
-                // this lane's box of tile t starts at key first_key(t); its page is looked up a tile ahead
-                auto first_key = [&](int t) { return t * kTileKV + i * p.box; };
+                // this lane's box of tile t starts at key first_key(t)
+                auto first_key = [&](int t) { return t * kTileKV + lane * p.box; };
                 auto look_up = [&](int t) {
                     const int j = first_key(t);
-                    return t < it.t1 && i < boxes && j < it.n ? row[p.by_page.div(j)] : 0;
+                    return t < it.t1 && lane < boxes && j < it.n ? row[p.by_page.div(j)] : 0;
                 };
                 int next_page = look_up(it.t0);
-                if (claim(&q_empty[qr.idx], &q_full[qr.idx], qr.phase, C::kQBytes)) {
-                    if (lane < C::kAtoms)
-                        tma_load_3d(smem + C::kOffQ + qr.idx * C::kQBytes + lane * (kN * 128), &qmap, &q_full[qr.idx], lane * 64,
-                                    it.chunk * p.G, it.b * (p.Hkv / p.chunks) + head);
-                    ++qcnt[qr.idx];
+                if (!is_k) {
+                    if (claim(&q_empty[qr.idx], &q_full[qr.idx], qr.phase, C::kQBytes)) {
+                        if (lane < C::kAtoms)
+                            tma_load_3d(smem + C::kOffQ + qr.idx * C::kQBytes + lane * (kN * 128), &qmap, &q_full[qr.idx], lane * 64,
+                                        it.chunk * p.G, it.b * (p.Hkv / p.chunks) + it.head);
+                        ++qcnt[qr.idx];
+                    }
+                    qr.advance();
                 }
-                qr.advance();
                 for (int t = it.t0; t < it.t1; ++t) {
                     int page = next_page;
                     next_page = look_up(t + 1);
                     const int j = first_key(t), off = j - p.by_page.div(j) * p.page;
-                    const bool mine = i < boxes && j < it.n;
+                    const bool mine = lane < boxes && j < it.n;
                     if (mine && (page < 0 || page >= p.num_pages)) {
                         page = p.num_pages;
                         atomicExch(p.status, kDevBadPage);
                     }
                     const int used = (min(it.n - t * kTileKV, kTileKV) + p.box - 1) >> p.box_log2;
                     const uint32_t bytes = static_cast<uint32_t>((used << p.box_log2) * 128 * C::kAtoms);
-                    if (claim(&k_empty[kr.idx], &k_full[kr.idx], kr.phase, bytes)) {
-                        if (mine) load_box(smem + C::kOffK + kr.idx * C::kKVBytes, &kmap, &k_full[kr.idx], page, off, head);
-                        ++kcnt[kr.idx];
+                    if (claim(&empty[r.idx], &full[r.idx], r.phase, bytes)) {
+                        if (mine) {
+                            uint8_t* dst = ring + r.idx * C::kKVBytes + lane * (p.box / 8) * L::kGroup;
+                            if constexpr (L::kInter)
+                                tma_load_5d_hint(dst, map, &full[r.idx], 0, 0, 0, page * p.groups + off / 8, it.head, pol);
+                            else
+                                tma_load_4d_hint(dst, map, &full[r.idx], 0, off, it.head, page, pol);
+                        }
+                        ++cnt[r.idx];
                     }
-                    kr.advance();
-                    if (claim(&v_empty[vr.idx], &v_full[vr.idx], vr.phase, bytes)) {
-                        if (mine) load_box(smem + C::kOffV + vr.idx * C::kKVBytes, &vmap, &v_full[vr.idx], page, off, head);
-                        ++vcnt[vr.idx];
-                    }
-                    vr.advance();
+                    r.advance();
                 }
             }
             // nothing may still be landing in shared memory when the CTA exits
             if (lane == 0) {
-                for (int n = 0; n < S; ++n) {
-                    if (kcnt[n]) drain_wait(&k_full[n], (kcnt[n] - 1) & 1, kDrainLimit);
-                    if (vcnt[n]) drain_wait(&v_full[n], (vcnt[n] - 1) & 1, kDrainLimit);
-                }
+                for (int n = 0; n < S; ++n)
+                    if (cnt[n]) drain_wait(&full[n], (cnt[n] - 1) & 1, kDrainLimit);
                 for (int n = 0; n < 2; ++n)
                     if (qcnt[n]) drain_wait(&q_full[n], (qcnt[n] - 1) & 1, kDrainLimit);
             }
             __syncwarp();
-        } else if (lane_id() == 0) {
+        }
+      } else if (!PAGED && warp == tma_warp<EPI>()) {
+        // ------------------------------------------------ TMA producer
+        if (lane_id() == 0) {
             tma_prefetch_desc(&qmap);
             tma_prefetch_desc(&kmap);
             tma_prefetch_desc(&vmap);
