@@ -28,8 +28,8 @@
 //  * Paged keys and values (PAGED): the producer gathers a tile page by page (see the producer), and
 //    the work split comes from the requests' lengths inside the kernel (see Line).
 //  * Roles (decode_kernel<D, CAUSAL, NC, PAGED>): warps 0-3 softmax.  EPI (see
-//    has_epilogue_warps): warps 4-7 epilogue, warp 8 TMA producer, warp 9 MMA issuer, warps 10-11 only complete
-//    their warpgroup; at the end of a work item the softmax warps hand its accumulators to the
+//    has_epilogue_warps): warps 4-7 epilogue, warp 8 TMA producer, warp 9 MMA issuer, warp 10 the second
+//    producer of paged tiles, the rest only completes its warpgroup; at the end of a work item the softmax warps hand its accumulators to the
 //    epilogue warps (Tensor Memory, two buffers) and go on with the next item while the epilogue
 //    normalises, stores and merges.  !EPI: warp 4 producer, warp 5 MMA, and the softmax
 //    warps run each item's short epilogue themselves.  Every wait is bounded; a timeout flips the
