@@ -7,7 +7,12 @@
 // Queries go to q_out, keys and values to the token's slot of the cache; values are copied.  Everything is
 // FP32 from the BF16 inputs to the one rounding of each output.
 //
-// Bound: HBM (every element read once and written once; a decoding step is latency-bound).
+// Bound: HBM (every element read once and written once; a decoding step is latency-bound).  A CTA's life is
+// two dependent DRAM accesses (slot and position, then angles; the heads beside them) and little arithmetic, so
+// occupancy and loads in flight set the rate.  8192 tokens, 32 + 8 + 8 heads of 128, norm and rotation: 34.8 us,
+// 5.8 TB/s = 0.87 of the copy bandwidth.  On the way there: one head per group of threads 55.7 us; four heads in
+// flight 48; the weights drawn into the angles, packed FP32 and five CTAs per SM 38.3 (four 41.5, six with
+// spills 43); the next heads fetched into L2 34.8.  8 tokens: 2.1 us of GPU time.
 #include <cuda_runtime.h>
 
 #include "fastdiv.cuh"
@@ -16,6 +21,8 @@
 
 namespace atc_gb300 {
 namespace {
+
+constexpr int kThreads = 128, kCtas = 5;   // per CTA, and CTAs per SM that the registers allow
 
 struct AppendParams {
     const uint16_t *q, *k, *v;
@@ -33,6 +40,7 @@ struct AppendParams {
     int T, Hq, Hkv, Sq;
     int* status;
     int q_sets, kv_sets;               // sets of heads of a token, of queries and of keys (or values)
+    int ahead;                         // tokens between one and the one whose heads are fetched into L2 with it
     FastDiv by_sets, by_page, by_sq;   // all of a token's sets, page and Sq
 };
 
@@ -91,7 +99,7 @@ __device__ __forceinline__ uint64_t swap2(uint64_t v)
 //   y_i = (x_i (w_i c) + x_j (-w_j s)) / rms     y_j = (x_j (w_j c) + x_i (w_i s)) / rms
 // three packed operations for two outputs.
 template <int D, bool PAIRS, int HEADS>
-__global__ void __launch_bounds__(128, 5) rope_append_kernel(const __grid_constant__ AppendParams p)
+__global__ void __launch_bounds__(kThreads, kCtas) rope_append_kernel(const __grid_constant__ AppendParams p)
 {
     constexpr int L = D / 16;   // threads per head
     griddep_launch_dependents();
@@ -108,7 +116,8 @@ __global__ void __launch_bounds__(128, 5) rope_append_kernel(const __grid_consta
     const int heads = min(HEADS, (kind == 0 ? p.Hq : p.Hkv) - h0);
     const Runs r = kind == 2 ? Runs{16 * l, 16 * l + 8} : runs_of<PAIRS>(l, p.R);
 
-    const uint16_t* x = (kind == 0 ? p.q + t * p.q_stride : kind == 1 ? p.k + t * p.k_stride : p.v + t * p.v_stride) + h0 * D;
+    const int64_t stride = kind == 0 ? p.q_stride : kind == 1 ? p.k_stride : p.v_stride;
+    const uint16_t* x = (kind == 0 ? p.q : kind == 1 ? p.k : p.v) + t * stride + h0 * D;
     uint4 u[HEADS][2];
 #pragma unroll
     for (int k = 0; k < HEADS; ++k)
@@ -116,6 +125,9 @@ __global__ void __launch_bounds__(128, 5) rope_append_kernel(const __grid_consta
             u[k][0] = *reinterpret_cast<const uint4*>(x + k * D + r.a);
             u[k][1] = *reinterpret_cast<const uint4*>(x + k * D + r.b);
         }
+    // the same heads of a token that a later CTA takes: into L2 meanwhile, a line per thread
+    if (HEADS > 1 && t + p.ahead < p.T && l * 64 < heads * D)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(x + p.ahead * stride + l * 64));
 
     if (slot < 0) return;
     if (slot >= p.num_slots || (p.R && (pos < 0 || pos >= p.max_pos))) {
@@ -229,8 +241,9 @@ int launch_append(AppendParams& p, cudaStream_t st)
     p.kv_sets = (p.Hkv + HEADS - 1) / HEADS;
     const int sets = p.q_sets + 2 * p.kv_sets;
     p.by_sets = FastDiv(static_cast<uint32_t>(sets));
+    p.ahead = num_sms() * kCtas * kThreads / (D / 16) / sets / 2 + 1;   // half of what the GPU holds
     const long long threads = static_cast<long long>(p.T) * sets * (D / 16);
-    FMHA_CHECK_CUDA(launch_pdl(rope_append_kernel<D, PAIRS, HEADS>, dim3(static_cast<unsigned>((threads + 127) / 128)), dim3(128), 0, st, p));
+    FMHA_CHECK_CUDA(launch_pdl(rope_append_kernel<D, PAIRS, HEADS>, dim3(static_cast<unsigned>((threads + kThreads - 1) / kThreads)), dim3(kThreads), 0, st, p));
     count_launch();
     return FMHA_OK;
 }
