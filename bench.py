@@ -34,16 +34,16 @@ FALLBACK_PEAKS = {"hbm_gbs": 6800.0, "bf16_tflops": 1900.0, "bf16_tflops_sustain
 # named kernel, with the sha256 of its source file and the shared device headers at capture time;
 # reported only while those sources are unchanged.
 TRAFFIC = {
-    # decode B8 H32 Sq1 Skv4096 D128 (decode_kernel<128, 0, 0>, 128 CTAs of two whole units): read
-    # 537,030,656 + written 2,818,304 bytes (profiles/decode_kernel_decode-B8-H32-Skv4096-D128.md)
-    "decode_kernel<128>": {"bytes": 539848960, "source_sha": "352c1ba17c15bf38"},
-    # ragged GQA decode B64 Hq32 Hkv8 Skv<=32768 D128 (decode_kernel<128, 0, 1>): the quarter-size workload
-    # (B16) read 1,005,865,216 + wrote 683,008 bytes for 1,001,226,240 algorithmic K/V bytes (1.005x); scaled
+    # decode B8 H32 Sq1 Skv4096 D128 (decode_kernel<128, 0, 1, 0>, 128 CTAs of two whole units): read
+    # 537,027,840 + written 2,855,424 bytes (profiles/decode_kernel_decode-B8-H32-Skv4096-D128.md)
+    "decode_kernel<128>": {"bytes": 539883264, "source_sha": "3712435e1c3e23dd"},
+    # ragged GQA decode B64 Hq32 Hkv8 Skv<=32768 D128 (decode_kernel<128, 0, 4, 0>): the quarter-size workload
+    # (B16) read 1,005,849,344 + wrote 394,240 bytes for 1,001,226,240 algorithmic K/V bytes (1.005x); scaled
     # by the K/V bytes to the full workload's 4,106,002,432 (profiles/side-kernels_ragged-decode-wide-combine-nvfp4.md)
-    "decode_kernel<128>/ragged": {"bytes": 4127827748, "source_sha": "352c1ba17c15bf38"},
-    # speculative decode B8 Hq32 Hkv8 Sq4 Skv8192 D128, causal (decode_kernel<128, 1, 1>): read 268,839,424 +
-    # written 2,847,232 bytes (profiles/decode_kernel_decode-B8-H32-Skv4096-D128.md)
-    "decode_kernel<128>/speculative": {"bytes": 271686656, "source_sha": "352c1ba17c15bf38"},
+    "decode_kernel<128>/ragged": {"bytes": 4126578428, "source_sha": "3712435e1c3e23dd"},
+    # speculative decode B8 Hq32 Hkv8 Sq4 Skv8192 D128, causal (decode_kernel<128, 1, 16, 0>): read 268,812,288 +
+    # written 3,061,504 bytes (profiles/decode_kernel_decode-B8-H32-Skv4096-D128.md)
+    "decode_kernel<128>/speculative": {"bytes": 271873792, "source_sha": "3712435e1c3e23dd"},
     # wide-head B32 Hq128 Hkv1 Skv16384 D512, independent CTAs: read 1,081,726,464 + written 10,248,960
     # bytes (profiles/wide_kernel_wide-head-B32-Hq128-Hkv1-Skv16384-D512.md)
     "wide_kernel<independent>": {"bytes": 1091975424, "source_sha": "78a9a91c90649bc2"},
@@ -481,9 +481,9 @@ def _workload_entry(F, w, idx, steps, warmup, peaks, causal=False, given_scale=F
         if w.D == 512:
             traffic = traffic_for("wide_kernel<pair>" if wide_variant == 2 else "wide_kernel<independent>", "wide.cu")
         elif w.ragged and not causal and not given_scale:
-            traffic = traffic_for("decode_kernel<128>/ragged", "decode.cu")
+            traffic = traffic_for("decode_kernel<128>/ragged", "decode_kernel.cuh")
         elif causal and w.Sq == 4 and w.Skv == 8192 and w.B == 8:
-            traffic = traffic_for("decode_kernel<128>/speculative", "decode.cu")
+            traffic = traffic_for("decode_kernel<128>/speculative", "decode_kernel.cuh")
         else:
             traffic = None
         roof = hbm_roofline(ach, peaks, read_peak)
@@ -552,7 +552,7 @@ def run_ours(args, rank, world, local):
     kern_ms = statistics.mean(r["kernel_ms"])
     achieved = head.algorithmic_bytes() / (kern_ms / 1e3) / 1e9
     roof = hbm_roofline(achieved, peaks, read_peak)
-    roof.update({"traffic": traffic_for("decode_kernel<128>", "decode.cu"),
+    roof.update({"traffic": traffic_for("decode_kernel<128>", "decode_kernel.cuh"),
                  "kernel": "decode_kernel<128>", "kernel_ms": kern_ms, "algorithmic_bytes": head.algorithmic_bytes(),
                  "kernel_events": f"CUDA events around {len(r['kernel_ms'])} of the {args.steps} timed calls "
                                   f"(one in {KERNEL_EVENT_EVERY})",
