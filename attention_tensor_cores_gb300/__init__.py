@@ -1,6 +1,7 @@
 """GB300 (sm_103a) fused multi-head attention: Python binding of libfmha.so.
 
-Thin ctypes marshalling only: every step of attention, split-KV combine and NVFP4 quantisation
+Thin marshalling only (ctypes; the paged cache's entry points through the native _binding.so, whose
+checks and calls take a microsecond): every step of attention, split-KV combine and NVFP4 quantisation
 runs in the library's CUDA kernels.  torch tensors supply device memory and the current stream.
 There is no CPU path: if libfmha.so is missing or cannot load, every call raises.
 

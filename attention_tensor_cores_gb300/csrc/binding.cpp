@@ -238,9 +238,10 @@ PyObject* rope_append(PyObject* self, PyObject* const* a, Py_ssize_t n)
         const float eps = number(a[5]);
         const int pairs = PyObject_IsTrue(a[11]);
         if (pairs < 0) throw std::exception();
+        const auto step = [T](const at::Tensor& t) { return T > 1 ? t.stride(0) : 0; };   // of one token, torch may say anything
         const fmha_stream_t st = stream_of(a[12], dev);
         return result(unlocked([&] {
-                          return lib.rope_append(q.data_ptr(), q.stride(0), k.data_ptr(), k.stride(0), v.data_ptr(), v.stride(0), w[0], w[1], eps,
+                          return lib.rope_append(q.data_ptr(), step(q), k.data_ptr(), step(k), v.data_ptr(), step(v), w[0], w[1], eps,
                                                  cos_sin, static_cast<int>(max_pos), static_cast<int>(R), pairs, positions,
                                                  data<int64_t>(slots), out.data_ptr(), &cache, static_cast<int>(T), static_cast<int>(Hq),
                                                  static_cast<int>(Sq), st);

@@ -233,7 +233,9 @@ using namespace atc_gb300;
 
 extern "C" size_t fmha_paged_workspace_size(int B, int Hq, int Sq, const fmha_kv_cache* cache, const fmha_opts* opts)
 {
-    if (!cache || cache->Hkv < 1 || B < 0 || Hq <= 0 || Sq < 0 || Hq % cache->Hkv || (cache->D != 64 && cache->D != 128)) return 0;
+    if (!cache || cache->Hkv < 1 || B < 0 || Hq <= 0 || Sq < 0 || Hq % cache->Hkv || (cache->D != 64 && cache->D != 128) ||
+        static_cast<long long>(B) * Hq * Sq >= (1LL << 31))
+        return 0;
     return paged_ws(B, Hq, Sq, cache, opts).total;
 }
 

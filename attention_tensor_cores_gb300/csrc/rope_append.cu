@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) rope_append_kernel(const __gr
         step = static_cast<int64_t>(p.Sq) * D;
         y = p.q_out + (static_cast<int64_t>(n) * p.Hq + h0) * step + (t - n * p.Sq) * D;
     } else {
-        const int64_t page = p.num_slots < (1LL << 31) ? p.by_page.div(static_cast<int>(slot)) : slot / p.page;
+        const int64_t page = p.by_page.div(static_cast<int>(slot));
         step = p.head_stride;
         y = (kind == 1 ? p.kc : p.vc) + page * p.page_stride + (slot - page * p.page) * p.token_stride + h0 * step;
     }

@@ -204,7 +204,7 @@ int nvfp4_quantize_scaled(const float* x, uint8_t* q, uint8_t* scales, int64_t n
 typedef struct {
     void* k;              /* device BF16 pools, 16-byte aligned */
     void* v;
-    int num_pages;        /* >= 1 */
+    int num_pages;        /* >= 1; num_pages * page_size below 2^31 */
     int page_size;        /* tokens per page, >= 1 (fmha_fwd_paged: a multiple of 8) */
     int Hkv;              /* key/value heads */
     int D;                /* 64 or 128 */

@@ -111,6 +111,14 @@ def test_far_positions():
     case(9, 4, 2, 64, 64, False, True, True, 16, "hnd", max_pos=200001)
 
 
+def test_one_token_of_any_stride():
+    x = torch.ones(1, 2, 64, dtype=torch.bfloat16, device="cuda").as_strided((1, 2, 64), (3, 64, 1))
+    kp, vp = make_pools(1, 2, 16, 64, "hnd", fill=0.0)
+    out = torch.zeros(1, 2, 64, dtype=torch.bfloat16, device="cuda")
+    F.fmha_rope_append(x, x, x, None, None, EPS, None, None, torch.tensor([5], device="cuda"), out, F.make_kv_cache(kp, vp))
+    assert F.fmha_check_status() == 0 and (out == 1).all() and (kp[0, :, 5] == 1).all() and (vp[0, :, 5] == 1).all()
+
+
 def test_no_tokens():
     case(0, 4, 2, 64, 64, False, True, True, 16, "hnd")
 

@@ -26,7 +26,7 @@ def cache(**kw):
 
 BAD_CACHES = [(dict(k=None), F.FMHA_ERR_INVALID), (dict(v=None), F.FMHA_ERR_INVALID), (dict(k=B8), F.FMHA_ERR_INVALID),
               (dict(num_pages=0), F.FMHA_ERR_INVALID), (dict(page_size=0), F.FMHA_ERR_INVALID), (dict(Hkv=0), F.FMHA_ERR_INVALID),
-              (dict(D=96), F.FMHA_ERR_UNSUPPORTED), (dict(D=512), F.FMHA_ERR_UNSUPPORTED), (dict(token_stride=60), F.FMHA_ERR_INVALID),
+              (dict(num_pages=1 << 27), F.FMHA_ERR_UNSUPPORTED), (dict(D=96), F.FMHA_ERR_UNSUPPORTED), (dict(D=512), F.FMHA_ERR_UNSUPPORTED), (dict(token_stride=60), F.FMHA_ERR_INVALID),
               (dict(token_stride=56), F.FMHA_ERR_INVALID), (dict(head_stride=-1024), F.FMHA_ERR_INVALID),
               (dict(page_stride=1 << 38), F.FMHA_ERR_INVALID)]
 
@@ -52,7 +52,8 @@ def test_cache_descriptor(lib, bad, code):
     (dict(q=None), 1), (dict(table=None), 1), (dict(lens=None), 1), (dict(out=None), 1), (dict(q=B8), 1), (dict(out=B8), 1),
     (dict(table=0x10002), 1), (dict(lens=0x10001), 1), (dict(lse=0x10002), 1), (dict(B=-1), 1), (dict(Sq=-1), 1), (dict(Hq=3), 1),
     (dict(Hq=0), 1), (dict(pages=0), 1), (dict(scale=0.0), 1), (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1),
-    (dict(c=cache(page_size=12)), 2), (dict(c=cache(page_size=4)), 2), (dict(pages=1 << 28), 2), (dict(B=1 << 30), 2),
+    (dict(c=cache(D=128, token_stride=128, head_stride=2048, page_stride=4608)), 2),
+    (dict(c=cache(D=128, token_stride=128, head_stride=2048, page_stride=1024)), 2), (dict(c=cache(page_size=12)), 2), (dict(c=cache(page_size=4)), 2), (dict(pages=1 << 28), 2), (dict(B=1 << 30), 2),
     (dict(opts=opts(out_kind=7)), 1), (dict(opts=opts(num_splits=-1)), 1), (dict(opts=opts(seqlens_k=A)), 1),
     (dict(opts=opts(out_kind=2)), 1), (dict(opts=opts(workspace=0x10010, workspace_bytes=1 << 20)), 1)])
 def test_paged_attention(lib, bad, code):
@@ -69,6 +70,7 @@ def test_paged_workspace_size(lib):
     assert lib.fmha_paged_workspace_size(2, 4, 1, c, opts(num_splits=1, out_kind=2)) > 0
     assert lib.fmha_paged_workspace_size(2, 3, 1, c, None) == 0
     assert lib.fmha_paged_workspace_size(2, 4, 1, None, None) == 0
+    assert lib.fmha_paged_workspace_size(1 << 29, 4, 1, c, opts()) == 0
     # more than 16 rows per key/value head: chunks of rows, each with partials of its own
     assert lib.fmha_paged_workspace_size(2, 64, 1, c, opts()) > lib.fmha_paged_workspace_size(2, 32, 1, c, opts())
 
