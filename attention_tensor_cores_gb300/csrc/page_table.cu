@@ -16,8 +16,8 @@
 //
 // Bound: launch latency and a chain of dependent loads (lengths, table or stack entry) for a decoding
 // step; 12 bytes written per token for prompts.  GPU time (without requests 1.8 us): 8 requests of a token 3.1 us,
-// 256 requests of which 32 end 5.5 (one CTA 7.2), 32 prompts of 131,000 tokens 5.9 (one CTA and an item at a
-// time 120; a cluster of eight CTAs 19).
+// 256 requests of which 32 end 4.8 (one CTA 7.2), 32 prompts of 131,000 tokens 4.6 (one CTA 120, a cluster of
+// eight 19).
 #include <cuda_runtime.h>
 
 #include "fastdiv.cuh"
@@ -99,8 +99,6 @@ __device__ __forceinline__ Sums request(const PageTableParams& p, int c, int a, 
     return r;
 }
 
-// RUN: tokens (and pages) a lane takes of 32 * RUN consecutive ones of its warp, their loads in flight together
-template <int RUN>
 __global__ void __launch_bounds__(1024) page_table_kernel(const __grid_constant__ PageTableParams p)
 {
     extern __shared__ int sh[];
@@ -183,43 +181,31 @@ __global__ void __launch_bounds__(1024) page_table_kernel(const __grid_constant_
     const auto fine = [&](int page) { return page >= 0 && page < p.num_pages; };
 
     if (p.parts & kTables) {
-        // a warp's 32 * RUN consecutive tokens, pages taken and pages given back, lane by lane: first all their
-        // pages are looked up, then all is written
+        // a token, a page taken and a page given back at a time: first all three are looked up, then written
         const int most = max(max(p.T, taken_n), given_n);
-        for (int x0 = (first & ~31) * RUN + lane; x0 < most; x0 += step * RUN) {
-            int pos[RUN], page[RUN], at[RUN], new_page[RUN], old_page[RUN];
-            int bt = x0 < tokens ? owner(s_cu, B, p.top, x0) : 0, ba = x0 < taken_n ? owner(s_aoff, B, p.top, x0) : 0;
-#pragma unroll
-            for (int k = 0; k < RUN; ++k) {
-                const int x = x0 + 32 * k;
-                pos[k] = page[k] = at[k] = new_page[k] = old_page[k] = 0;
-                if (x < tokens) {
-                    while (bt + 1 < B && s_cu[bt + 1] <= x) ++bt;
-                    pos[k] = s_ctx[bt] + (x - s_cu[bt]);
-                    const int i = p.by_page.div(pos[k]), held = p.by_page.up(s_ctx[bt]);
-                    page[k] = *(i < held ? row(bt) + i : taken(s_aoff[bt] + i - held));
-                }
-                if (x < taken_n) {
-                    while (ba + 1 < B && s_aoff[ba + 1] <= x) ++ba;
-                    at[k] = ba;
-                    new_page[k] = *taken(x);
-                }
-                if (x < given_n) old_page[k] = *given(x);
+        for (int x = first; x < most; x += step) {
+            int pos = 0, page = 0, to = 0, new_page = 0, old_page = 0;
+            if (x < tokens) {
+                const int b = owner(s_cu, B, p.top, x);
+                pos = s_ctx[b] + (x - s_cu[b]);
+                const int i = p.by_page.div(pos), held = p.by_page.up(s_ctx[b]);
+                page = *(i < held ? row(b) + i : taken(s_aoff[b] + i - held));
             }
-#pragma unroll
-            for (int k = 0; k < RUN; ++k) {
-                const int x = x0 + 32 * k;
-                if (x < p.T) {
-                    const bool ok = x < tokens && fine(page[k]);
-                    if (x < tokens && !ok) atomicExch(p.status, kDevBadPage);
-                    p.positions[x] = pos[k];
-                    p.slots[x] = ok ? static_cast<long long>(page[k]) * P + (pos[k] - p.by_page.div(pos[k]) * P) : -1;
-                }
-                if (x < taken_n) row(at[k])[p.by_page.up(s_ctx[at[k]]) + (x - s_aoff[at[k]])] = new_page[k];
-                if (x < given_n) {
-                    p.free_pages[n + x] = old_page[k];
-                    if (!fine(old_page[k])) atomicExch(p.status, kDevBadPage);
-                }
+            if (x < taken_n) {
+                to = owner(s_aoff, B, p.top, x);
+                new_page = *taken(x);
+            }
+            if (x < given_n) old_page = *given(x);
+            if (x < p.T) {
+                const bool ok = x < tokens && fine(page);
+                if (x < tokens && !ok) atomicExch(p.status, kDevBadPage);
+                p.positions[x] = pos;
+                p.slots[x] = ok ? static_cast<long long>(page) * P + (pos - p.by_page.div(pos) * P) : -1;
+            }
+            if (x < taken_n) row(to)[p.by_page.up(s_ctx[to]) + (x - s_aoff[to])] = new_page;
+            if (x < given_n) {
+                p.free_pages[n + x] = old_page;
+                if (!fine(old_page)) atomicExch(p.status, kDevBadPage);
             }
         }
         for (int b = first; b <= B; b += step) p.cu[b] = b < B ? s_cu[b] : tokens;
@@ -233,12 +219,11 @@ __global__ void __launch_bounds__(1024) page_table_kernel(const __grid_constant_
     }
 }
 
-template <int RUN>
 int launch_table(PageTableParams& p, int parts, int ctas, int threads, cudaStream_t st)
 {
     p.parts = parts;
-    FMHA_CHECK_CUDA(set_smem_limit_once(reinterpret_cast<const void*>(page_table_kernel<RUN>), kMaxRequests * 16));
-    FMHA_CHECK_CUDA(launch_pdl(page_table_kernel<RUN>, dim3(static_cast<unsigned>(ctas)), dim3(static_cast<unsigned>(threads)),
+    FMHA_CHECK_CUDA(set_smem_limit_once(reinterpret_cast<const void*>(page_table_kernel), kMaxRequests * 16));
+    FMHA_CHECK_CUDA(launch_pdl(page_table_kernel, dim3(static_cast<unsigned>(ctas)), dim3(static_cast<unsigned>(threads)),
                                static_cast<size_t>(p.B) * 16, st, p));
     count_launch();
     return FMHA_OK;
@@ -272,15 +257,16 @@ extern "C" int fmha_page_table(const int32_t* ctx_lens, const int32_t* new_lens,
                       positions, slots, T, free_count_out, status, FastDiv(static_cast<uint32_t>(page_size)), 0, 0};
     while ((p.top ? 2 * p.top : 1) < B) p.top = p.top ? 2 * p.top : 1;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    // Up to 2048 tokens a lane takes one item, beyond that four at once.  Enough CTAs for the tokens and, as
-    // requests that end give back many pages, eight items per request; all of them sum the lengths.  An update
-    // in place has one CTA, or beyond 2048 tokens or requests a launch of its own after the others have read.
+    // An item per thread: the tokens, or, as requests that end give back many pages, 32 per request (8: 32
+    // requests 5.0 us against 4.1, 256 5.4 / 4.8).  Every CTA sums the lengths, so many requests take larger and
+    // fewer ones (1024 requests with 256, 512, 1024 threads 6.5, 6.2, 7.1; 4096 45, 13.4, 9.8).  An update in
+    // place has one CTA, or beyond 2048 tokens or requests a launch of its own after the others have read.
+    // (Four items per thread, their loads in flight together: 131,000 tokens 5.9 against 4.6.)
     const bool in_place = seqlens == ctx_lens || free_count_out == free_count;
     const int most = T > B ? T : B;
-    if (in_place && most <= 2048) return launch_table<1>(p, kTables | kLengths, 1, most <= 256 ? 256 : 1024, st);
-    const int parts = in_place ? kTables : kTables | kLengths, limit = 4 * num_sms();
-    const int items = T <= 2048 ? (T > 8 * B ? T : 8 * B) : (T > 8 * B ? T : 8 * B) / 4;
-    const int ctas = items <= 256 ? 1 : (items + 255) / 256 < limit ? (items + 255) / 256 : limit;
-    const int rc = T <= 2048 ? launch_table<1>(p, parts, ctas, 256, st) : launch_table<4>(p, parts, ctas, 256, st);
-    return rc || !in_place ? rc : launch_table<1>(p, kLengths, 1, 1024, st);
+    if (in_place && most <= 2048) return launch_table(p, kTables | kLengths, 1, most <= 256 ? 256 : 1024, st);
+    const int threads = B > 2048 ? 1024 : B > 512 ? 512 : 256, items = T > 32 * B ? T : 32 * B, want = (items + threads - 1) / threads;
+    const int limit = 1024 / threads * num_sms();
+    const int rc = launch_table(p, in_place ? kTables : kTables | kLengths, want < 1 ? 1 : want < limit ? want : limit, threads, st);
+    return rc || !in_place ? rc : launch_table(p, kLengths, 1, 1024, st);
 }
