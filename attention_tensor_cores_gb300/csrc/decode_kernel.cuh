@@ -96,6 +96,8 @@ struct DecodeCfg {
     static constexpr int kOffV = kOffK + kStages * kKVBytes;
     static constexpr int kOffP = kOffV + kStages * kKVBytes;
     static constexpr int kSmemBytes = kOffP + 2 * kPBytes + 1024;   // + alignment slack
+    // paged, 16 columns: two more P buffers behind the first two (see store_p)
+    static constexpr int smem_bytes(int nc, bool paged) { return kSmemBytes + (paged && nc == 16 ? 2 * kPBytes : 0); }
     static constexpr uint32_t kTmemCols = 128;             // S[2] x 16, O[2] x 16, handoff[2] x 32
 };
 
@@ -162,7 +164,8 @@ struct Item {
 // Paged work split.  The line of T tiles (below 2^31) is cut for P CTAs at c T / P, P as many as leave each
 // kMinPiece tiles or as there are units with keys; a cut less than kMinPiece tiles from an end of its unit moves
 // there.  A piece of a unit costs its publication and a share of the merge, several tiles' time, so short units
-// stay whole.
+// stay whole.  With 2, 4 and 6 tiles at least (Hq32 Hkv8 D128): B1 500 keys 10.1, 8.1 and 8.1 us, B1 2000 13.6,
+// 12.6 and 16.4, B8 0..1000 11.7, 11.5 and 13.4, B1 8000 19.6, 18.4 and 17.3, B16 Hkv1 0..4000 17.5, 15.1 and 16.3.
 constexpr int kMinPiece = 4;
 
 struct Line {
@@ -357,23 +360,41 @@ __device__ __forceinline__ uint64_t sdesc_sw32(uint32_t saddr, uint32_t sbo_byte
     return d;
 }
 
-// Row `key` of P^T, rounded to BF16 (the operand type of the MMA; half a step, 2^-9 to 2^-8 of a weight)
-template <int NC>
-__device__ __forceinline__ void store_p(uint8_t* sP, int key, const float (&pv)[NC])
+// Row `key` of P^T, rounded to BF16 (the operand type of the MMA; half a step, 2^-9 to 2^-8 of a weight).  TWO
+// (paged): what the rounding leaves goes along as a second BF16, so that P is good to 2^-17 and the output's
+// own rounding is the only one that shows (rms error of BF16 outputs 1.7e-3 of them instead of 2.3e-3).  Up to eight
+// columns it takes the other eight of the 16 (columns 8 ..) and no time that shows, with 16 a second buffer, `low`,
+// and a second MMA (B17 Hq16 Hkv4 Sq4 D64, up to 5001 keys: 21.2 us instead of 20.0).
+template <int NC, bool TWO>
+__device__ __forceinline__ void store_p(uint8_t* sP, uint8_t* low, int key, const float (&pv)[NC])
 {
-    uint8_t* row = sP + key * 32 + ((key >> 2) & 1) * 16;   // columns 0..7; 8..15 are in the other half
+    const int first = key * 32 + ((key >> 2) & 1) * 16, second = first ^ 16;   // columns 0..7 and 8..15
     if constexpr (NC == 1) {
-        *reinterpret_cast<uint16_t*>(row) = float_to_bf16_bits(pv[0]);
+        const uint16_t w = float_to_bf16_bits(pv[0]);
+        *reinterpret_cast<uint16_t*>(sP + first) = w;
+        if constexpr (TWO)
+            *reinterpret_cast<uint16_t*>(sP + second) = float_to_bf16_bits(pv[0] - __uint_as_float(static_cast<uint32_t>(w) << 16));
     } else {
-        uint32_t w[NC / 2];
+        uint32_t w[NC / 2], x[NC / 2];
 #pragma unroll
-        for (int i = 0; i < NC / 2; ++i) w[i] = pack_bf16x2(pv[2 * i], pv[2 * i + 1]);
+        for (int i = 0; i < NC / 2; ++i) {
+            w[i] = pack_bf16x2(pv[2 * i], pv[2 * i + 1]);
+            if constexpr (TWO)
+                x[i] = pack_bf16x2(pv[2 * i] - __uint_as_float(w[i] << 16), pv[2 * i + 1] - __uint_as_float(w[i] & 0xffff0000u));
+        }
         if constexpr (NC == 4) {
-            *reinterpret_cast<uint2*>(row) = make_uint2(w[0], w[1]);
+            *reinterpret_cast<uint2*>(sP + first) = make_uint2(w[0], w[1]);
+            if constexpr (TWO) *reinterpret_cast<uint2*>(sP + second) = make_uint2(x[0], x[1]);
         } else {
-            *reinterpret_cast<uint4*>(row) = make_uint4(w[0], w[1], w[2], w[3]);
-            if constexpr (NC == 16)
-                *reinterpret_cast<uint4*>(sP + key * 32 + (((key >> 2) & 1) ^ 1) * 16) = make_uint4(w[4], w[5], w[6], w[7]);
+            *reinterpret_cast<uint4*>(sP + first) = make_uint4(w[0], w[1], w[2], w[3]);
+            if constexpr (NC == 8 && TWO) *reinterpret_cast<uint4*>(sP + second) = make_uint4(x[0], x[1], x[2], x[3]);
+            if constexpr (NC == 16) {
+                *reinterpret_cast<uint4*>(sP + second) = make_uint4(w[4], w[5], w[6], w[7]);
+                if constexpr (TWO) {
+                    *reinterpret_cast<uint4*>(low + first) = make_uint4(x[0], x[1], x[2], x[3]);
+                    *reinterpret_cast<uint4*>(low + second) = make_uint4(x[4], x[5], x[6], x[7]);
+                }
+            }
         }
     }
 }
@@ -528,8 +549,8 @@ constexpr int kFixChunk = 32;   // partials whose weights are in shared memory a
 
 // Paged split mode finds the work split itself when it has up to this many batch entries: every CTA sums
 // the entries' tiles into its shared memory, which costs less than a launch that leaves them in global
-// memory.
-constexpr int kInlineB = 1024;
+// memory.  Twice as many would not fit beside 16 columns' P at D = 128.
+constexpr int kInlineB = 512;
 
 // O = 0 and LSE = -inf for batch entry b without keys, by the whole CTA
 __device__ __forceinline__ void write_empty_entry(const DecodeParams& p, int b)
@@ -1181,6 +1202,7 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
                         const uint64_t da = sdesc_sw128(sV + ks * 2 * L::kGroup, lbo_v, L::kGroup);
                         const uint64_t db = sdesc_sw32(sP + ks * 512, 256);
                         mma_ss(dO, da, db, idesc_pv, ks > 0 ? 1u : 0u);
+                        if constexpr (PAGED && NC == 16) mma_ss(dO, da, sdesc_sw32(sP + 2 * C::kPBytes + ks * 512, 256), idesc_pv, 1u);
                     }
                     mma_commit(&o_full[orr.idx]);
                     mma_commit(&v_empty[vr.idx]);
@@ -1253,7 +1275,15 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
                 tc_fence_after();
                 uint32_t ov[NC];
                 tmem_ld<NC>(tmem + lane_base + 32 + orr.idx * 16, ov);
-                tmem_ld_wait();
+                if constexpr (PAGED && NC <= 8) {   // and what the roundings of P left (see store_p)
+                    uint32_t ow[NC];
+                    tmem_ld<NC>(tmem + lane_base + 40 + orr.idx * 16, ow);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int q = 0; q < NC; ++q) ov[q] = __float_as_uint(__uint_as_float(ov[q]) + __uint_as_float(ow[q]));
+                } else {
+                    tmem_ld_wait();
+                }
                 orr.advance();
                 if (moved_prev) {
 #pragma unroll
@@ -1324,9 +1354,9 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
                     }
                 }
                 vr.advance();
-                // rows of P beyond NC keep what they held: they only reach columns of O that nobody reads
+                // other columns of P keep what they held: they only reach columns of O that nobody reads
                 uint8_t* sP = smem + C::kOffP + pr.idx * C::kPBytes;
-                store_p<NC>(sP, tid, pv);
+                store_p<NC, PAGED>(sP, sP + 2 * C::kPBytes, tid, pv);
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();

@@ -100,16 +100,16 @@ def attention_ref(q, k, v, lens, scale, causal):
     return o, lse, a
 
 
-# Tolerance of the output, from the roundings that the kernel makes: each p_j to BF16 (half a step, 2^-8 of
-# itself: 2^-8 a in all), the output to BF16 (2^-8 |o|), and FP32 sums.  The scores' FP32 sums over D <= 128
-# features err by at most 128 * 2^-23 * |q|.|k| scale <= 2^-16 * 16 for unit normals (|q|.|k| scale < 16 at
-# D <= 128), 2^-12 of each p_j; the sums over keys, split by tiles of 128, by less than 2^-13 a.  So
-# 2^-8 a (1 + 2^-4 + 2^-5) + 2^-8 |o|, and for the log-sum-exp 2^-12 + a few 2^-22 |lse|.
+# Tolerance of the output, from the roundings that the kernel makes: each p_j to two BF16 (what the first leaves,
+# 2^-8 of p_j, rounded to half a step of its own: 2^-16 a in all), the output to BF16 (2^-8 |o|), and FP32 sums.
+# The scores' FP32 sums over D <= 128 features err by at most 128 * 2^-23 * |q|.|k| scale <= 2^-16 * 16 for unit
+# normals (|q|.|k| scale < 16 at D <= 128), 2^-12 of each p_j; the sums over keys, split by tiles of 128, by less
+# than 2^-13 a.  So a (2^-12 + 2^-13 + 2^-16) + 2^-8 |o|, and for the log-sum-exp 2^-12 + a few 2^-22 |lse|.
 def check_attention(out, lse, ref, bf16=True, what=""):
     o, l, a = ref
     out = out.double().cpu().view_as(o)
     assert torch.isfinite(out).all(), f"{what}: non-finite output"
-    tol = 2.0 ** -8 * a * (1 + 3 / 32) + (2.0 ** -8 * o.abs() if bf16 else 0)
+    tol = a * (2.0 ** -12 + 2.0 ** -13 + 2.0 ** -16) + (2.0 ** -8 * o.abs() if bf16 else 0)
     over = (out - o).abs() - tol
     assert over.max() <= 0, f"{what}: off by {(out - o).abs().flatten()[over.argmax()]:.3e}, {over.max():.3e} too much"
     if lse is not None:
