@@ -293,11 +293,6 @@ def fmha_fwd_decode_noalloc(q, k, v, out, lse, scale: float, seqlens_k=None, str
 # ------------------------------------------------------------------------------------------------
 # paged key/value cache
 # ------------------------------------------------------------------------------------------------
-def _need(cond, what: str):
-    if not cond:
-        raise FmhaError(FMHA_ERR_INVALID, what)
-
-
 _ext = None
 
 

@@ -50,7 +50,7 @@ Shape paged_shape(int B, int Hq, int Sq, const fmha_kv_cache* c)
     Shape s{};
     s.chunks = rows > 0 ? (rows + kN - 1) / kN : 1;
     s.G = rows > 0 ? (rows + s.chunks - 1) / s.chunks : 0;
-    s.U = B * c->Hkv * s.chunks;
+    s.U = rows > 0 ? B * c->Hkv * s.chunks : 0;
     return s;
 }
 
@@ -67,6 +67,7 @@ PagedWs paged_ws(int B, int Hq, int Sq, const fmha_kv_cache* c, const fmha_opts*
 {
     auto al = [](size_t x) { return (x + 255) & ~size_t(255); };
     const Shape s = paged_shape(B, Hq, Sq, c);
+    if (s.U == 0) return {};   // nothing to do, nothing to do it in
     const int nsm = num_sms() > 0 ? num_sms() : 256;   // sized for the largest plausible SM count
     const bool split = o && o->num_splits != 1;
     const size_t slots = split ? static_cast<size_t>(s.U) + nsm : 0;

@@ -247,7 +247,8 @@ int fmha_page_table(const int32_t* ctx_lens, const int32_t* new_lens, int B, int
  *   positions: int32[T].  The first rope_dim features of queries and keys are rotated: feature i with
  *   i + rope_dim / 2, or (interleaved != 0) 2i with 2i + 1.  rope_dim: a multiple of 16 up to D, 0 = none
  *   (cos_sin and positions are not read).
- *   slots: int64[T], distinct; a negative slot is padding: nothing of that token is read or written.
+ *   slots: int64[T], distinct; a negative slot is padding: that token's rows of q, k and v, which are there, may
+ *   hold anything, and nothing of it is written.
  *   q_out: BF16 [T / Sq][Hq][Sq][D], token t = n * Sq + s at [n][h][s] (Sq = 1: [T][Hq][D]).
  * Keys and values go to their slots of `cache` (values as they are).  FP32 throughout, one rounding to
  * BF16 per output.  A token with a slot or position out of bounds is left out like padding and reported.
@@ -267,8 +268,9 @@ int fmha_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_s
  *   seqlens_k must be NULL.  With a workspace of fmha_paged_workspace_size() bytes the keys are split over
  *   every SM, without one each (request, kv-head) is one CTA's.
  * Made for up to 16 query rows per key/value head, (Hq / Hkv) * Sq; more rows run in chunks of at most 16,
- * each reading the keys again.  Entries of the block table behind the last key are not read.  A page out
- * of the pool reads as zero keys and values, a length out of bounds is clamped, and both are reported.
+ * each reading the keys again.  Entries of the block table behind the last key are not read.  Queries, keys and
+ * values are finite; pool rows behind a request's length may hold anything (NaN too).  A page out of the pool
+ * reads as zero keys and values, a length out of bounds is clamped, and both are reported.
  */
 int fmha_fwd_paged(const void* q, const fmha_kv_cache* cache, const int32_t* block_table, int max_pages,
                    const int32_t* seqlens, void* out, float* lse, int B, int Hq, int Sq, float scale,

@@ -72,6 +72,7 @@ def test_paged_workspace_size(lib):
     assert lib.fmha_paged_workspace_size(2, 4, 1, None, None) == 0
     assert lib.fmha_paged_workspace_size(1 << 29, 4, 1, c, opts()) == 0
     # more than 16 rows per key/value head: chunks of rows, each with partials of its own
+    assert lib.fmha_paged_workspace_size(1 << 30, 4, 0, c, opts()) == lib.fmha_paged_workspace_size(0, 4, 1, c, opts()) == 0
     assert lib.fmha_paged_workspace_size(2, 64, 1, c, opts()) > lib.fmha_paged_workspace_size(2, 32, 1, c, opts())
 
 
