@@ -98,7 +98,9 @@ struct DecodeCfg {
     static constexpr int kSmemBytes = kOffP + 2 * kPBytes + 1024;   // + alignment slack
     // paged, 16 columns: two more P buffers behind the first two (see store_p)
     static constexpr int smem_bytes(int nc, bool paged) { return kSmemBytes + (paged && nc == 16 ? 2 * kPBytes : 0); }
-    static constexpr uint32_t kTmemCols = 128;             // S[2] x 16, O[2] x 16, handoff[2] x 32
+    // Tensor Memory columns: S[2] x 16, O[2] x 16, handoff[2] x 32; paged, 16 columns: O[2] x 32 behind them
+    static constexpr uint32_t tmem_cols(int nc, bool paged) { return paged && nc == 16 ? 256 : 128; }
+    static constexpr uint32_t o_col(int nc, bool paged, uint32_t buffer) { return paged && nc == 16 ? 128 + buffer * 32 : 32 + buffer * 16; }
 };
 
 struct DecodeParams {
@@ -348,12 +350,12 @@ __device__ __forceinline__ void tma_load_4d_hint(void* dst, const CUtensorMap* m
 // P^T of a tile is an MN-major operand with the 32-byte swizzle: 16 columns of a key in a row of 32 bytes, so
 // that the thread with the key stores them with at most two 16-byte stores (K-major rows of keys took one
 // 2-byte store per column); rows 4..7 of each 8 have their 16-byte halves exchanged.  Atoms of 8 keys are 256
-// bytes apart.
-__device__ __forceinline__ uint64_t sdesc_sw32(uint32_t saddr, uint32_t sbo_bytes)
+// bytes apart (SBO), the next 16 columns, if any, `lbo_bytes`.
+__device__ __forceinline__ uint64_t sdesc_sw32(uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_bytes)
 {
     uint64_t d = 0;
     d |= static_cast<uint64_t>((saddr & 0x3FFFF) >> 4);
-    d |= static_cast<uint64_t>(1) << 16;   // one atom spans all 16 columns: no stride between atoms along them
+    d |= static_cast<uint64_t>((lbo_bytes >> 4) & 0x3FFF) << 16;
     d |= static_cast<uint64_t>((sbo_bytes >> 4) & 0x3FFF) << 32;
     d |= static_cast<uint64_t>(1) << 46;
     d |= static_cast<uint64_t>(6) << 61;
@@ -363,8 +365,9 @@ __device__ __forceinline__ uint64_t sdesc_sw32(uint32_t saddr, uint32_t sbo_byte
 // Row `key` of P^T, rounded to BF16 (the operand type of the MMA; half a step, 2^-9 to 2^-8 of a weight).  TWO
 // (paged): what the rounding leaves goes along as a second BF16, so that P is good to 2^-17 and the output's
 // own rounding is the only one that shows (rms error of BF16 outputs 1.7e-3 of them instead of 2.3e-3).  Up to eight
-// columns it takes the other eight of the 16 (columns 8 ..) and no time that shows, with 16 a second buffer, `low`,
-// and a second MMA (B17 Hq16 Hkv4 Sq4 D64, up to 5001 keys: 21.2 us instead of 20.0).
+// columns it takes the other eight of the 16 (columns 8 ..), with 16 a second buffer, `low`, and an MMA of 32
+// columns over both.  Neither costs time that shows: an MMA takes as long as its V operand takes to be read
+// (4 KB, some 32 cycles; a second MMA of 16 columns instead cost B17 Hq16 Hkv4 Sq4 D64 1.2 of 20 us).
 template <int NC, bool TWO>
 __device__ __forceinline__ void store_p(uint8_t* sP, uint8_t* low, int key, const float (&pv)[NC])
 {
@@ -629,7 +632,7 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
         fence_barrier_init();
     }
     if (warp == mma_warp<EPI>()) {
-        tmem_alloc(&tmem_slot, C::kTmemCols);
+        tmem_alloc(&tmem_slot, C::tmem_cols(NC, PAGED));
         tmem_relinquish();
     }
     if constexpr (PAGED) {
@@ -642,7 +645,7 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tmem_slot;   // S buffers at columns 0/16, O buffers at 32/48, handoff at 64/96
+    const uint32_t tmem = tmem_slot;   // S buffers at columns 0/16, handoff at 64/96, O buffers at o_col()
     griddep_wait();   // the previous kernel of the stream has completed: global memory from here on
     if (blockIdx.x == 0 && threadIdx.x == 0 && p.nv_ts) *p.nv_ts = *p.nv_sg;   // single-pass NVFP4: report s_g
 
@@ -1185,7 +1188,7 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
         // ------------------------------------------------ MMA issuer
         if (lane_id() == 0) {
             constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kN, false, false);
-            constexpr uint32_t idesc_pv = idesc_bf16_f32(128, kN, true, true);
+            constexpr uint32_t idesc_pv = idesc_bf16_f32(128, PAGED && NC == 16 ? 2 * kN : kN, true, true);
             using L = TileLayout<D, PAGED>;
             constexpr uint32_t lbo_v = (D >= 128) ? L::kHalf : 0u;   // D = 64: M rows 64..127 repeat 0..63
             Ring qr(2), kr(S), vr(S), sr(2), pr(2), orr(2);
@@ -1196,13 +1199,12 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
                 if (!aborted(wc)) {
                     const uint32_t sV = smem_u32(smem + C::kOffV + vr.idx * C::kKVBytes);
                     const uint32_t sP = smem_u32(smem + C::kOffP + pr.idx * C::kPBytes);
-                    const uint32_t dO = tmem + 32 + orr.idx * 16;
+                    const uint32_t dO = tmem + C::o_col(NC, PAGED, orr.idx);
 #pragma unroll
                     for (int ks = 0; ks < kTileKV / 16; ++ks) {
                         const uint64_t da = sdesc_sw128(sV + ks * 2 * L::kGroup, lbo_v, L::kGroup);
-                        const uint64_t db = sdesc_sw32(sP + ks * 512, 256);
+                        const uint64_t db = sdesc_sw32(sP + ks * 512, 2 * C::kPBytes, 256);
                         mma_ss(dO, da, db, idesc_pv, ks > 0 ? 1u : 0u);
-                        if constexpr (PAGED && NC == 16) mma_ss(dO, da, sdesc_sw32(sP + 2 * C::kPBytes + ks * 512, 256), idesc_pv, 1u);
                     }
                     mma_commit(&o_full[orr.idx]);
                     mma_commit(&v_empty[vr.idx]);
@@ -1274,10 +1276,10 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
                 mbar_wait(&o_full[orr.idx], orr.phase, wc);
                 tc_fence_after();
                 uint32_t ov[NC];
-                tmem_ld<NC>(tmem + lane_base + 32 + orr.idx * 16, ov);
-                if constexpr (PAGED && NC <= 8) {   // and what the roundings of P left (see store_p)
+                tmem_ld<NC>(tmem + lane_base + C::o_col(NC, PAGED, orr.idx), ov);
+                if constexpr (PAGED) {   // and what the roundings of P left (see store_p)
                     uint32_t ow[NC];
-                    tmem_ld<NC>(tmem + lane_base + 40 + orr.idx * 16, ow);
+                    tmem_ld<NC>(tmem + lane_base + C::o_col(NC, PAGED, orr.idx) + (NC == 16 ? 16 : 8), ow);
                     tmem_ld_wait();
 #pragma unroll
                     for (int q = 0; q < NC; ++q) ov[q] = __float_as_uint(__uint_as_float(ov[q]) + __uint_as_float(ow[q]));
@@ -1443,7 +1445,7 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
 
     tc_fence_before();
     __syncthreads();
-    if (warp == mma_warp<EPI>()) tmem_dealloc(tmem, C::kTmemCols);
+    if (warp == mma_warp<EPI>()) tmem_dealloc(tmem, C::tmem_cols(NC, PAGED));
     if constexpr (PAGED) {
         const int B = p.U / p.Hkv;
         if (blockIdx.x == 0)
