@@ -427,17 +427,18 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N])
 template <int N>
 __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[N])
 {
-    static_assert(N == 2 || N == 8 || N == 16 || N == 32, "column counts in use");
-    if constexpr (N == 2)
-        asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(taddr), "r"(r[0]), "r"(r[1]) : "memory");
+    static_assert(N == 1 || N == 4 || N == 8 || N == 16, "column counts in use");
+    if constexpr (N == 1)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(r[0]) : "memory");
+    else if constexpr (N == 4)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+                     : "memory");
     else if constexpr (N == 8)
         asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
                      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                      : "memory");
-    else if constexpr (N == 16)
-        tmem_st16(taddr, r);
     else
-        tmem_st32(taddr, r);
+        tmem_st16(taddr, r);
 }
 
 // Barrier over the first 128 threads' warps that also returns whether any of them passes true
@@ -1255,9 +1256,71 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
         const int lane = static_cast<int>(lane_id());
         const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
         Ring sr(2), pr(2), orr(2), vr(S), hr(2);
-        while (sched.next(it)) {
+        float acc[NC], alpha_prev[NC];   // O of the tiles before the last, and what the last tile's max makes of it
+        bool moved_prev = false;
+        // O of the tile before: one tile late, so that its PV runs beside the softmax of the next
+        auto consume = [&]() {
+            mbar_wait(&o_full[orr.idx], orr.phase, wc);
+            tc_fence_after();
+            uint32_t ov[NC];
+            tmem_ld<NC>(tmem + lane_base + C::o_col(NC, PAGED, orr.idx), ov);
+            if constexpr (PAGED) {   // and what the roundings of P left (see store_p)
+                uint32_t ow[NC];
+                tmem_ld<NC>(tmem + lane_base + C::o_col(NC, PAGED, orr.idx) + (NC == 16 ? 16 : 8), ow);
+                tmem_ld_wait();
+#pragma unroll
+                for (int q = 0; q < NC; ++q) ov[q] = __float_as_uint(__uint_as_float(ov[q]) + __uint_as_float(ow[q]));
+            } else {
+                tmem_ld_wait();
+            }
+            orr.advance();
+            if (moved_prev) {
+#pragma unroll
+                for (int q = 0; q < NC; ++q) acc[q] = fmaf(acc[q], alpha_prev[q], __uint_as_float(ov[q]));
+            } else {
+#pragma unroll
+                for (int q = 0; q < NC; ++q) acc[q] += __uint_as_float(ov[q]);
+            }
+        };
+        // DEFER: an item's last O is consumed beside the next item's first tile too (Hq32 Hkv8 D128: B128 0..200 keys
+        // 21.1 -> 19.5 us, B32 0..300 10.9 -> 10.5, B32 0..1500 20.4 -> 20.0).  It publishes a partial later, which a
+        // merge waits for: B4 0..6000 16.4 -> 16.6, and with 16 columns B17 Hq16 Hkv4 Sq4 D64 20.1 -> 21.7, dense
+        // speculative decode (B8 Hq32 Hkv8 Sq4 8192 keys) 43.8 -> 45.6.  Deferring whole items alone takes most of
+        // the gain away (21.0 for the first).
+        constexpr bool DEFER = PAGED && NC <= 8;
+        bool pending = false;   // an item whose last O is still to come
+        // hands it to the epilogue warpgroup, with acc and the partial column sums through Tensor Memory (lane tid)
+        // and the reference maxima through shared memory, the sums and maxima at the item's end; the softmax goes on
+        // meanwhile.  Both sides walk the same item sequence and take part in every handoff whatever their waits
+        // return (a timeout only drains).
+        auto hand_off = [&]() {
+            __syncwarp();   // tcgen05.st is warp-collective
+            uint32_t hv[NC];
+#pragma unroll
+            for (int q = 0; q < NC; ++q) hv[q] = __float_as_uint(acc[q]);
+            tmem_st<NC>(tmem + lane_base + 64 + hr.idx * 32, hv);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ep_full[hr.idx]);
+            hr.advance();
+            pending = false;
+#pragma unroll
+            for (int q = 0; q < NC; ++q) acc[q] = 0.f;
+        };
+#pragma unroll
+        for (int q = 0; q < NC; ++q) acc[q] = 0.f;
+        for (;;) {
+            const bool more = sched.next(it);
+            if constexpr (DEFER) {
+                if (pending && !(more && it.t1 > it.t0)) {   // no tile comes to consume the last O beside
+                    consume();
+                    hand_off();
+                }
+            }
+            if (!more) break;
             const int G = unit_cols<PAGED>(p, it);
-            float m[NC], l[NC], acc[NC], alpha_prev[NC];
+            float m[NC], l[NC];
             // keys visible to column q: 0 .. lim[q] - 1 (causal: query q % Sq sees keys up to
             // (q % Sq) + n - Sq; otherwise all n)
             int lim[NC];
@@ -1268,33 +1331,7 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
             for (int q = 0; q < NC; ++q) {
                 m[q] = q < G ? -INFINITY : INFINITY;   // a column without a query: P = 0, never the largest
                 l[q] = 0.f;
-                acc[q] = 0.f;
-                alpha_prev[q] = 1.f;
             }
-            bool moved_prev = false;
-            auto consume = [&]() {
-                mbar_wait(&o_full[orr.idx], orr.phase, wc);
-                tc_fence_after();
-                uint32_t ov[NC];
-                tmem_ld<NC>(tmem + lane_base + C::o_col(NC, PAGED, orr.idx), ov);
-                if constexpr (PAGED) {   // and what the roundings of P left (see store_p)
-                    uint32_t ow[NC];
-                    tmem_ld<NC>(tmem + lane_base + C::o_col(NC, PAGED, orr.idx) + (NC == 16 ? 16 : 8), ow);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int q = 0; q < NC; ++q) ov[q] = __float_as_uint(__uint_as_float(ov[q]) + __uint_as_float(ow[q]));
-                } else {
-                    tmem_ld_wait();
-                }
-                orr.advance();
-                if (moved_prev) {
-#pragma unroll
-                    for (int q = 0; q < NC; ++q) acc[q] = fmaf(acc[q], alpha_prev[q], __uint_as_float(ov[q]));
-                } else {
-#pragma unroll
-                    for (int q = 0; q < NC; ++q) acc[q] += __uint_as_float(ov[q]);
-                }
-            };
             for (int t = it.t0; t < it.t1; ++t) {
                 mbar_wait(&s_full[sr.idx], sr.phase, wc);
                 tc_fence_after();
@@ -1364,44 +1401,36 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[pr.idx]);
                 pr.advance();
-                if (t > it.t0) consume();
+                if (t > it.t0 || (DEFER && pending)) consume();
+                if (DEFER && pending) hand_off();
                 moved_prev = moved;
                 if (moved)
 #pragma unroll
                     for (int q = 0; q < NC; ++q) alpha_prev[q] = alpha[q];
             }
-            if (it.t1 > it.t0) consume();
-
-            if constexpr (!EPI) {
-                run_epilogue(it, it.t1 <= it.t0, m, l, acc, tid, warp, 1, false);
-                continue;
-            }
-            // ---- hand the item to the epilogue warpgroup: acc and the partial column sums l through
-            // Tensor Memory (lane tid), the reference maxima through shared memory; the softmax goes
-            // on with the next item meanwhile.  Both sides walk the same item sequence and take part
-            // in every handoff whatever their waits return (a timeout only drains).
-            {
+            if constexpr (EPI) {
                 mbar_wait(&ep_empty[hr.idx], hr.phase ^ 1, wc);
                 tc_fence_after();
-                __syncwarp();   // tcgen05.st is warp-collective
-                if constexpr (EPI) {
-                    uint32_t hv[2 * NC];
+                __syncwarp();
+                uint32_t hv[NC];
 #pragma unroll
-                    for (int q = 0; q < NC; ++q) {
-                        hv[q] = __float_as_uint(acc[q]);
-                        hv[NC + q] = __float_as_uint(l[q]);
-                    }
-                    tmem_st<2 * NC>(tmem + lane_base + 64 + hr.idx * 32, hv);
-                    tmem_st_wait();
-                }
+                for (int q = 0; q < NC; ++q) hv[q] = __float_as_uint(l[q]);
+                tmem_st<NC>(tmem + lane_base + 64 + NC + hr.idx * 32, hv);
                 if (tid == 0)
 #pragma unroll
                     for (int q = 0; q < NC; ++q) ep_m[hr.idx][q] = m[q];
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ep_full[hr.idx]);
+                if (DEFER && it.t1 > it.t0) {
+                    pending = true;
+                } else {
+                    if (it.t1 > it.t0) consume();
+                    hand_off();
+                }
+            } else {
+                if (it.t1 > it.t0) consume();
+                run_epilogue(it, it.t1 <= it.t0, m, l, acc, tid, warp, 1, false);
+#pragma unroll
+                for (int q = 0; q < NC; ++q) acc[q] = 0.f;
             }
-            hr.advance();
         }
     } else {
       if constexpr (EPI) {
