@@ -29,8 +29,9 @@
 //    the work split comes from the requests' lengths inside the kernel (see Line).
 //  * Roles (decode_kernel<D, CAUSAL, NC, PAGED>): warps 0-3 softmax.  EPI (see
 //    has_epilogue_warps): warps 4-7 epilogue, warp 8 TMA producer, warp 9 MMA issuer, warp 10 the second
-//    producer of paged tiles, the rest only completes its warpgroup; at the end of a work item the softmax warps hand its accumulators to the
-//    epilogue warps (Tensor Memory, two buffers) and go on with the next item while the epilogue
+//    producer of paged tiles, the rest only completes its warpgroup; at the end of a work item the
+//    softmax warps hand its accumulators to the epilogue warps (Tensor Memory, two buffers; see DEFER)
+//    and go on with the next item while the epilogue
 //    normalises, stores and merges.  !EPI: warp 4 producer, warp 5 MMA, and the softmax
 //    warps run each item's short epilogue themselves.  Every wait is bounded; a timeout flips the
 //    CTA into a drain mode (no new TMA/MMA, loops run out) and sets the device status word.
@@ -366,8 +367,8 @@ __device__ __forceinline__ uint64_t sdesc_sw32(uint32_t saddr, uint32_t lbo_byte
 // (paged): what the rounding leaves goes along as a second BF16, so that P is good to 2^-17 and the output's
 // own rounding is the only one that shows (rms error of BF16 outputs 1.7e-3 of them instead of 2.3e-3).  Up to eight
 // columns it takes the other eight of the 16 (columns 8 ..), with 16 a second buffer, `low`, and an MMA of 32
-// columns over both.  Neither costs time that shows: an MMA takes as long as its V operand takes to be read
-// (4 KB, some 32 cycles; a second MMA of 16 columns instead cost B17 Hq16 Hkv4 Sq4 D64 1.2 of 20 us).
+// columns over both.  Neither costs time that shows: an MMA of up to 64 columns takes the same 50 cycles (a second
+// MMA of 16 columns instead cost B17 Hq16 Hkv4 Sq4 D64 1.2 of 20 us).
 template <int NC, bool TWO>
 __device__ __forceinline__ void store_p(uint8_t* sP, uint8_t* low, int key, const float (&pv)[NC])
 {

@@ -36,14 +36,14 @@ FALLBACK_PEAKS = {"hbm_gbs": 6800.0, "bf16_tflops": 1900.0, "bf16_tflops_sustain
 TRAFFIC = {
     # decode B8 H32 Sq1 Skv4096 D128 (decode_kernel<128, 0, 1, 0>, 128 CTAs of two whole units): read
     # 537,031,168 + written 3,233,024 bytes (profiles/decode_kernel_decode-B8-H32-Skv4096-D128.md)
-    "decode_kernel<128>": {"bytes": 540264192, "source_sha": "c7bc57fab364d81f"},
+    "decode_kernel<128>": {"bytes": 540264192, "source_sha": "709afd275356f11d"},
     # ragged GQA decode B64 Hq32 Hkv8 Skv<=32768 D128 (decode_kernel<128, 0, 4, 0>): the quarter-size workload
     # (B16) read 1,005,855,232 + wrote 384,256 bytes for 1,001,226,240 algorithmic K/V bytes (1.005x); scaled
     # by the K/V bytes to the full workload's 4,106,002,432 (profiles/side-kernels_ragged-decode-wide-combine-nvfp4.md)
-    "decode_kernel<128>/ragged": {"bytes": 4126561630, "source_sha": "c7bc57fab364d81f"},
+    "decode_kernel<128>/ragged": {"bytes": 4126561630, "source_sha": "709afd275356f11d"},
     # speculative decode B8 Hq32 Hkv8 Sq4 Skv8192 D128, causal (decode_kernel<128, 1, 16, 0>): read 268,811,776 +
     # written 2,683,904 bytes (profiles/decode_kernel_decode-B8-H32-Skv4096-D128.md)
-    "decode_kernel<128>/speculative": {"bytes": 271495680, "source_sha": "c7bc57fab364d81f"},
+    "decode_kernel<128>/speculative": {"bytes": 271495680, "source_sha": "709afd275356f11d"},
     # wide-head B32 Hq128 Hkv1 Skv16384 D512, independent CTAs: read 1,081,726,464 + written 10,248,960
     # bytes (profiles/wide_kernel_wide-head-B32-Hq128-Hkv1-Skv16384-D512.md)
     "wide_kernel<independent>": {"bytes": 1091975424, "source_sha": "78a9a91c90649bc2"},

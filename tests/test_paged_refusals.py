@@ -56,7 +56,7 @@ def test_cache_descriptor(lib, bad, code):
     (dict(c=cache(D=128, token_stride=128, head_stride=2048, page_stride=1024)), 2), (dict(c=cache(page_size=12)), 2), (dict(c=cache(page_size=4)), 2), (dict(pages=1 << 28), 2), (dict(B=1 << 30), 2),
     (dict(opts=opts(out_kind=7)), 1), (dict(opts=opts(num_splits=-1)), 1), (dict(opts=opts(seqlens_k=A)), 1),
     (dict(opts=opts(out_kind=2)), 1), (dict(opts=opts(workspace=0x10010, workspace_bytes=1 << 20)), 1)])
-def test_paged_attention(lib, bad, code):
+def test_fwd_paged(lib, bad, code):
     assert paged(lib, **bad) == code
     assert b"fmha_fwd_paged" in lib.fmha_last_error()
 
