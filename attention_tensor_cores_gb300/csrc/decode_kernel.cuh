@@ -866,15 +866,19 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
         // one abort decision for all four warps (named barriers and shuffles below)
         if (tid == 0) ep_abort = aborted(wc) ? 1 : 0;
         named_bar_sync(bar, 128);
-        if (ep_abort) return;
+        const bool lost = ep_abort != 0;
         // single-pass NVFP4 in split mode: whole units also go through the combine, which
         // encodes every row in parallel (encoding here would lengthen the CTAs holding many
         // short units)
         const bool final_here = it.whole && !(p.split && p.nv_codes);
+        // An aborted CTA writes no result, but a partial that is counted goes out all the same, as one without a
+        // visible key: a graph's replays carry one tag, so an arrival left out here would be made up for by the
+        // next replay's first one.
+        if (lost && !(p.fixup && !final_here)) return;
         float local_amax = 0.f;
         float o[NC];
 #pragma unroll
-        for (int q = 0; q < NC; ++q) o[q] = col_inv[q] > 0.f ? acc[q] * col_inv[q] : 0.f;   // 0: no visible key in this range
+        for (int q = 0; q < NC; ++q) o[q] = col_inv[q] > 0.f && !lost ? acc[q] * col_inv[q] : 0.f;   // 0: no visible key in this range
         if (final_here) {
             if (tid < D) {
                 local_amax = write_rows(o, tid);
@@ -892,7 +896,7 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
                 for (int q = 0; q < NC; ++q)
                     if (q < G) dst[q * D] = o[q];
             }
-            if (tid < G) p.part_lse[static_cast<size_t>(it.slot) * kN + tid] = col_lse[tid];
+            if (tid < G) p.part_lse[static_cast<size_t>(it.slot) * kN + tid] = lost ? -INFINITY : col_lse[tid];
         }
         if (p.amax_bits && final_here) {
             const float wm = warp_max(local_amax);
