@@ -13,7 +13,7 @@
 #include <string>
 
 #include "internal.h"
-#include "paged.h"
+#include "ptx.cuh"
 
 namespace atc_gb300 {
 
@@ -32,10 +32,9 @@ int cuda_error(cudaError_t e, const char* what)
 }
 
 // ---- device status word ----------------------------------------------------------------------------
-// One int per device in this library's module: kernels write a nonzero code when a bounded wait
-// expires.  Its address is looked up once per device and passed to kernels as a pointer.
+// One int per device in this library's module: kernels leave the largest of their codes in it
+// (ptx.cuh).  Its address is looked up once per device and passed to kernels as a pointer.
 static __device__ int g_status_word;
-static constexpr int kDevMergeLost = 6;   // the value the split-KV merge leaves (ptx.cuh)
 static constexpr int kMaxDevices = 64;
 static std::atomic<int*> g_status_addr[kMaxDevices];
 static std::atomic<int> g_num_sms[kMaxDevices];

@@ -6,9 +6,6 @@
 
 namespace atc_gb300 {
 
-// Status word value that the paged-cache kernels leave for device data out of bounds
-constexpr int kDevBadPage = 7;
-
 inline bool misaligned(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
 
 // Checks of a cache descriptor that every entry point makes.
