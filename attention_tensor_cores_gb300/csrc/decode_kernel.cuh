@@ -490,6 +490,21 @@ struct Ring {
     }
 };
 
+// The same for merges, where a NaN is to be seen
+__device__ __forceinline__ float redux_max_nan(float v)
+{
+    float r;
+    asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+__device__ __forceinline__ float fmax_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 __device__ __forceinline__ float warp_max(float v)
 {
 #pragma unroll
@@ -859,7 +874,7 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
 #pragma unroll
             for (int q = 1; q < NC; ++q)
                 if (q == tid) mq = m[q];
-            const bool none = !(Lq > 0.f);   // no visible key in this range
+            const bool none = Lq == 0.f;   // no visible key in this range; a NaN score makes L, the row and its LSE NaN
             col_inv[tid] = none ? 0.f : 1.f / Lq;
             col_lse[tid] = none ? -INFINITY : (mq + __log2f(Lq)) * kLn2;
         }
@@ -878,7 +893,7 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
         float local_amax = 0.f;
         float o[NC];
 #pragma unroll
-        for (int q = 0; q < NC; ++q) o[q] = col_inv[q] > 0.f && !lost ? acc[q] * col_inv[q] : 0.f;   // 0: no visible key in this range
+        for (int q = 0; q < NC; ++q) o[q] = col_inv[q] != 0.f && !lost ? acc[q] * col_inv[q] : 0.f;   // 0: no visible key in this range
         if (final_here) {
             if (tid < D) {
                 local_amax = write_rows(o, tid);
@@ -946,8 +961,8 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             lv[i] = i < ns ? __ldcg(p.part_lse + static_cast<size_t>(fx_slot[i]) * kN + tid) : -INFINITY;
-                        const float mx = fmaxf(fmaxf(lv[0], lv[1]), fmaxf(lv[2], lv[3]));
-                        const bool any = mx > -INFINITY;   // partials without a visible key carry -inf
+                        const float mx = fmax_nan(fmax_nan(lv[0], lv[1]), fmax_nan(lv[2], lv[3]));
+                        const bool any = mx != -INFINITY;   // partials without a visible key carry -inf
                         float sum = 0.f;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) sum += (any && i < ns) ? __expf(lv[i] - mx) : 0.f;
@@ -979,24 +994,24 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
                     for (int c = 0; c < kCols; ++c) mx[c] = lv[c] = load_lse(c, lane);
                     for (int i = lane + kFixChunk; i < ns; i += kFixChunk)
 #pragma unroll
-                        for (int c = 0; c < kCols; ++c) mx[c] = fmaxf(mx[c], load_lse(c, i));
+                        for (int c = 0; c < kCols; ++c) mx[c] = fmax_nan(mx[c], load_lse(c, i));
 #pragma unroll
                     for (int c = 0; c < kCols; ++c) {
-                        mx[c] = redux_max(mx[c]);
+                        mx[c] = redux_max_nan(mx[c]);
                         // partials without a visible key carry lse = -inf and weigh 0; all of them -> empty row
-                        all[c] = mx[c] > -INFINITY ? __expf(lv[c] - mx[c]) : 0.f;
+                        all[c] = mx[c] != -INFINITY ? __expf(lv[c] - mx[c]) : 0.f;
                     }
                     for (int i = lane + kFixChunk; i < ns; i += kFixChunk)
 #pragma unroll
                         for (int c = 0; c < kCols; ++c)
-                            if (mx[c] > -INFINITY) all[c] += __expf(load_lse(c, i) - mx[c]);
+                            if (mx[c] != -INFINITY) all[c] += __expf(load_lse(c, i) - mx[c]);
 #pragma unroll
                     for (int x = 16; x > 0; x >>= 1)
 #pragma unroll
                         for (int c = 0; c < kCols; ++c) all[c] += __shfl_xor_sync(0xffffffffu, all[c], x);
 #pragma unroll
                     for (int c = 0; c < kCols; ++c) {
-                        all[c] = mx[c] > -INFINITY ? mx[c] + __logf(all[c]) : -INFINITY;
+                        all[c] = mx[c] != -INFINITY ? mx[c] + __logf(all[c]) : -INFINITY;
                         if (lane == 0 && ew + 4 * c < NC) fx_lse[ew + 4 * c] = all[c];
                     }
                     const int d = ew * 32 + (lane & 7) * 4, first = lane >> 3;
@@ -1008,7 +1023,7 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
 #pragma unroll
                         for (int c = 0; c < kCols; ++c) {
                             const float x = c0 ? load_lse(c, c0 + lane) : lv[c];
-                            if (ew + 4 * c < NC) fx_w[ew + 4 * c][lane] = all[c] > -INFINITY ? __expf(x - all[c]) : 0.f;
+                            if (ew + 4 * c < NC) fx_w[ew + 4 * c][lane] = all[c] != -INFINITY ? __expf(x - all[c]) : 0.f;
                         }
                         named_bar_sync(bar, 128);
                         const int nc = min(kFixChunk, ns - c0);
@@ -1608,11 +1623,11 @@ __global__ void combine_kernel(const __grid_constant__ DecodeParams p, int nctas
         __syncwarp();
         // LSE of the merged row and each partial's weight exp(lse_i - lse), once per block
         float mx = -INFINITY;
-        for (int i = static_cast<int>(threadIdx.x); i < cnt; i += 32) mx = fmaxf(mx, p.part_lse[static_cast<size_t>(slots[i]) * kN + q]);
+        for (int i = static_cast<int>(threadIdx.x); i < cnt; i += 32) mx = fmax_nan(mx, p.part_lse[static_cast<size_t>(slots[i]) * kN + q]);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        for (int o = 16; o > 0; o >>= 1) mx = fmax_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
         // partials without a visible key carry lse = -inf and weigh 0; all of them -> empty row
-        const bool any = mx > -INFINITY;
+        const bool any = mx != -INFINITY;
         float sum = 0.f;
         if (any)
             for (int i = static_cast<int>(threadIdx.x); i < cnt; i += 32) sum += __expf(p.part_lse[static_cast<size_t>(slots[i]) * kN + q] - mx);

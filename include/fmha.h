@@ -269,7 +269,8 @@ int fmha_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_s
  *   every SM, without one each (request, kv-head) is one CTA's.
  * Made for up to 16 query rows per key/value head, (Hq / Hkv) * Sq; more rows run in chunks of at most 16,
  * each reading the keys again.  Entries of the block table behind the last key are not read.  Queries, keys and
- * values are finite; pool rows behind a request's length may hold anything (NaN too).  A page out of the pool
+ * values are finite (a score of NaN or infinity makes its row and that row's LSE NaN, however the keys are
+ * split); pool rows behind a request's length may hold anything (NaN too).  A page out of the pool
  * reads as zero keys and values, a length out of bounds is clamped, and both are reported.
  */
 int fmha_fwd_paged(const void* q, const fmha_kv_cache* cache, const int32_t* block_table, int max_pages,
