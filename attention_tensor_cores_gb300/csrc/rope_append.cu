@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) rope_append_kernel(const __gr
     const Runs r = kind == 2 ? Runs{16 * l, 16 * l + 8} : runs_of<PAIRS>(l, p.R);
 
     const int64_t stride = kind == 0 ? p.q_stride : kind == 1 ? p.k_stride : p.v_stride;
-    const uint16_t* x = (kind == 0 ? p.q : kind == 1 ? p.k : p.v) + t * stride + h0 * D;
+    const uint16_t* x = (kind == 0 ? p.q : kind == 1 ? p.k : p.v) + t * stride + static_cast<int64_t>(h0) * D;
     uint4 u[HEADS][2];
 #pragma unroll
     for (int k = 0; k < HEADS; ++k)
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) rope_append_kernel(const __gr
     if (kind == 0) {
         const int n = p.by_sq.div(t);
         step = static_cast<int64_t>(p.Sq) * D;
-        y = p.q_out + (static_cast<int64_t>(n) * p.Hq + h0) * step + (t - n * p.Sq) * D;
+        y = p.q_out + (static_cast<int64_t>(n) * p.Hq + h0) * step + static_cast<int64_t>(t - n * p.Sq) * D;
     } else {
         const int64_t page = p.by_page.div(static_cast<int>(slot));
         step = p.head_stride;
