@@ -58,10 +58,11 @@ struct PagedWs {
     size_t prefix_off, ctr_off, lse_off, o_off, stage_off, amax_off, total;
 };
 
-// The kernel finds the work split and merges split units itself, except for single-pass NVFP4, whose rows a
-// combine kernel encodes (as in the dense decode), and very large batches, whose split a kernel of its own
-// finds.
-bool needs_prefix(int B, bool encode) { return encode || B > kInlineB; }
+// The kernel merges split units itself, except for single-pass NVFP4, whose rows a combine kernel encodes (as in
+// the dense decode), and for more SMs than it has slots for a unit's partials.  It finds the work split itself,
+// except for very large batches, and where the combine kernel, which takes it from global memory, is to see it.
+bool needs_combine(bool encode, int nsm) { return encode || nsm > kMaxFixSlots; }
+bool needs_prefix(int B, bool encode, int nsm) { return needs_combine(encode, nsm) || B > kInlineB; }
 
 PagedWs paged_ws(int B, int Hq, int Sq, const fmha_kv_cache* c, const fmha_opts* o)
 {
@@ -74,7 +75,7 @@ PagedWs paged_ws(int B, int Hq, int Sq, const fmha_kv_cache* c, const fmha_opts*
     PagedWs w{};
     size_t off = 0;
     w.prefix_off = off;
-    off += split && needs_prefix(B, o->nvfp4_scale_in != nullptr) ? al((static_cast<size_t>(B) + 2) * 4) : 0;
+    off += split && needs_prefix(B, o->nvfp4_scale_in != nullptr, nsm) ? al((static_cast<size_t>(B) + 2) * 4) : 0;
     w.ctr_off = off;
     off += split ? al(static_cast<size_t>(s.U) * 8) : 0;
     w.lse_off = off;
@@ -167,8 +168,8 @@ int run_paged(const PagedArgs& a, bool split, const PagedWs& w, uint8_t* base, c
     p.cap = a.max_pages * a.c->page_size;
     p.Skv = p.cap;
     p.split = split ? 1 : 0;
-    p.fixup = split && !a.nv_sg && nsm <= kMaxFixSlots ? 1 : 0;
-    p.prefix = split && needs_prefix(a.B, a.nv_sg != nullptr) ? reinterpret_cast<const int32_t*>(base + w.prefix_off) : nullptr;
+    p.fixup = split && !needs_combine(a.nv_sg != nullptr, nsm) ? 1 : 0;
+    p.prefix = split && needs_prefix(a.B, a.nv_sg != nullptr, nsm) ? reinterpret_cast<const int32_t*>(base + w.prefix_off) : nullptr;
     p.out = a.out_kind == FMHA_OUT_NVFP4 ? nullptr : a.out;
     p.out_f32 = a.out_kind == FMHA_OUT_F32 ? 1 : 0;
     p.lse = a.lse;
