@@ -72,6 +72,7 @@ class fmha_kv_cache(ctypes.Structure):
         ("head_stride", ctypes.c_int64),
         ("token_stride", ctypes.c_int64),
     ]
+    device = None   # index of the pools' CUDA device (make_kv_cache), compared with the other tensors' at every call
 
 
 def header_functions() -> list[str]:
@@ -334,7 +335,7 @@ def make_kv_cache(k, v) -> fmha_kv_cache:
     c.k, c.v = k.data_ptr(), v.data_ptr()
     c.num_pages, c.Hkv, c.page_size, c.D = k.shape
     c.page_stride, c.head_stride, c.token_stride = strides(k)
-    c.pools = (k, v)
+    c.pools, c.device = (k, v), k.get_device()
     return c
 
 

@@ -127,6 +127,21 @@ T structure(PyObject* o, const char* what)
     return v;
 }
 
+// The cache's descriptor.  Its pools are bare pointers, so the device that make_kv_cache saw them on goes along as an
+// attribute; a descriptor filled by hand has None there and is taken at its word.
+fmha_kv_cache cache_of(PyObject* o, int device)
+{
+    const fmha_kv_cache c = structure<fmha_kv_cache>(o, "cache must be a fmha_kv_cache (make_kv_cache)");
+    static PyObject* const name = PyUnicode_InternFromString("device");
+    PyObject* at = PyObject_GetAttr(o, name);
+    if (!at) PyErr_Clear();
+    const bool here = !at || at == Py_None || PyLong_AsLong(at) == device;
+    if (PyErr_Occurred()) PyErr_Clear();
+    Py_XDECREF(at);
+    need(here, "the cache's pools must be on the device of the other tensors");
+    return c;
+}
+
 template <typename F>
 PyObject* guarded(F&& body)
 {
@@ -197,7 +212,7 @@ PyObject* rope_append(PyObject* self, PyObject* const* a, Py_ssize_t n)
         const at::Tensor& slots = tensor(a[8], "slots must be an int64 tensor");
         const int dev = device_of(slots);
         plain(a[8], dev, at::kLong, "slots must be a contiguous int64 tensor");
-        const fmha_kv_cache cache = structure<fmha_kv_cache>(a[10], "cache must be a fmha_kv_cache (make_kv_cache)");
+        const fmha_kv_cache cache = cache_of(a[10], dev);
         const char* shapes = "q must be BF16 [T, Hq, D], k and v [T, Hkv, D], with contiguous heads, on the device of slots";
         const at::Tensor &q = tensor(a[0], shapes), &k = tensor(a[1], shapes), &v = tensor(a[2], shapes);
         need(q.dim() == 3, shapes);
@@ -258,7 +273,7 @@ PyObject* fwd_paged(PyObject* self, PyObject* const* a, Py_ssize_t n)
         const at::Tensor& q = tensor(a[0], "q must be a tensor");
         const int dev = device_of(q);
         plain(a[0], dev, at::kBFloat16, "q must be a contiguous BF16 tensor");
-        const fmha_kv_cache cache = structure<fmha_kv_cache>(a[1], "cache must be a fmha_kv_cache (make_kv_cache)");
+        const fmha_kv_cache cache = cache_of(a[1], dev);
         fmha_opts opts{};
         const bool has_opts = a[7] != Py_None;
         if (has_opts) opts = structure<fmha_opts>(a[7], "opts must be a fmha_opts (make_opts) or None");
