@@ -215,7 +215,7 @@ typedef struct {
 
 /*
  * Pages, block tables and slots from request lengths, for one step of B requests (at most 8192), in
- * one launch.
+ * one launch (two for an update in place of more than 2048 tokens or requests).
  *   ctx_lens: int32[B], tokens request b has in the cache; new_lens: int32[B], tokens to come (0: none),
  *   or a negative number: the request is done and its pages go back.
  *   free_pages: int32[num_pages], a stack of free pages whose height is *free_count.  First the pages of
@@ -230,7 +230,9 @@ typedef struct {
  * arrays may overlap.  With a length that is negative or passes the table row, a stack height outside
  * 0..num_pages, too few free pages, or more than T new tokens, nothing is given or taken: seqlens =
  * ctx_lens, cu_new 0, positions 0, slots -1, the stack as it was, and FMHA_ERR_PAGES from
- * fmha_check_status.  A token whose page is not one of the pool's gets slot -1 and the same report.
+ * fmha_check_status.  An id that is not one of the pool's pages is handed on like any other: a token on
+ * such a page gets slot -1, and a done request's goes on the stack with its other pages, both with the
+ * same report.  It stays in the pool until the program takes it out.
  * All pointers device memory; slots 8-byte, the others 4-byte aligned.
  */
 int fmha_page_table(const int32_t* ctx_lens, const int32_t* new_lens, int B, int page_size, int32_t* free_pages,
