@@ -32,8 +32,8 @@ int cuda_error(cudaError_t e, const char* what)
 }
 
 // ---- device status word ----------------------------------------------------------------------------
-// One int per device in this library's module: kernels leave the largest of their codes in it
-// (ptx.cuh).  Its address is looked up once per device and passed to kernels as a pointer.
+// One int per device in this library's module: kernels leave their codes in it (ptx.cuh).  Its address
+// is looked up once per device and passed to kernels as a pointer.
 static __device__ int g_status_word;
 static constexpr int kMaxDevices = 64;
 static std::atomic<int*> g_status_addr[kMaxDevices];

@@ -931,7 +931,7 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
                 const int arrived = n > 0 ? arrive_unit(p.unit_ctr + it.u, p.gen, n) : 0;
                 // -1: the counter kept changing under us (another call on this workspace):
                 // the unit may stay unmerged, so say so instead of failing silently
-                if (arrived < 0) report(p.status, kDevMergeLost);
+                if (arrived < 0) atomicExch(p.status, kDevMergeLost);
                 fx_last = (arrived == n && n > 0) ? 1 : 0;
                 // every arrival of this call is in: clear the counter for the next call.  A CUDA graph
                 // replays a call with the same tag, so its arrivals must not be left over (0 carries
@@ -1127,7 +1127,7 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
                     const bool mine = lane < boxes && j < it.n;
                     if (mine && (page < 0 || page >= p.num_pages)) {
                         page = p.num_pages;
-                        report(p.status, kDevBadPage);
+                        report_bad_page(p.status);
                     }
                     const int used = (min(it.n - t * kTileKV, kTileKV) + p.box - 1) >> p.box_log2;
                     const uint32_t bytes = static_cast<uint32_t>((used << p.box_log2) * 128 * C::kAtoms);
@@ -1499,7 +1499,7 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
         const int B = p.U / p.Hkv;
         if (blockIdx.x == 0)
             for (int b = threadIdx.x; b < B; b += blockDim.x)
-                if (p.seqlens[b] < 0 || p.seqlens[b] > p.cap) report(p.status, kDevBadPage);
+                if (p.seqlens[b] < 0 || p.seqlens[b] > p.cap) report_bad_page(p.status);
         if (p.fixup)   // no combine kernel runs: entries without keys are written here
             for (int b = blockIdx.x; b < B; b += gridDim.x)
                 if (pre[b + 1] == pre[b]) write_empty_entry(p, b);

@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(1024) page_table_kernel(const __grid_constant_
                 p.positions[t] = 0;
                 p.slots[t] = -1;
             }
-            if (first == 0) report(p.status, kDevBadPage);
+            if (first == 0) report_bad_page(p.status);
         }
         if (p.parts & kLengths) {
             for (int b = first; b < B; b += step) p.seqlens[b] = s_ctx[b];
@@ -198,14 +198,14 @@ __global__ void __launch_bounds__(1024) page_table_kernel(const __grid_constant_
             if (x < given_n) old_page = *given(x);
             if (x < p.T) {
                 const bool ok = x < tokens && fine(page);
-                if (x < tokens && !ok) report(p.status, kDevBadPage);
+                if (x < tokens && !ok) report_bad_page(p.status);
                 p.positions[x] = pos;
                 p.slots[x] = ok ? static_cast<long long>(page) * P + (pos - p.by_page.div(pos) * P) : -1;
             }
             if (x < taken_n) row(to)[p.by_page.up(s_ctx[to]) + (x - s_aoff[to])] = new_page;
             if (x < given_n) {
                 p.free_pages[n + x] = old_page;
-                if (!fine(old_page)) report(p.status, kDevBadPage);
+                if (!fine(old_page)) report_bad_page(p.status);
             }
         }
         for (int b = first; b <= B; b += step) p.cu[b] = b < B ? s_cu[b] : tokens;

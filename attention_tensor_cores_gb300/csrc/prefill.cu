@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(prefill_threads<RING>(), 1)
                         }
                         if (!did && clock64() - t_idle > p.limit) {
                             abort_flag = 1;
-                            report(p.status, kDevTimeout);
+                            atomicExch(p.status, kDevTimeout);
                         }
                     }
                     if (!aborted(wc)) mma_commit(&q_empty[qr.idx]);

@@ -98,12 +98,12 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity)
 // shared memory.
 constexpr long long kDrainLimit = 4000000000LL;
 
-// Status codes a kernel can leave in the device status word (the host maps them to fmha_status), in the order
-// of what they say about the results: after kDevBadPage (paged-cache data out of bounds) they are defined, after
-// the others they are not.  The word keeps the largest.
+// Status codes a kernel can leave in the device status word (the host maps them to fmha_status).  After
+// kDevBadPage (paged-cache data out of bounds) results are defined, after the others they are not: those
+// overwrite the word (atomicExch), and kDevBadPage, the lowest, only goes into an empty one.
 enum : int { kDevOk = 0, kDevBadPage = 1, kDevTimeout = 5, kDevMergeLost = 6 };
 
-__device__ __forceinline__ void report(int* status, int code) { atomicMax(status, code); }
+__device__ __forceinline__ void report_bad_page(int* status) { atomicMax(status, kDevBadPage); }
 
 // Per-CTA abort state: once any wait of a CTA gives up, every later wait of that CTA returns
 // false at once, so all roles run their (bounded) loops to the end without blocking and meet
@@ -135,7 +135,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const 
             return false;
         if (clock64() - t0 > w.limit) {
             *reinterpret_cast<volatile int*>(w.abort_flag) = 1;
-            report(w.status, kDevTimeout);
+            atomicExch(w.status, kDevTimeout);
             return false;
         }
         if (mbar_try_wait(a, parity))
@@ -222,7 +222,7 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
             return false;
         if (clock64() - t0 > w.limit) {
             *reinterpret_cast<volatile int*>(w.abort_flag) = 1;
-            report(w.status, kDevTimeout);
+            atomicExch(w.status, kDevTimeout);
             return false;
         }
         if (mbar_try_wait_cluster(a, parity))

@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) rope_append_kernel(const __gr
 
     if (slot < 0) return;
     if (slot >= p.num_slots || (p.R && (pos < 0 || pos >= p.max_pos))) {
-        report(p.status, kDevBadPage);
+        report_bad_page(p.status);
         return;
     }
     uint16_t* y;

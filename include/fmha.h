@@ -302,9 +302,9 @@ int fmha_selftest(int which, const void* in, void* out, size_t out_bytes, int pa
  * Waits for `stream`, then returns FMHA_ERR_TIMEOUT if any kernel of this library timed out
  * in a bounded wait since the last call, FMHA_ERR_RACE if a split-KV merge found its arrival
  * counter changing under it (overlapping calls on one workspace), FMHA_ERR_PAGES if a paged-cache
- * call met device data out of bounds, clearing that state in all three cases.  Of several, RACE is
- * reported before TIMEOUT and TIMEOUT before PAGES: the results of calls that met data out of bounds are
- * defined, those of the other two are not.  FMHA_ERR_CUDA if the stream reports an error; else FMHA_OK.
+ * call met device data out of bounds, clearing that state in all three cases.  Of several, the
+ * latest of TIMEOUT and RACE is reported, and PAGES only after neither: the results of calls that met data
+ * out of bounds are defined, those of the other two are not.  FMHA_ERR_CUDA if the stream reports an error; else FMHA_OK.
  */
 int fmha_check_status(fmha_stream_t stream);
 
