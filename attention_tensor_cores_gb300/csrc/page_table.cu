@@ -15,9 +15,11 @@
 // a launch of several CTAs leaves them to a second launch when they are.
 //
 // Bound: launch latency and a chain of dependent loads (lengths, table or stack entry) for a decoding
-// step; 12 bytes written per token for prompts.  GPU time (without requests 1.8 us): 8 requests of a token 3.1 us,
-// 256 requests of which 32 end 4.8 (one CTA 7.2), 32 prompts of 131,000 tokens 4.6 (one CTA 120, a cluster of
-// eight 19).
+// step; 12 bytes written per token for prompts.  GPU time (without requests 1.8 us): 8 requests of a token 2.9 us,
+// 256 requests of which 32 end 4.6 (one CTA 7.2), 32 prompts of 131,000 tokens 4.4 (one CTA 120, a cluster of
+// eight 19).  An update in place is slower, as its CTAs may not write what others still read (separate arrays / in
+// place, pages of 16, a token each): 8 requests 3.1 / 3.4, 256 (pages of 64, 77 of padding) 3.7 / 4.2, 1024
+// 4.7 / 5.6, 2049 6.7 / 10.9; 32 prompts of 4000 tokens 4.0 / 6.9.
 #include <cuda_runtime.h>
 
 #include "fastdiv.cuh"

@@ -12,8 +12,9 @@
 //
 // Bound: HBM (every key and value row read once) where there are keys enough, else latency: about 4 us from
 // launch to the first S (lengths, split, page, K), a tile each 0.5 to 1 us, and 1 us of epilogue, 3 to 5 with a
-// merge.  B64 Hq32 Hkv8 D128, up to 32768 keys in pages of 16: 600 us, 7.2 TB/s = 1.05 of the measured copy
-// bandwidth (reads only); B8 Hq32 Hkv32 4096 keys: 82 us, 6.5 TB/s = 0.96; B1 Hq32 Hkv8 500 keys: 8.0 us.
+// merge.  B64 Hq32 Hkv8 D128, up to 32768 keys in pages of 16: 611 us, 7.0 TB/s = 1.03 of the measured copy
+// bandwidth (reads only); B8 Hq32 Hkv32 4096 keys: 82 us, 6.5 TB/s = 0.96 (84.7 a call live); B1 Hq32 Hkv8 500
+// keys: 8.1 us.
 #include <cuda_runtime.h>
 
 #include "decode_kernel.cuh"

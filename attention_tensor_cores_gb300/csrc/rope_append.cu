@@ -9,10 +9,10 @@
 //
 // Bound: HBM (every element read once and written once; a decoding step is latency-bound).  A CTA's life is
 // two dependent DRAM accesses (slot and position, then angles; the heads beside them) and little arithmetic, so
-// occupancy and loads in flight set the rate.  8192 tokens, 32 + 8 + 8 heads of 128, norm and rotation: 34.8 us,
-// 5.8 TB/s = 0.87 of the copy bandwidth.  On the way there: one head per group of threads 55.7 us; four heads in
+// occupancy and loads in flight set the rate.  8192 tokens, 32 + 8 + 8 heads of 128, norm and rotation: 34.8 to
+// 35.4 us, 5.8 TB/s = 0.85 to 0.87 of the copy bandwidth.  On the way there: one head per group of threads 55.7 us; four heads in
 // flight 48; the weights drawn into the angles, packed FP32 and five CTAs per SM 38.3 (four 41.5, six with
-// spills 43); the next heads fetched into L2 34.8.  8 tokens: 2.1 us of GPU time.
+// spills 43); the next heads fetched into L2 34.8.  8 tokens: 2.2 us of GPU time.
 #include <cuda_runtime.h>
 
 #include "fastdiv.cuh"

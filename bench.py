@@ -35,20 +35,20 @@ FALLBACK_PEAKS = {"hbm_gbs": 6800.0, "bf16_tflops": 1900.0, "bf16_tflops_sustain
 # reported only while those sources are unchanged.
 TRAFFIC = {
     # decode B8 H32 Sq1 Skv4096 D128 (decode_kernel<128, 0, 1, 0>, 128 CTAs of two whole units): read
-    # 537,031,168 + written 3,233,024 bytes (profiles/decode_kernel_decode-B8-H32-Skv4096-D128.md)
-    "decode_kernel<128>": {"bytes": 540264192, "source_sha": "709afd275356f11d"},
+    # 537,030,144 + written 2,933,248 bytes (profiles/decode_kernel_decode-B8-H32-Skv4096-D128.md)
+    "decode_kernel<128>": {"bytes": 539963392, "source_sha": "c6cd4045a971fbd8"},
     # ragged GQA decode B64 Hq32 Hkv8 Skv<=32768 D128 (decode_kernel<128, 0, 4, 0>): the quarter-size workload
-    # (B16) read 1,005,855,232 + wrote 384,256 bytes for 1,001,226,240 algorithmic K/V bytes (1.005x); scaled
+    # (B16) read 1,005,853,696 + wrote 381,696 bytes for 1,001,226,240 algorithmic K/V bytes (1.005x); scaled
     # by the K/V bytes to the full workload's 4,106,002,432 (profiles/side-kernels_ragged-decode-wide-combine-nvfp4.md)
-    "decode_kernel<128>/ragged": {"bytes": 4126561630, "source_sha": "709afd275356f11d"},
-    # speculative decode B8 Hq32 Hkv8 Sq4 Skv8192 D128, causal (decode_kernel<128, 1, 16, 0>): read 268,811,776 +
-    # written 2,683,904 bytes (profiles/decode_kernel_decode-B8-H32-Skv4096-D128.md)
-    "decode_kernel<128>/speculative": {"bytes": 271495680, "source_sha": "709afd275356f11d"},
-    # wide-head B32 Hq128 Hkv1 Skv16384 D512, independent CTAs: read 1,081,726,464 + written 10,248,960
+    "decode_kernel<128>/ragged": {"bytes": 4126544832, "source_sha": "c6cd4045a971fbd8"},
+    # speculative decode B8 Hq32 Hkv8 Sq4 Skv8192 D128, causal (decode_kernel<128, 1, 16, 0>): read 268,808,192 +
+    # written 2,878,208 bytes (profiles/decode_kernel_decode-B8-H32-Skv4096-D128.md)
+    "decode_kernel<128>/speculative": {"bytes": 271686400, "source_sha": "c6cd4045a971fbd8"},
+    # wide-head B32 Hq128 Hkv1 Skv16384 D512, independent CTAs: read 1,081,724,928 + written 10,330,368
     # bytes (profiles/wide_kernel_wide-head-B32-Hq128-Hkv1-Skv16384-D512.md)
-    "wide_kernel<independent>": {"bytes": 1091975424, "source_sha": "78a9a91c90649bc2"},
-    # same workload, CTA-pair MMA: read 1,081,783,808 + written 10,341,632 bytes (same file)
-    "wide_kernel<pair>": {"bytes": 1092125440, "source_sha": "78a9a91c90649bc2"},
+    "wide_kernel<independent>": {"bytes": 1092055296, "source_sha": "ac65112b3ad87a06"},
+    # same workload, CTA-pair MMA: read 1,081,825,280 + written 10,803,968 bytes (same file)
+    "wide_kernel<pair>": {"bytes": 1092629248, "source_sha": "ac65112b3ad87a06"},
 }
 
 

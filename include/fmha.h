@@ -52,7 +52,9 @@ typedef enum {
     FMHA_ERR_TIMEOUT = 5,     /* a kernel's bounded wait expired (see fmha_check_status) */
     FMHA_ERR_RACE = 6,        /* a split-KV merge counter never settled: calls sharing one
                                  workspace (or the allocation-free scratch) overlapped on the
-                                 GPU, so some output rows may be unmerged (see fmha_check_status) */
+                                 GPU, so some output rows may be unmerged (see fmha_check_status).
+                                 Make the call once eagerly before a captured one of that workspace
+                                 is replayed: that clears the arrivals a replay would take up */
     FMHA_ERR_PAGES = 7        /* a paged-cache call met data out of bounds on the device: a length, page,
                                  slot or position, or too few free pages (see fmha_check_status) */
 } fmha_status;
