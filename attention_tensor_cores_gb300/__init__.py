@@ -118,6 +118,11 @@ def load(path: str | None = None):
             "fmha_rope_append": ([V, I64, V, I64, V, I64, V, V, F, V, I, I, I, V, V, V, ctypes.POINTER(fmha_kv_cache), I, I, I, V], I),
             "fmha_fwd_paged": ([V, ctypes.POINTER(fmha_kv_cache), V, I, V, V, V, I, I, I, F, V, ctypes.POINTER(fmha_opts)], I),
             "fmha_paged_workspace_size": ([I, I, I, ctypes.POINTER(fmha_kv_cache), ctypes.POINTER(fmha_opts)], S),
+            "fmha_fwd_prefix": ([V, ctypes.POINTER(fmha_kv_cache), V, I, V, V, V, I, V, V, I, I, I, F, V, ctypes.POINTER(fmha_opts)], I),
+            "fmha_prefix_workspace_size": ([I, I, I, ctypes.POINTER(fmha_kv_cache), ctypes.POINTER(fmha_opts)], S),
+            "fmha_page_fork": ([V, I, V, I, I, V, I, V, V, I, V, V, V, V, V, V, V], I),
+            "fmha_page_copy": ([ctypes.POINTER(fmha_kv_cache), I, V, V, V, I, V, V], I),
+            "fmha_page_compact": ([V, I, I, V, I, V, V, I, V, V, V, V, I, V, V, V], I),
             "fmha_fwd_decode_noalloc": ([V, V, V, V, V, I, I, I, I, I, I, F, V, V], I),
         }
         for name, (args, res) in sig.items():
@@ -308,7 +313,8 @@ def _native():
         except ImportError as e:
             raise FmhaError(FMHA_ERR_CUDA, f"_binding.so not built for this torch: run attention_tensor_cores_gb300/build.py ({e})")
         ext.bind(FmhaError, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
-            lib.fmha_page_table, lib.fmha_rope_append, lib.fmha_fwd_paged, lib.fmha_last_error, lib.fmha_error_string)))
+            lib.fmha_page_table, lib.fmha_rope_append, lib.fmha_fwd_paged, lib.fmha_fwd_prefix, lib.fmha_page_fork, lib.fmha_page_copy,
+            lib.fmha_page_compact, lib.fmha_last_error, lib.fmha_error_string)))
         _ext = ext
     return _ext
 
@@ -363,3 +369,40 @@ def fmha_fwd_paged(q, cache: fmha_kv_cache, block_table, seqlens, out, lse, scal
     """Attention of q [B, Hq, Sq, D] over the first seqlens[b] tokens of each request's pages, block_table
     int32 [B, max_pages]; out per opts.out_kind, lse FP32 [B, Hq, Sq] or None (see make_opts, make_kv_cache)."""
     (_ext or _native()).fwd_paged(q, cache, block_table, seqlens, out, lse, scale, opts, stream)
+
+
+# ------------------------------------------------------------------------------------------------
+# pages that requests share
+# ------------------------------------------------------------------------------------------------
+def fmha_prefix_workspace_size(B, Hq, Sq, cache: fmha_kv_cache, opts: fmha_opts | None = None) -> int:
+    return int(load().fmha_prefix_workspace_size(B, Hq, Sq, ctypes.byref(cache), None if opts is None else ctypes.byref(opts)))
+
+
+def fmha_fwd_prefix(q, cache: fmha_kv_cache, block_table, seqlens, cu_groups, prefix_lens, out, lse, scale: float,
+                    opts: fmha_opts | None = None, stream=None):
+    """fmha_fwd_paged for groups of requests, cu_groups int32 [N + 1], whose first prefix_lens [N] tokens are in the same
+    pages: those are read once for the group.  opts needs a workspace of fmha_prefix_workspace_size bytes."""
+    (_ext or _native()).fwd_prefix(q, cache, block_table, seqlens, cu_groups, prefix_lens, out, lse, scale, opts, stream)
+
+
+def fmha_page_fork(parents, ctx_lens, page_size: int, block_table, free_pages, free_count, new_table, seqlens, copy_src, copy_dst,
+                   copy_tokens, free_count_out, stream=None):
+    """The requests parents [B] (negative: an empty slot) of this step's ctx_lens [B_old], block_table [B_old, max_pages] as the next
+    step's: new_table [B, max_pages], seqlens [B], the pages to be copied (copy_src, copy_dst, copy_tokens [B]) and the stack of
+    free pages; all int32."""
+    (_ext or _native()).page_fork(parents, ctx_lens, page_size, block_table, free_pages, free_count, new_table, seqlens, copy_src,
+                                  copy_dst, copy_tokens, free_count_out, stream)
+
+
+def fmha_page_copy(caches, src, dst, tokens=None, count=None, stream=None):
+    """Copies the first tokens[i] tokens (None: all) of page src[i] to page dst[i], int32 [n], in each of the caches (a list: a
+    model's layers); only the first count [1] pairs if given."""
+    (_ext or _native()).page_copy(caches, src, dst, tokens, count, stream)
+
+
+def fmha_page_compact(seqlens, page_size: int, block_table, free_pages, free_count, new_ids, new_table, copy_src, copy_dst, copy_count,
+                      free_pages_out, stream=None):
+    """Used pages to the low ids: new_ids [num_pages], new_table [B, max_pages], the moves (copy_src, copy_dst of at least num_pages / 2
+    entries, copy_count [1]) and free_pages_out [num_pages]; all int32."""
+    (_ext or _native()).page_compact(seqlens, page_size, block_table, free_pages, free_count, new_ids, new_table, copy_src, copy_dst,
+                                     copy_count, free_pages_out, stream)

@@ -1,0 +1,210 @@
+// Used pages to the low ids (fmha_page_compact): where each goes, the block table that says so, the moves and
+// the stack of free pages.
+//
+// With n free pages of N, U = N - n are used.  The k-th used page with an id of at least U (ascending) moves to the
+// k-th free id below U; as many of either exist.  With f(x) the number of free pages below x, a used page x >= U is
+// the (x - U - (f(x) - f(U)))-th to move, and f(U) pages move in all.
+//
+// One launch of clusters of eight CTAs.  Each cluster reads the whole stack into a set of bits spread over its
+// shared memory, then each of its CTAs takes a copy of the set and sums it in blocks of 256 pages: f is a sum and
+// up to eight popcounts, its inverse a binary search and as many.  Everything else is a lookup per output.
+// Bound: latency, stack -> set -> copy -> outputs, with two cluster barriers.
+#include <cuda_runtime.h>
+
+#include "cluster_bits.cuh"
+#include "fastdiv.cuh"
+#include "paged.h"
+#include "ptx.cuh"
+
+namespace atc_gb300 {
+namespace {
+
+constexpr int kCompactThreads = 1024;
+
+struct CompactParams {
+    const int32_t* seqlens;
+    int B, page;
+    FastDiv by_page;
+    const int32_t* table;
+    int max_pages;
+    const int32_t* free_pages;
+    const int32_t* free_count;
+    int num_pages;
+    int32_t* new_ids;
+    int32_t* new_table;
+    int32_t* src;
+    int32_t* dst;
+    int cap;
+    int32_t* moves;
+    int32_t* free_out;
+    int* status;
+    int words;    // of each CTA's part of the set
+    int blocks;   // runs of 256 pages
+};
+
+__global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kCompactThreads, 1)
+    page_compact_kernel(const __grid_constant__ CompactParams p)
+{
+    extern __shared__ uint32_t shm[];
+    uint32_t* part = shm;                                                          // this CTA's part of the set
+    uint32_t* bits = shm + p.words;                                                // all of it
+    int* below = reinterpret_cast<int*>(bits + static_cast<size_t>(p.blocks) * 8);  // free pages before each block
+    __shared__ int sums[32], bad_at[1];
+    griddep_launch_dependents();
+    const int tid = threadIdx.x, lane = tid & 31, N = p.num_pages;
+    const int rank = static_cast<int>(cluster_ctarank());
+    for (int i = tid; i < p.words; i += kCompactThreads) part[i] = 0;
+    if (tid == 0) bad_at[0] = 0;
+    griddep_wait();
+    cluster_sync();   // every CTA's words are zero
+
+    const int n = *p.free_count;
+    const PageBits set{smem_u32(part), p.words};
+    const long long room = static_cast<long long>(p.max_pages) * p.page;
+    bool bad = n < 0 || n > N;
+    const auto fine = [&](int page) { return page >= 0 && page < N; };
+    if (!bad)
+#pragma unroll 4
+        for (int i = rank * kCompactThreads + tid; i < n; i += kClusterCtas * kCompactThreads) {
+            const int x = p.free_pages[i];
+            if (!fine(x) || set.test_set(x)) bad = true;   // not a page, or twice on the stack
+        }
+    for (int b = tid; b < p.B; b += kCompactThreads) {
+        const int c = p.seqlens[b];
+        bad = bad || c < 0 || c > room;
+    }
+    bad = __syncthreads_or(bad);
+    if (tid < kClusterCtas && bad) st_cluster(mapa_shared(smem_u32(&bad_at[0]), static_cast<uint32_t>(tid)), 1u);
+    cluster_sync();   // the set is complete
+    for (int i = tid; i < p.blocks * 8; i += kCompactThreads) {
+        const int r = i / p.words;
+        bits[i] = r < kClusterCtas ? ld_cluster(mapa_shared(smem_u32(part + (i - r * p.words)), static_cast<uint32_t>(r))) : 0u;
+    }
+    cluster_sync();   // nobody looks into another CTA's memory from here on
+    bad = bad_at[0] != 0;
+
+    const auto count_block = [&](int k) {
+        int c = 0;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) c += __popc(bits[k * 8 + w]);
+        return c;
+    };
+    const int per = (p.blocks + kCompactThreads - 1) / kCompactThreads;
+    const int k0 = min(p.blocks, tid * per), k1 = min(p.blocks, k0 + per);
+    int own = 0, total;
+    for (int k = k0; k < k1; ++k) own += count_block(k);
+    int at = block_scan(own, sums, total);
+    for (int k = k0; k < k1; ++k) {
+        below[k] = at;
+        at += count_block(k);
+    }
+    __syncthreads();
+
+    const auto is_free = [&](int x) { return (bits[x >> 5] >> (x & 31)) & 1; };
+    // free pages below x < N
+    const auto free_below = [&](int x) {
+        int c = below[x >> 8];
+        for (int w = (x >> 8) * 8; w < x >> 5; ++w) c += __popc(bits[w]);
+        return c + __popc(bits[x >> 5] & ((1u << (x & 31)) - 1));
+    };
+    // the k-th free page
+    const auto nth_free = [&](int k) {
+        int lo = 0, hi = p.blocks - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (below[mid] <= k) lo = mid; else hi = mid - 1;
+        }
+        k -= below[lo];
+        int w = lo * 8;
+        for (int c; k >= (c = __popc(bits[w])); ++w) k -= c;
+        uint32_t v = bits[w];
+        for (; k > 0; --k) v &= v - 1;
+        return w * 32 + __ffs(v) - 1;
+    };
+    const int U = N - n;
+    const int M = bad || U == N ? 0 : free_below(U);
+    // a used page's place among those that move
+    const auto mover = [&](int x) { return x - U - (free_below(x) - M); };
+
+    const int first = blockIdx.x * kCompactThreads + tid, step = gridDim.x * kCompactThreads;
+    for (int x = first; x < N; x += step) {
+        int to = x;
+        if (!bad) {
+            if (is_free(x)) {
+                to = -1;
+            } else if (x >= U) {
+                const int k = mover(x);
+                to = nth_free(k);
+                p.src[k] = x;
+                p.dst[k] = to;
+            }
+        }
+        p.new_ids[x] = to;
+        if (x < n) p.free_out[x] = bad ? p.free_pages[x] : N - 1 - x;
+    }
+    for (int k = M + first; k < p.cap; k += step) p.src[k] = p.dst[k] = -1;
+    if (first == 0) {
+        *p.moves = M;
+        if (bad) report_bad_page(p.status);
+    }
+    // a warp per request: its row
+    bool odd = false;
+    for (int b = first / 32; b < p.B; b += step / 32) {
+        const long long len = p.seqlens[b], held_tokens = len < 0 ? 0 : len > room ? room : len;
+        const int k = p.by_page.up(static_cast<int>(held_tokens));
+        const size_t row = static_cast<size_t>(b) * p.max_pages;
+#pragma unroll 4
+        for (int j = lane; j < k; j += 32) {
+            const int x = p.table[row + j];
+            int to = x;
+            if (!fine(x) || (!bad && is_free(x)))
+                odd = true;
+            else if (!bad && x >= U)
+                to = nth_free(mover(x));
+            p.new_table[row + j] = to;
+        }
+    }
+    if (odd) report_bad_page(p.status);
+}
+
+}  // namespace
+}  // namespace atc_gb300
+
+using namespace atc_gb300;
+
+extern "C" int fmha_page_compact(const int32_t* seqlens, int B, int page_size, const int32_t* block_table, int max_pages,
+                                 const int32_t* free_pages, const int32_t* free_count, int num_pages, int32_t* new_ids, int32_t* new_table,
+                                 int32_t* copy_src, int32_t* copy_dst, int n_copies, int32_t* copy_count, int32_t* free_pages_out,
+                                 fmha_stream_t stream)
+{
+    if (B < 0 || page_size < 1 || num_pages < 1 || max_pages < 1 || n_copies < num_pages / 2)
+        return set_error(FMHA_ERR_INVALID, "fmha_page_compact: need B >= 0, page_size, num_pages and max_pages >= 1, n_copies >= num_pages / 2");
+    if (!free_pages || !free_count || !new_ids || !copy_count || !free_pages_out || (n_copies > 0 && (!copy_src || !copy_dst)) ||
+        (B > 0 && (!seqlens || !block_table || !new_table)))
+        return set_error(FMHA_ERR_INVALID, "fmha_page_compact: NULL pointer");
+    for (const void* x : {static_cast<const void*>(seqlens), static_cast<const void*>(block_table), static_cast<const void*>(free_pages),
+                          static_cast<const void*>(free_count), static_cast<const void*>(new_ids), static_cast<const void*>(new_table),
+                          static_cast<const void*>(copy_src), static_cast<const void*>(copy_dst), static_cast<const void*>(copy_count),
+                          static_cast<const void*>(free_pages_out)})
+        if (misaligned(x, 4)) return set_error(FMHA_ERR_INVALID, "fmha_page_compact: arrays must be 4-byte aligned");
+    if (free_pages_out == free_pages || (B > 0 && new_table == block_table))
+        return set_error(FMHA_ERR_INVALID, "fmha_page_compact: new_table and free_pages_out must not be block_table and free_pages");
+    if (static_cast<long long>(max_pages) * page_size > (1LL << 31) - 256 || num_pages > kMaxPoolPages || n_copies > (1 << 30) || B > (1 << 24))
+        return set_error(FMHA_ERR_UNSUPPORTED, "fmha_page_compact: max_pages * page_size past 2^31, more than 2^20 pages, 2^24 requests or 2^30 copies");
+    int* status = device_status_ptr();
+    if (!status) return set_error(FMHA_ERR_CUDA, "no CUDA device");
+    const int words = (num_pages + 32 * kClusterCtas - 1) / (32 * kClusterCtas), blocks = (num_pages + 255) / 256;
+    const CompactParams p{seqlens, B, page_size, FastDiv(static_cast<uint32_t>(page_size)), block_table, max_pages, free_pages, free_count,
+                          num_pages, new_ids, new_table, copy_src, copy_dst, n_copies, copy_count, free_pages_out, status, words, blocks};
+    // a cluster for each 65536 outputs
+    const long long outputs = 3LL * num_pages + static_cast<long long>(B) * max_pages;
+    const int most = num_sms() / kClusterCtas;
+    const int clusters = static_cast<int>(1 + outputs / 65536 < most ? 1 + outputs / 65536 : most);
+    const int smem = 4 * words + 36 * blocks;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    FMHA_CHECK_CUDA(set_smem_limit_once(reinterpret_cast<const void*>(page_compact_kernel), kMaxPoolPages / 8 / kClusterCtas + 36 * (kMaxPoolPages / 256)));
+    FMHA_CHECK_CUDA(launch_pdl(page_compact_kernel, dim3(static_cast<unsigned>((clusters > 0 ? clusters : 1) * kClusterCtas)), dim3(kCompactThreads),
+                               static_cast<size_t>(smem), st, p));
+    count_launch();
+    return FMHA_OK;
+}

@@ -92,27 +92,6 @@ PagedWs paged_ws(int B, int Hq, int Sq, const fmha_kv_cache* c, const fmha_opts*
     return w;
 }
 
-// D = 128: runs of 8 keys from one page to the next
-int64_t page_groups(const fmha_kv_cache* c) { return c->num_pages > 1 ? c->page_stride / (8 * c->token_stride) : c->page_size / 8; }
-
-int make_pool_map(CUtensorMap* map, const void* pool, const fmha_kv_cache* c, int box)
-{
-    if (c->D == 128) {
-        const uint64_t dims[5] = {64, 8, 2, static_cast<uint64_t>((c->num_pages - 1) * page_groups(c) + c->page_size / 8),
-                                  static_cast<uint64_t>(c->Hkv)};
-        const uint64_t strides[4] = {static_cast<uint64_t>(c->token_stride) * 2, 128, static_cast<uint64_t>(c->token_stride) * 16,
-                                     static_cast<uint64_t>(c->head_stride) * 2};
-        const uint32_t boxes[5] = {64, 8, 2, static_cast<uint32_t>(box / 8), 1};
-        return make_tmap_bf16(map, pool, 5, dims, strides, boxes);
-    }
-    const uint64_t dims[4] = {static_cast<uint64_t>(c->D), static_cast<uint64_t>(c->page_size), static_cast<uint64_t>(c->Hkv),
-                              static_cast<uint64_t>(c->num_pages)};
-    const uint64_t strides[3] = {static_cast<uint64_t>(c->token_stride) * 2, static_cast<uint64_t>(c->head_stride) * 2,
-                                 static_cast<uint64_t>(c->page_stride) * 2};
-    const uint32_t boxes[4] = {64, static_cast<uint32_t>(box), 1, 1};
-    return make_tmap_bf16(map, pool, 4, dims, strides, boxes);
-}
-
 template <int D, bool CAUSAL>
 auto kernel_for(int G) -> decltype(&decode_kernel<D, CAUSAL, 1, true>)
 {
@@ -141,8 +120,7 @@ int run_paged(const PagedArgs& a, bool split, const PagedWs& w, uint8_t* base, c
         const int rc = make_tmap_bf16(&qmap, a.q, 3, dims, strides, box);
         if (rc) return rc;
     }
-    int box = kTileKV;
-    while (a.c->page_size % box) box >>= 1;
+    const int box = page_box(a.c);
     int rc = make_pool_map(&kmap, a.c->k, a.c, box);
     if (rc) return rc;
     rc = make_pool_map(&vmap, a.c->v, a.c, box);
@@ -217,11 +195,8 @@ int check_paged(const fmha_kv_cache* c, int B, int Hq, int Sq, int max_pages, co
     const char* who = "fmha_fwd_paged";
     if (B < 0 || Hq <= 0 || Sq < 0 || max_pages < 1 || Hq % c->Hkv != 0)
         return set_error(FMHA_ERR_INVALID, std::string(who) + ": need B >= 0, Sq >= 0, max_pages >= 1, Hq > 0 a multiple of Hkv");
-    if (c->page_size % 8 != 0) return set_error(FMHA_ERR_UNSUPPORTED, std::string(who) + ": page_size must be a multiple of 8");
-    if (c->D == 128 && c->num_pages > 1 &&
-        (c->page_stride % (8 * c->token_stride) != 0 || page_groups(c) < c->page_size / 8 || page_groups(c) * (c->num_pages + 1LL) >= (1LL << 31)))
-        return set_error(FMHA_ERR_UNSUPPORTED, std::string(who) + ": with D = 128, page_stride must be a multiple of 8 * token_stride that "
-                                                                  "holds a page, and the pool less than 2^31 runs of 8 tokens");
+    const int rc = check_tiles(c, who);
+    if (rc) return rc;
     const long long cap = static_cast<long long>(max_pages) * c->page_size;
     const long long rows = static_cast<long long>(B) * Hq * Sq;
     const long long units = static_cast<long long>(B) * c->Hkv * ((static_cast<long long>(Hq / c->Hkv) * Sq + kN - 1) / kN);

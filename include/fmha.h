@@ -198,7 +198,9 @@ int nvfp4_quantize_scaled(const float* x, uint8_t* q, uint8_t* scales, int64_t n
  * token's place in the pool, page * page_size + token.
  *
  * A step of serving is fmha_page_table (pages and slots for the new tokens), then in every layer
- * fmha_rope_append (queries, and keys and values into the cache) and fmha_fwd_paged.  All three are
+ * fmha_rope_append (queries, and keys and values into the cache) and fmha_fwd_paged.  Where several
+ * requests continue one prompt, fmha_page_fork and fmha_page_copy go before them, the requests hold the
+ * pages of their common beginning together, and fmha_fwd_prefix reads those once.  All are
  * stream-ordered, allocate nothing and can be captured.  Data on the device that is out of bounds (a
  * length, page, slot or position) is never followed: the call does what its text says and
  * fmha_check_status reports FMHA_ERR_PAGES.
@@ -283,6 +285,96 @@ int fmha_fwd_paged(const void* q, const fmha_kv_cache* cache, const int32_t* blo
 
 /* Bytes of workspace fmha_fwd_paged needs for this problem and these options (0 if none or invalid). */
 size_t fmha_paged_workspace_size(int B, int Hq, int Sq, const fmha_kv_cache* cache, const fmha_opts* opts);
+
+/*
+ * ---- Pages that requests share ---------------------------------------------------------------------
+ * Requests that continue one prompt (parallel samples, beams, a common system prompt) may have the same
+ * pages at the beginning of their rows of the block table.  Who holds a page stands in the table alone:
+ * there are no reference counts.  Pages that several requests hold are full and are not written any more;
+ * a partly filled page belongs to one request.  fmha_page_fork keeps it so.  Requests that share pages end
+ * through fmha_page_fork, as fmha_page_table gives back every page of a request that ends.
+ */
+
+/*
+ * Attention of the last Sq tokens of each request over its pages, as fmha_fwd_paged, with the common
+ * beginning of the requests of a group read once for all of them.
+ *   cu_groups: int32[N + 1], first request of each group and B; N >= 1 groups (at most 8192) of neighbouring
+ *   requests, in order, that make up the batch; a group may have one request, or none.
+ *   prefix_lens: int32[N], tokens that the group's requests have in the same pages: the rows of the block table
+ *   agree there, as far as each request's tokens reach (a request may end inside, and an empty slot has none).
+ *   They are read through the row of the group's first request, so as far as its tokens reach (the other requests
+ *   read what is left through their own rows).
+ *   q, cache, block_table, max_pages, seqlens, out, lse, scale: as in fmha_fwd_paged, and the same results within
+ *   rounding.  At most 64 rows per key/value head, (Hq / Hkv) * Sq, are shared; with more every request
+ *   is read by itself, in chunks of up to 128 rows.
+ *   opts: out_kind, workspace (always needed: fmha_prefix_workspace_size() bytes), causal and the NVFP4 fields;
+ *   num_splits 0 (or above 1); seqlens_k must be NULL.
+ * Lengths and pages out of bounds as in fmha_fwd_paged; with cu_groups that is no such list nothing is
+ * shared; each is reported.  A prefix length below 0 is 0.
+ */
+int fmha_fwd_prefix(const void* q, const fmha_kv_cache* cache, const int32_t* block_table, int max_pages,
+                    const int32_t* seqlens, const int32_t* cu_groups, const int32_t* prefix_lens, int N, void* out, float* lse,
+                    int B, int Hq, int Sq, float scale, fmha_stream_t stream, const fmha_opts* opts);
+
+/* Bytes of workspace fmha_fwd_prefix needs for this problem and these options (0 if none or invalid). */
+size_t fmha_prefix_workspace_size(int B, int Hq, int Sq, const fmha_kv_cache* cache, const fmha_opts* opts);
+
+/*
+ * The next step's B requests as children of this step's B_old (at most 8192 each), in one launch: the
+ * choice of a beam search, a prompt forked into samples, requests that end, a batch put in another order.
+ *   parents: int32[B], the request that child b continues, or a negative number: an empty slot.
+ *   ctx_lens: int32[B_old], tokens in the cache; block_table: int32[B_old][max_pages]; page_size.
+ *   free_pages, free_count, num_pages (at most 2^20): the stack of free pages, as in fmha_page_table.
+ * A child has its parent's tokens and pages, except that of several children of one parent all but the first
+ * get a page of their own in place of a partly filled last one, whose tokens are to be copied (fmha_page_copy).
+ * A request without children ends.  First the pages that rows of ended requests name and no row of a
+ * continued one does are pushed, in the order of their ids; then the copies' pages are taken from the top,
+ * in the order of the children.
+ * Outputs: new_table: int32[B][max_pages], the entries of each child's pages (no other is written); seqlens[b];
+ *   copy_src[b], copy_dst[b] and copy_tokens[b]: the page to be copied, to which, and how many tokens of it (-1, -1, 0:
+ *   none); *free_count_out, the stack's new height (may be free_count; no other arrays may overlap).
+ * With a parent that is not one of the B_old, a length that is negative or passes the table row, a stack height
+ * outside 0..num_pages or passing it, or too few free pages, the stack stays as it was, seqlens are 0, the copies none,
+ * new_table holds nothing of use, and FMHA_ERR_PAGES is reported: the old table still stands.  An id that is not one
+ * of the pool's pages is handed on to children, not given back, and reported.
+ * All arrays device memory, 4-byte aligned.
+ */
+int fmha_page_fork(const int32_t* parents, int B, const int32_t* ctx_lens, int B_old, int page_size, const int32_t* block_table,
+                   int max_pages, int32_t* free_pages, const int32_t* free_count, int num_pages, int32_t* new_table,
+                   int32_t* seqlens, int32_t* copy_src, int32_t* copy_dst, int32_t* copy_tokens, int32_t* free_count_out,
+                   fmha_stream_t stream);
+
+/*
+ * Copies pages inside each of n_caches caches (a model's layers, of one size and the same strides; the array is read
+ * on the host): the first tokens[i] tokens (NULL: all) of page src[i], all heads, keys and values, to page dst[i],
+ * i < n, or i < *count if count is given (device int32[1], 0..n).  A pair with a negative page is left out.
+ * No page may be a destination twice, or source and destination.  A page outside the pool is left out, a
+ * number of tokens or pairs outside its range clamped, and each is reported.
+ * src, dst, tokens: int32[n], device memory, 4-byte aligned.
+ */
+int fmha_page_copy(const fmha_kv_cache* caches, int n_caches, const int32_t* src, const int32_t* dst, const int32_t* tokens, int n,
+                   const int32_t* count, fmha_stream_t stream);
+
+/*
+ * Used pages to the low ids, in one launch: with n = *free_count of num_pages (at most 2^20) pages free, the used ones
+ * end up in 0 .. num_pages - n - 1.  The k-th used page behind them moves to the k-th free page among them.  The data
+ * moves with fmha_page_copy(copy_src, copy_dst, NULL, n_copies, copy_count) in every layer.
+ *   seqlens: int32[B], tokens of each request; block_table: int32[B][max_pages]; free_pages: int32[num_pages].
+ * A page that is not on the stack is used, whether or not a request names it.
+ * Outputs: new_ids: int32[num_pages], where each page goes (itself if it stays; -1: free); new_table: int32[B][max_pages],
+ *   block_table's entries of each request's pages with their new ids (no other is written); copy_src, copy_dst: int32[n_copies],
+ *   n_copies >= num_pages / 2, the *copy_count moves, and -1 behind them; free_pages_out: the stack, the lowest free page
+ *   on top, the same number of pages (its entries above are not written).  No arrays may overlap.
+ * With a stack height outside 0..num_pages, an entry that is not one of the pool's pages or is twice on the stack, or a
+ * length that is negative or passes the table row, nothing moves (new_ids, tables and stack as they are, no copies)
+ * and FMHA_ERR_PAGES is reported.  An entry of the table that is no page of the pool, or a free one, is
+ * handed on and reported.
+ * All arrays device memory, 4-byte aligned.
+ */
+int fmha_page_compact(const int32_t* seqlens, int B, int page_size, const int32_t* block_table, int max_pages,
+                      const int32_t* free_pages, const int32_t* free_count, int num_pages, int32_t* new_ids, int32_t* new_table,
+                      int32_t* copy_src, int32_t* copy_dst, int n_copies, int32_t* copy_count, int32_t* free_pages_out,
+                      fmha_stream_t stream);
 
 /*
  * Test hook: raw S = Q K^T in FP32, no scale ("CURRENT_ISSUE.md" @57d67e6, "The 4x Bug":

@@ -1,0 +1,198 @@
+"""Attention of groups of requests that share their first pages (fmha_fwd_prefix) against the 64-bit statement.
+
+Tolerances are check_attention's: the kernel rounds each weight to two BF16 (2^-17) and the output once, and sums in FP32
+over tiles of 128 keys, as the paged attention does; merging partials adds a few 2^-23 of them.
+"""
+import math
+
+import pytest
+import torch
+
+import attention_tensor_cores_gb300 as F
+from paged_util import attention_ref, check_attention
+from shared_util import Groups
+
+pytestmark = pytest.mark.gpu
+
+
+def call(q, gr, cache=None, causal=False, scale=None, kind=F.FMHA_OUT_BF16, fill=None, **kw):
+    B, Hq, Sq, D = q.shape
+    cache = cache or F.make_kv_cache(gr.k, gr.v)
+    need = F.fmha_prefix_workspace_size(B, Hq, Sq, cache, F.make_opts(out_kind=kind, causal=causal))
+    ws = torch.full((need,), 0xff, dtype=torch.uint8, device="cuda")       # NaN wherever a partial is not written
+    out = torch.full(q.shape, float("nan"), dtype=torch.float32 if kind == F.FMHA_OUT_F32 else torch.bfloat16, device="cuda")
+    lse = torch.full(q.shape[:3], float("nan"), device="cuda")
+    F.fmha_fwd_prefix(q, cache, gr.table, gr.seqlens, gr.cu, gr.prefix_lens, out, lse, scale or D ** -0.5,
+                      F.make_opts(out_kind=kind, workspace=ws, causal=causal), **kw)
+    return out, lse
+
+
+def run(lens, prefix, P=16, Hq=8, Hkv=2, Sq=1, D=64, layout="hnd", causal=False, kind=F.FMHA_OUT_BF16, seed=1, scale=1.0):
+    gr = Groups(lens, prefix, P, Hkv, D, layout, seed, scale)
+    g = torch.Generator().manual_seed(seed + 1)
+    q = torch.randn(len(gr.lens), Hq, Sq, D, generator=g).to(torch.bfloat16)
+    out, lse = call(q.cuda(), gr, causal=causal, kind=kind)
+    assert F.fmha_check_status() == F.FMHA_OK
+    ref = attention_ref(q, *gr.dense, gr.lens, D ** -0.5, causal)
+    check_attention(out, lse, ref, bf16=kind == F.FMHA_OUT_BF16, what=f"{lens} {prefix}")
+    return gr, q, out, lse
+
+
+def test_one_group_one_tile():
+    run([[600, 590]], [512], D=128)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens, prefix", [
+    ([[1]], [0]), ([[128]], [0]), ([[129]], [128]), ([[500]], [0]),                      # a request alone
+    ([[513, 700, 900, 514]], [512]), ([[512, 512]], [512]), ([[640, 641]], [528]),       # all, none or a part of a tile behind the prefix
+    ([[2000, 0, 300, 100]], [1600]), ([[0, 2000, 1900]], [1600]), ([[90, 2000, 1900]], [1600]),   # empty slots, requests that end inside
+    ([[0, 0, 0]], [0]), ([[0], [0, 0], [5]], [0, 0, 0]),
+    ([[1300] * 3, [], [700, 701], [40], [2100] * 5], [1024, 0, 688, 0, 2096])])
+def test_lengths(lens, prefix, D):
+    run(lens, prefix, D=D)
+
+
+@pytest.mark.parametrize("Hq, Hkv, Sq", [(1, 1, 1), (2, 2, 1), (8, 1, 1), (16, 1, 1), (7, 1, 1), (6, 2, 2), (14, 2, 3), (4, 1, 4), (8, 8, 4),
+                                         (32, 1, 2), (64, 1, 1), (16, 1, 4), (33, 1, 2), (65, 1, 1), (128, 1, 1), (40, 1, 4), (64, 1, 5)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_heads_and_rows(Hq, Hkv, Sq, causal):
+    if causal and Sq == 1:
+        pytest.skip("one query sees every key either way")
+    run([[1300, 1200, 1157, 1280, 1153], [400, 390]], [1152, 384], Hq=Hq, Hkv=Hkv, Sq=Sq, causal=causal, D=64 if Hq % 2 else 128)
+
+
+@pytest.mark.parametrize("Sq", [2, 4, 16])
+def test_causal_rows_that_end_inside_the_prefix(Sq):
+    # the first request reaches to the prefix's end, so its earlier queries do not see all of it; a request shorter than Sq
+    # has queries that see nothing
+    run([[640, 641, 643, 700, 3, Sq, 0, 512, 513]], [640], Hq=4, Hkv=2, Sq=Sq, causal=True, D=64)
+
+
+@pytest.mark.parametrize("P", [8, 24, 40, 48, 64, 128, 256, 1000])
+@pytest.mark.parametrize("layout", ["hnd", "nhd", "kv"])
+def test_pages(P, layout):
+    p = 1000 // P * P
+    run([[p + 37, p + 1, p + 500], [p + 2, p]], [p, p], P=P, layout=layout, D=128 if P in (24, 64, 1000) else 64)
+
+
+@pytest.mark.parametrize("members", [2, 31, 32, 33, 64, 100])
+def test_many_requests(members):
+    run([[700 + 3 * i for i in range(members)]], [640], Hq=8, Hkv=2)
+
+
+@pytest.mark.parametrize("B", [383, 384, 385, 1000])
+def test_many_groups(B):
+    # more entries than threads: runs of them per thread
+    groups = [[140 + i % 7, 150, 141][:1 + i % 3] for i in range(B // 2)]
+    run(groups, [128] * len(groups), Hq=2, Hkv=1)
+    run([[n] for n in range(B)], [0] * B, Hq=2, Hkv=1)
+
+
+def test_long_prefix_over_every_sm():
+    run([[20000 + i for i in range(8)]], [19968], Hq=4, Hkv=1, D=128)
+
+
+@pytest.mark.parametrize("scale", [0.1, 8.0])
+def test_reference_moves(scale):
+    # large scores: the running maximum moves, and partials of very different weights meet
+    run([[1500, 1400, 1300]], [1280], scale=scale)
+
+
+@pytest.mark.parametrize("kind", [F.FMHA_OUT_F32])
+def test_fp32_output(kind):
+    run([[700, 800, 650], [50], [0]], [640, 0, 0], kind=kind, D=128)
+
+
+def test_same_as_paged_attention():
+    gr, q, out, lse = run([[3000 + 11 * i for i in range(16)], [77], [400, 500]], [2992, 0, 400], Hq=32, Hkv=8, D=128)
+    cache = F.make_kv_cache(gr.k, gr.v)
+    ws = torch.empty(F.fmha_paged_workspace_size(len(gr.lens), 32, 1, cache, F.make_opts()), dtype=torch.uint8, device="cuda")
+    o2, l2 = torch.empty_like(out), torch.empty_like(lse)
+    F.fmha_fwd_paged(q.cuda(), cache, gr.table, gr.seqlens, o2, l2, 128 ** -0.5, F.make_opts(workspace=ws))
+    # each within FP32 roundings of the same number: a step of BF16 apart at most (2^-7 of the value) where they round apart
+    assert ((out.float() - o2.float()).abs() <= 2.0 ** -7 * o2.float().abs() + 2.0 ** -12).all()
+    assert (lse - l2).abs().max() <= 2.0 ** -12
+
+
+@pytest.mark.parametrize("single", [False, True])
+def test_nvfp4(single):
+    import oracle
+    import numpy as np
+    gr = Groups([[700, 800, 650], [50], [0]], [640, 0, 0], 16, 2, 128)
+    q = torch.randn(5, 8, 1, 128, generator=torch.Generator().manual_seed(5)).to(torch.bfloat16)
+    cache = F.make_kv_cache(gr.k, gr.v)
+    n = q.numel()
+    codes, scales = torch.zeros(n // 2, dtype=torch.uint8, device="cuda"), torch.zeros(n // 16, dtype=torch.uint8, device="cuda")
+    ts, amax, o32 = torch.zeros(1, device="cuda"), torch.zeros(1, device="cuda"), torch.zeros(n, device="cuda")
+    given = torch.tensor([2.5e-4], device="cuda") if single else None
+    lse = torch.zeros(5, 8, 1, device="cuda")
+
+    def opts(**kw):
+        return F.make_opts(F.FMHA_OUT_NVFP4, out_scales=scales, out_tensor_scale=ts, nvfp4_scale_in=given, out_amax=amax, **kw)
+    for stage in (o32, None):
+        need = F.fmha_prefix_workspace_size(5, 8, 1, cache, opts(out_f32=stage))
+        ws = torch.full((need,), 0xff, dtype=torch.uint8, device="cuda")
+        F.fmha_fwd_prefix(q.cuda(), cache, gr.table, gr.seqlens, gr.cu, gr.prefix_lens, codes, lse, 128 ** -0.5, opts(out_f32=stage, workspace=ws))
+        assert F.fmha_check_status() == F.FMHA_OK
+        ref = attention_ref(q, *gr.dense, gr.lens, 128 ** -0.5, False)
+        check_attention(o32.view(q.shape), lse, ref, bf16=False)
+        o = o32.cpu().numpy()
+        if single:
+            c, s = oracle.nvfp4_quantize_scaled(o, float(given))[:2]
+        else:
+            c, s, _ = oracle.nvfp4_quantize(o)
+        assert np.array_equal(codes.cpu().numpy(), c) and np.array_equal(scales.cpu().numpy(), s[:n // 16])
+        assert float(amax) == np.abs(o).max()
+
+
+def test_bad_lists_lengths_and_pages():
+    lens, prefix = [[700, 800, 650], [50, 60]], [640, 48]
+    gr = Groups(lens, prefix, 16, 2, 64)
+    q = torch.randn(5, 8, 1, 64, generator=torch.Generator().manual_seed(5)).to(torch.bfloat16)
+    ref = attention_ref(q, *gr.dense, gr.lens, 0.125, False)
+    good = gr.cu.clone()
+    # no list of groups: everything is computed without sharing, and reported
+    for cu in ([1, 3, 5], [0, 6, 5], [0, 3, 4], [0, -1, 5], [0, 3, 6], [0, 1 << 30, 5]):
+        gr.cu = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        out, lse = call(q.cuda(), gr)
+        assert F.fmha_check_status() == F.FMHA_ERR_PAGES
+        check_attention(out, lse, ref, what=str(cu))
+    gr.cu = good
+    # a prefix below 0 is none; one behind the first request's tokens reaches as far as they do
+    gr.prefix_lens = torch.tensor([-5, 1 << 30], dtype=torch.int32, device="cuda")
+    gr2 = Groups([[700, 800, 650], [48, 48]], [640, 48], 16, 2, 64)
+    gr2.prefix_lens = gr.prefix_lens
+    out, lse = call(q.cuda(), gr2)
+    assert F.fmha_check_status() == F.FMHA_OK
+    check_attention(out, lse, attention_ref(q, *gr2.dense, gr2.lens, 0.125, False))
+    # lengths out of bounds are clamped
+    gr.prefix_lens = torch.tensor(prefix, dtype=torch.int32, device="cuda")
+    keep = gr.seqlens.clone()
+    gr.seqlens[3] = -7
+    out, lse = call(q.cuda(), gr)
+    assert F.fmha_check_status() == F.FMHA_ERR_PAGES
+    assert (out[3] == 0).all() and (lse[3] == -math.inf).all()
+    pick = torch.tensor([0, 1, 2, 4])
+    check_attention(out.cpu()[pick], lse.cpu()[pick], tuple(x[pick] for x in ref))
+    gr.seqlens = keep
+    # a page out of the pool reads as zero keys and values
+    gr.table[1, 45] = 1 << 20
+    gr.dense[0][1, :, 720:736] = 0
+    gr.dense[1][1, :, 720:736] = 0
+    out, lse = call(q.cuda(), gr)
+    assert F.fmha_check_status() == F.FMHA_ERR_PAGES
+    check_attention(out, lse, attention_ref(q, *gr.dense, gr.lens, 0.125, False))
+    assert F.fmha_check_status() == F.FMHA_OK
+
+
+def test_nan_and_infinite_scores():
+    gr = Groups([[1500, 1400, 1300], [1300]], [1280, 0], 16, 2, 64)
+    q = torch.randn(4, 4, 1, 64, generator=torch.Generator().manual_seed(5)).to(torch.bfloat16)
+    q[1, 2] = float("nan")
+    q[3, 0] = float("nan")
+    out, lse = call(q.cuda(), gr)
+    assert F.fmha_check_status() == F.FMHA_OK
+    bad = torch.zeros(4, 4, 1, dtype=torch.bool)
+    bad[1, 2] = bad[3, 0] = True
+    assert torch.equal(out.isnan().all(-1).cpu(), bad) and torch.equal(lse.isnan().cpu(), bad)
