@@ -27,6 +27,8 @@
 //    num_splits == 1 each CTA takes whole units instead.
 //  * Paged keys and values (PAGED): the producer gathers a tile page by page (see the producer), and
 //    the work split comes from the requests' lengths inside the kernel (see Line).
+//  * REST: the first tiles of some requests' keys are attended to by another kernel (prefix.cu), which leaves the prefix of the
+//    tiles behind them.  What is not a request's whole attention goes to the workspace as partials that a third kernel merges.
 //  * Roles (decode_kernel<D, CAUSAL, NC, PAGED>): warps 0-3 softmax.  EPI (see
 //    has_epilogue_warps): warps 4-7 epilogue, warp 8 TMA producer, warp 9 MMA issuer, warp 10 the second
 //    producer of paged tiles, the rest only completes its warpgroup; at the end of a work item the
@@ -162,6 +164,7 @@ struct Item {
     bool whole;      // covers every tile of the unit
     int slot;        // partial slot (u + cta)
     int b, head, chunk;   // paged: batch entry, key/value head and chunk of its rows
+    bool after;      // REST: the unit has keys that are attended to elsewhere
 };
 
 // Paged work split.  The line of T tiles (below 2^31) is cut for P CTAs at c T / P, P as many as leave each
@@ -197,9 +200,6 @@ __device__ __forceinline__ int unit_cut(int x, int s, int e)
     return x - s <= e - x ? (x - s < kMinPiece ? s : x) : (e - x < kMinPiece ? e : x);
 }
 
-template <bool PAGED>
-struct Sched;
-
 // Rows of a unit.  Dense: unit u = (b, kv-head) owns rows u * G .. u * G + G - 1.  Paged: a key/value
 // head with more than 16 query rows is cut into `chunks` units of at most G rows each.
 template <bool PAGED>
@@ -222,7 +222,7 @@ __device__ __forceinline__ void place_unit(const DecodeParams& p, Item& it, int 
     it.chunk = p.chunks == 1 ? 0 : i - it.head * p.chunks;
 }
 
-template <bool PAGED>
+template <bool PAGED, bool REST = false>
 struct Sched {
     const DecodeParams* p;
     const int* pre;     // paged split mode: exclusive prefix of the batch entries' tiles
@@ -288,6 +288,12 @@ struct Sched {
                 it.whole = (it.t0 == 0 && it.t1 == nt);
                 it.slot = it.u + cta;
                 place_unit(*p, it, b, i);
+                if constexpr (REST) {   // the line has the request's last nt tiles
+                    const int off = (it.n + kTileKV - 1) / kTileKV - nt;
+                    it.t0 += off;
+                    it.t1 += off;
+                    it.after = off > 0;
+                }
                 g += it.t1 - it.t0;
                 ++i;
                 return true;
@@ -592,7 +598,7 @@ __device__ __forceinline__ void write_empty_entry(const DecodeParams& p, int b)
 // Columns the softmax computes for units of G rows (the MMA's N stays kN): 1, 4, 8 or 16.
 inline int decode_columns(int G) { return G <= 1 ? 1 : G <= 4 ? 4 : G <= 8 ? 8 : 16; }
 
-template <int D, bool CAUSAL, int NC, bool PAGED = false>
+template <int D, bool CAUSAL, int NC, bool PAGED = false, bool REST = false>
 __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()>(), 1)
     decode_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap, const __grid_constant__ DecodeParams p)
@@ -784,7 +790,7 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
         }
     }
 
-    Sched<PAGED> sched;
+    Sched<PAGED, REST> sched;
     sched.init(&p, blockIdx.x, gridDim.x, pre, keys, first, end);
     Item it;
 
@@ -885,7 +891,7 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
         // single-pass NVFP4 in split mode: whole units also go through the combine, which
         // encodes every row in parallel (encoding here would lengthen the CTAs holding many
         // short units)
-        const bool final_here = it.whole && !(p.split && p.nv_codes);
+        const bool final_here = it.whole && !(p.split && p.nv_codes) && !(REST && (it.after || !p.out));
         // An aborted CTA writes no result, but a partial that is counted goes out all the same, as one without a
         // visible key: a graph's replays carry one tag, so an arrival left out here would be made up for by the
         // next replay's first one.

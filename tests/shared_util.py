@@ -63,9 +63,10 @@ def compact_ref(lens, P, table, free, n, new_table, free_out, copies):
 # ------------------------------------------------------------------------------------------------
 class Groups:
     """Requests lens[g][i] of each group whose first prefix[g] tokens (whole pages of P) are in the same pages; pools with NaN
-    wherever no key is, table entries behind a request's pages `junk`."""
+    wherever no key is, table entries behind a request's pages `junk`.  A wide table has room for more than 6000 key tiles,
+    the fewest for which keys are read once for a group."""
 
-    def __init__(self, lens, prefix, P, Hkv, D, layout="hnd", seed=0, scale=1.0, junk=-3, device="cuda"):
+    def __init__(self, lens, prefix, P, Hkv, D, layout="hnd", seed=0, scale=1.0, junk=-3, device="cuda", wide=True):
         g = torch.Generator().manual_seed(seed)
         self.members = [len(x) for x in lens]
         self.lens = [n for group in lens for n in group]
@@ -74,6 +75,8 @@ class Groups:
         assert all(p % P == 0 for p in prefix)
         held = [up(n, P) for n in self.lens]
         width = max(held + [1]) + 2
+        if wide:
+            width = max(width, up((6000 // (B * Hkv) + 1) * 128, P))
         total = sum(p // P for p in prefix) + sum(held)
         ids = torch.randperm(total + 5, generator=g)
         self.k, self.v = make_pools(total + 5, Hkv, P, D, layout, device="cpu")

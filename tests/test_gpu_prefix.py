@@ -27,8 +27,8 @@ def call(q, gr, cache=None, causal=False, scale=None, kind=F.FMHA_OUT_BF16, fill
     return out, lse
 
 
-def run(lens, prefix, P=16, Hq=8, Hkv=2, Sq=1, D=64, layout="hnd", causal=False, kind=F.FMHA_OUT_BF16, seed=1, scale=1.0):
-    gr = Groups(lens, prefix, P, Hkv, D, layout, seed, scale)
+def run(lens, prefix, P=16, Hq=8, Hkv=2, Sq=1, D=64, layout="hnd", causal=False, kind=F.FMHA_OUT_BF16, seed=1, scale=1.0, wide=True):
+    gr = Groups(lens, prefix, P, Hkv, D, layout, seed, scale, wide=wide)
     g = torch.Generator().manual_seed(seed + 1)
     q = torch.randn(len(gr.lens), Hq, Sq, D, generator=g).to(torch.bfloat16)
     out, lse = call(q.cuda(), gr, causal=causal, kind=kind)
@@ -38,8 +38,11 @@ def run(lens, prefix, P=16, Hq=8, Hkv=2, Sq=1, D=64, layout="hnd", causal=False,
     return gr, q, out, lse
 
 
-def test_one_group_one_tile():
-    run([[600, 590]], [512], D=128)
+@pytest.mark.parametrize("wide", [True, False])
+def test_one_group(wide):
+    before = F.fmha_launch_count()
+    run([[600, 590]], [512], D=128, wide=wide)
+    assert F.fmha_launch_count() - before == (3 if wide else 1)    # few tiles: the paged attention
 
 
 @pytest.mark.parametrize("D", [64, 128])
@@ -57,8 +60,6 @@ def test_lengths(lens, prefix, D):
                                          (32, 1, 2), (64, 1, 1), (16, 1, 4), (33, 1, 2), (65, 1, 1), (128, 1, 1), (40, 1, 4), (64, 1, 5)])
 @pytest.mark.parametrize("causal", [False, True])
 def test_heads_and_rows(Hq, Hkv, Sq, causal):
-    if causal and Sq == 1:
-        pytest.skip("one query sees every key either way")
     run([[1300, 1200, 1157, 1280, 1153], [400, 390]], [1152, 384], Hq=Hq, Hkv=Hkv, Sq=Sq, causal=causal, D=64 if Hq % 2 else 128)
 
 
