@@ -5,10 +5,10 @@
 // k-th free id below U; as many of either exist.  With f(x) the number of free pages below x, a used page x >= U is
 // the (x - U - (f(x) - f(U)))-th to move, and f(U) pages move in all.
 //
-// One launch of clusters of eight CTAs.  Each cluster reads the whole stack into a set of bits spread over its
-// shared memory, then each of its CTAs takes a copy of the set and sums it in blocks of 256 pages: f is a sum and
-// up to eight popcounts, its inverse a binary search and as many.  Everything else is a lookup per output.
-// Bound: latency, stack -> set -> copy -> outputs, with two cluster barriers.
+// One launch of single CTAs or clusters of eight.  Each reads the whole stack into a set of bits that every CTA of it gets a copy
+// of, and sums it in blocks of 256 pages: f is a sum and up to eight popcounts, its inverse a binary search and as many.
+// Everything else is a lookup per output.  The stack names each page once if the set has as many bits as it has entries.
+// Bound: latency, stack -> set -> copy -> outputs.
 #include <cuda_runtime.h>
 
 #include "cluster_bits.cuh"
@@ -20,6 +20,8 @@ namespace atc_gb300 {
 namespace {
 
 constexpr int kCompactThreads = 1024;
+constexpr int kCompactCtas = 8;              // of a cluster
+constexpr int kMaxCompactPages = 1 << 20;
 
 struct CompactParams {
     const int32_t* seqlens;
@@ -38,50 +40,50 @@ struct CompactParams {
     int32_t* moves;
     int32_t* free_out;
     int* status;
-    int words;    // of each CTA's part of the set
-    int blocks;   // runs of 256 pages
+    int blocks;   // runs of 256 pages, 8 words of the set each
 };
 
-__global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kCompactThreads, 1)
-    page_compact_kernel(const __grid_constant__ CompactParams p)
+template <int CTAS>
+__global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kCompactThreads, 1) page_compact_kernel(const __grid_constant__ CompactParams p)
 {
-    extern __shared__ uint32_t shm[];
-    uint32_t* part = shm;                                                          // this CTA's part of the set
-    uint32_t* bits = shm + p.words;                                                // all of it
-    int* below = reinterpret_cast<int*>(bits + static_cast<size_t>(p.blocks) * 8);  // free pages before each block
-    __shared__ int sums[32], bad_at[1];
+    extern __shared__ uint32_t bits[];                                   // the set
+    const int words = p.blocks * 8;
+    uint32_t* slice = bits + words;                                      // this CTA's blocks of the joined one
+    int* below = reinterpret_cast<int*>(slice + (CTAS > 1 ? p.blocks + 8 * CTAS : 0));   // free pages before each block
+    __shared__ int sums[32];
     griddep_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, N = p.num_pages;
-    const int rank = static_cast<int>(cluster_ctarank());
-    for (int i = tid; i < p.words; i += kCompactThreads) part[i] = 0;
-    if (tid == 0) bad_at[0] = 0;
+    const int rank = CTAS > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    for (int i = tid; i < words; i += kCompactThreads) bits[i] = 0;
     griddep_wait();
-    cluster_sync();   // every CTA's words are zero
+    __syncthreads();
 
     const int n = *p.free_count;
-    const PageBits set{smem_u32(part), p.words};
     const long long room = static_cast<long long>(p.max_pages) * p.page;
     bool bad = n < 0 || n > N;
     const auto fine = [&](int page) { return page >= 0 && page < N; };
     if (!bad)
-#pragma unroll 4
-        for (int i = rank * kCompactThreads + tid; i < n; i += kClusterCtas * kCompactThreads) {
+#pragma unroll 8
+        for (int i = rank * kCompactThreads + tid; i < n; i += CTAS * kCompactThreads) {
             const int x = p.free_pages[i];
-            if (!fine(x) || set.test_set(x)) bad = true;   // not a page, or twice on the stack
+            if (fine(x)) set_bit(bits, x);
         }
     for (int b = tid; b < p.B; b += kCompactThreads) {
         const int c = p.seqlens[b];
         bad = bad || c < 0 || c > room;
     }
     bad = __syncthreads_or(bad);
-    if (tid < kClusterCtas && bad) st_cluster(mapa_shared(smem_u32(&bad_at[0]), static_cast<uint32_t>(tid)), 1u);
-    cluster_sync();   // the set is complete
-    for (int i = tid; i < p.blocks * 8; i += kCompactThreads) {
-        const int r = i / p.words;
-        bits[i] = r < kClusterCtas ? ld_cluster(mapa_shared(smem_u32(part + (i - r * p.words)), static_cast<uint32_t>(r))) : 0u;
+    if constexpr (CTAS > 1) {
+        const int per = (words + CTAS - 1) / CTAS;
+        cluster_sync();   // all sets are marked
+        for (int i = tid; i < per; i += kCompactThreads) slice[i] = rank * per + i < words ? joined_word<CTAS>(bits, rank * per + i) : 0u;
+        cluster_sync();   // all slices are joined, and nobody looks at the sets any more
+        for (int i = tid; i < words; i += kCompactThreads) {
+            const int r = i / per;
+            bits[i] = ld_cluster(mapa_shared(smem_u32(slice + (i - r * per)), static_cast<uint32_t>(r)));
+        }
+        cluster_sync();   // nobody looks into another CTA's memory from here on
     }
-    cluster_sync();   // nobody looks into another CTA's memory from here on
-    bad = bad_at[0] != 0;
 
     const auto count_block = [&](int k) {
         int c = 0;
@@ -99,6 +101,7 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kCompactT
         at += count_block(k);
     }
     __syncthreads();
+    bad = bad || total != n;   // an entry that is no page, or twice the same
 
     const auto is_free = [&](int x) { return (bits[x >> 5] >> (x & 31)) & 1; };
     // free pages below x < N
@@ -117,9 +120,17 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kCompactT
         k -= below[lo];
         int w = lo * 8;
         for (int c; k >= (c = __popc(bits[w])); ++w) k -= c;
-        uint32_t v = bits[w];
-        for (; k > 0; --k) v &= v - 1;
-        return w * 32 + __ffs(v) - 1;
+        const uint32_t v = bits[w];
+        int pos = 0;
+#pragma unroll
+        for (int h = 16; h > 0; h >>= 1) {
+            const int c = __popc((v >> pos) & ((1u << h) - 1));
+            if (k >= c) {
+                k -= c;
+                pos += h;
+            }
+        }
+        return w * 32 + pos;
     };
     const int U = N - n;
     const int M = bad || U == N ? 0 : free_below(U);
@@ -189,22 +200,23 @@ extern "C" int fmha_page_compact(const int32_t* seqlens, int B, int page_size, c
         if (misaligned(x, 4)) return set_error(FMHA_ERR_INVALID, "fmha_page_compact: arrays must be 4-byte aligned");
     if (free_pages_out == free_pages || (B > 0 && new_table == block_table))
         return set_error(FMHA_ERR_INVALID, "fmha_page_compact: new_table and free_pages_out must not be block_table and free_pages");
-    if (static_cast<long long>(max_pages) * page_size > (1LL << 31) - 256 || num_pages > kMaxPoolPages || n_copies > (1 << 30) || B > (1 << 24))
+    if (static_cast<long long>(max_pages) * page_size > (1LL << 31) - 256 || num_pages > kMaxCompactPages || n_copies > (1 << 30) || B > (1 << 24))
         return set_error(FMHA_ERR_UNSUPPORTED, "fmha_page_compact: max_pages * page_size past 2^31, more than 2^20 pages, 2^24 requests or 2^30 copies");
     int* status = device_status_ptr();
     if (!status) return set_error(FMHA_ERR_CUDA, "no CUDA device");
-    const int words = (num_pages + 32 * kClusterCtas - 1) / (32 * kClusterCtas), blocks = (num_pages + 255) / 256;
+    const int blocks = (num_pages + 255) / 256;
     const CompactParams p{seqlens, B, page_size, FastDiv(static_cast<uint32_t>(page_size)), block_table, max_pages, free_pages, free_count,
-                          num_pages, new_ids, new_table, copy_src, copy_dst, n_copies, copy_count, free_pages_out, status, words, blocks};
-    // a cluster for each 65536 outputs
+                          num_pages, new_ids, new_table, copy_src, copy_dst, n_copies, copy_count, free_pages_out, status, blocks};
+    // a CTA for up to 8192 pages and as many outputs; else a cluster for each 65536 outputs
     const long long outputs = 3LL * num_pages + static_cast<long long>(B) * max_pages;
-    const int most = num_sms() / kClusterCtas;
+    const bool one = num_pages <= 8192 && outputs <= 32768;
+    const int most = num_sms() / kCompactCtas > 0 ? num_sms() / kCompactCtas : 1;
     const int clusters = static_cast<int>(1 + outputs / 65536 < most ? 1 + outputs / 65536 : most);
-    const int smem = 4 * words + 36 * blocks;
+    const auto kernel = one ? page_compact_kernel<1> : page_compact_kernel<kCompactCtas>;
+    const int smem = 36 * blocks + (one ? 0 : 4 * (blocks + 8 * kCompactCtas));
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    FMHA_CHECK_CUDA(set_smem_limit_once(reinterpret_cast<const void*>(page_compact_kernel), kMaxPoolPages / 8 / kClusterCtas + 36 * (kMaxPoolPages / 256)));
-    FMHA_CHECK_CUDA(launch_pdl(page_compact_kernel, dim3(static_cast<unsigned>((clusters > 0 ? clusters : 1) * kClusterCtas)), dim3(kCompactThreads),
-                               static_cast<size_t>(smem), st, p));
+    FMHA_CHECK_CUDA(set_smem_limit_once(reinterpret_cast<const void*>(kernel), 40 * (kMaxCompactPages / 256) + 4 * 8 * kCompactCtas));
+    FMHA_CHECK_CUDA(launch_pdl(kernel, dim3(static_cast<unsigned>(one ? 1 : clusters * kCompactCtas)), dim3(kCompactThreads), static_cast<size_t>(smem), st, p));
     count_launch();
     return FMHA_OK;
 }

@@ -11,10 +11,9 @@
 //
 // No reference counts are kept between calls: who holds a page stands in the tables.
 //
-// One launch.  A cluster of eight CTAs finds the freed pages in a set of bits that is spread over their
-// shared memory (gone pages set, then kept pages cleared), counts them in the order of ids and hands out
-// the copies' pages; more clusters, if the tables are large, copy the rows meanwhile.  Bound: latency, a chain
-// of lengths and parents -> rows -> two or three cluster barriers -> stack -> last pages.
+// One launch.  A CTA, or a cluster of eight for larger tables, marks gone and kept pages in sets of bits, counts the freed
+// ones in the order of ids and hands out the copies' pages; more clusters, if the tables are large, copy the rows meanwhile.
+// Bound: latency, a chain of lengths and parents -> rows -> sets -> stack -> last pages.
 #include <cuda_runtime.h>
 
 #include "cluster_bits.cuh"
@@ -27,6 +26,10 @@ namespace {
 
 constexpr int kMaxForkRequests = 8192;
 constexpr int kForkThreads = 1024;
+
+constexpr int kMaxForkPages = 1 << 19;   // two sets of 64 KB
+constexpr int kForkCtas = 8;             // of a cluster
+constexpr int kSegment = 256;            // entries of a row that a warp takes at a time, eight loads a lane
 
 struct ForkParams {
     const int32_t* parents;
@@ -46,23 +49,26 @@ struct ForkParams {
     int32_t* tokens;
     int32_t* free_count_out;
     int* status;
-    int words;   // of each CTA's part of the set
+    int words;      // of a set
+    int segments;   // runs of kSegment entries of a row
 };
 
-__global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kForkThreads, 1) page_fork_kernel(const __grid_constant__ ForkParams p)
+template <int CTAS>
+__global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kForkThreads, 1) page_fork_kernel(const __grid_constant__ ForkParams p)
 {
     extern __shared__ int sh[];
     int* first = sh;                 // an old request's lowest child
     int* held_tokens = sh + p.Bo;    // and its tokens
-    uint32_t* bits = reinterpret_cast<uint32_t*>(sh + 2 * p.Bo);
-    __shared__ int sums[32], given[kClusterCtas];
+    uint32_t* gone = reinterpret_cast<uint32_t*>(sh + 2 * p.Bo);
+    uint32_t* kept = gone + p.words;
+    __shared__ int sums[32], given[CTAS];
     griddep_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, B = p.B, Bo = p.Bo, P = p.page;
-    const int rank = static_cast<int>(cluster_ctarank()), cluster = blockIdx.x / kClusterCtas, clusters = gridDim.x / kClusterCtas;
+    const int rank = CTAS > 1 ? static_cast<int>(cluster_ctarank()) : 0, cluster = blockIdx.x / CTAS, clusters = gridDim.x / CTAS;
     const bool counts = cluster == 0;   // this cluster finds the freed pages
     for (int i = tid; i < Bo; i += kForkThreads) first[i] = INT32_MAX;
     if (counts)
-        for (int i = tid; i < p.words; i += kForkThreads) bits[i] = 0;
+        for (int i = tid; i < 2 * p.words; i += kForkThreads) gone[i] = 0;
     griddep_wait();
 
     const long long room = static_cast<long long>(p.max_pages) * P;
@@ -73,9 +79,14 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kForkThre
         held_tokens[i] = c;
         bad = bad || c < 0 || c > room;
     }
+    // children in a run per thread; the first of them, the usual number, stays in a register
+    const int per_b = (B + kForkThreads - 1) / kForkThreads;
+    const int b0 = min(B, tid * per_b), b1 = min(B, b0 + per_b);
+    const int parent0 = b0 < b1 ? p.parents[b0] : -1;
+    const auto parent = [&](int b) { return b == b0 ? parent0 : p.parents[b]; };
     __syncthreads();
-    for (int b = tid; b < B; b += kForkThreads) {
-        const int i = p.parents[b];
+    for (int b = b0; b < b1; ++b) {
+        const int i = parent(b);
         bad = bad || i >= Bo;
         if (i >= 0 && i < Bo) atomicMin(&first[i], b);
     }
@@ -86,83 +97,91 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kForkThre
     const auto copies = [&](int b, int i) { return i >= 0 && first[i] != b && part(i) != 0; };
     const auto fine = [&](int page) { return page >= 0 && page < p.num_pages; };
     const auto row = [&](int i) { return p.table + static_cast<size_t>(i) * p.max_pages; };
-    const int warps = kForkThreads / 32, cluster_warp = rank * warps + (tid >> 5), cluster_warps = kClusterCtas * warps;
-
-    // a warp per child: its row, up to a page that it gets for itself
-    if (!bad && (clusters == 1 || !counts)) {
-        const int step = clusters == 1 ? cluster_warps : (clusters - 1) * cluster_warps;
-        for (int b = clusters == 1 ? cluster_warp : (cluster - 1) * cluster_warps + cluster_warp; b < B; b += step) {
-            const int i = p.parents[b];
-            if (i < 0) continue;
-            const int k = held(i) - (copies(b, i) ? 1 : 0);
-            const int32_t* from = row(i);
-            int32_t* to = p.new_table + static_cast<size_t>(b) * p.max_pages;
-            bool odd = false;
-#pragma unroll 4
-            for (int j = lane; j < k; j += 32) {
-                const int x = from[j];
-                odd = odd || !fine(x);
-                to[j] = x;
+    const int warps = kForkThreads / 32, cluster_warp = rank * warps + (tid >> 5), cluster_warps = CTAS * warps;
+    // The first count(i) entries of rows 0 .. n - 1 by `nw` warps, this one the w-th: a warp per row, or several where there are
+    // more of them.  put(row, entry, page)
+    const auto walk = [&](int n, int w, int nw, auto&& from, auto&& count, auto&& put) {
+        const int shared = max(1, min(p.segments, nw / max(n, 1)));   // warps of a row
+        for (int v = w; v < n * shared; v += nw) {
+            const int i = v / shared, k = count(i);
+            for (int s = v - i * shared; s * kSegment < k; s += shared) {
+                const int32_t* row = from(i);
+                int x[kSegment / 32];
+#pragma unroll
+                for (int u = 0; u < kSegment / 32; ++u) {
+                    const int j = s * kSegment + u * 32 + lane;
+                    x[u] = j < k ? row[j] : 0;
+                }
+#pragma unroll
+                for (int u = 0; u < kSegment / 32; ++u) {
+                    const int j = s * kSegment + u * 32 + lane;
+                    if (j < k) put(i, j, x[u]);
+                }
             }
-            if (odd) report_bad_page(p.status);
         }
+    };
+
+    bool odd = false;
+    // the children's rows, up to a page that a child gets for itself
+    if (!bad && (clusters == 1 || !counts)) {
+        const int others = clusters == 1 ? 1 : clusters - 1, me = clusters == 1 ? 0 : cluster - 1;
+        walk(B, me * cluster_warps + cluster_warp, others * cluster_warps, [&](int b) { return row(p.parents[b]); },
+             [&](int b) {
+                 const int i = p.parents[b];
+                 return i < 0 ? 0 : held(i) - (copies(b, i) ? 1 : 0);
+             },
+             [&](int b, int j, int x) {
+                 odd = odd || !fine(x);
+                 p.new_table[static_cast<size_t>(b) * p.max_pages + j] = x;
+             });
     }
-    if (!counts) return;
+    if (!counts) {
+        if (odd) report_bad_page(p.status);
+        return;
+    }
 
     // which pages go back
-    const PageBits set{smem_u32(bits), p.words};
-    int R = 0, before = 0, own = 0, at = 0;
-    const int per = (p.words + kForkThreads - 1) / kForkThreads;
-    const int w0 = min(p.words, tid * per), w1 = min(p.words, w0 + per);
-    bool gone = false;
+    int R = 0, before = 0, at = 0;
+    const int slice = (p.words + CTAS - 1) / CTAS, per = (slice + kForkThreads - 1) / kForkThreads;   // words of a CTA and of a thread
+    const int w1 = min(p.words, min((rank + 1) * slice, rank * slice + (tid + 1) * per)), w0 = min(w1, rank * slice + tid * per);
+    bool ends = false;
     if (!bad)
-        for (int i = tid; i < Bo; i += kForkThreads) gone = gone || (first[i] == INT32_MAX && held_tokens[i] > 0);
-    gone = __syncthreads_or(gone);
-    if (gone) {
-        cluster_sync();   // every CTA's words are zero
-        bool odd = false;
-        for (int i = cluster_warp; i < Bo; i += cluster_warps)
-            if (first[i] == INT32_MAX)
-#pragma unroll 4
-                for (int j = lane; j < held(i); j += 32) {
-                    const int x = row(i)[j];
-                    if (fine(x))
-                        set.set(x);
-                    else
-                        odd = true;
-                }
-        if (odd) report_bad_page(p.status);
-        cluster_sync();
-        for (int i = cluster_warp; i < Bo; i += cluster_warps)
-            if (first[i] != INT32_MAX)
-#pragma unroll 4
-                for (int j = lane; j < held(i); j += 32) {
-                    const int x = row(i)[j];
-                    if (fine(x)) set.clear(x);
-                }
-        cluster_sync();
-        for (int w = w0; w < w1; ++w) own += __popc(bits[w]);
-        int total;
+        for (int i = tid; i < Bo; i += kForkThreads) ends = ends || (first[i] == INT32_MAX && held_tokens[i] > 0);
+    ends = __syncthreads_or(ends);
+    if (ends) {
+        walk(Bo, cluster_warp, cluster_warps, row, held, [&](int i, int, int x) {
+            const bool last = first[i] == INT32_MAX;
+            if (fine(x))
+                set_bit(last ? gone : kept, x);
+            else
+                odd = odd || last;
+        });
+        sync_ctas<CTAS>();
+        int own = 0, total;
+        for (int w = w0; w < w1; ++w) own += __popc(joined_word<CTAS>(gone, w) & ~joined_word<CTAS>(kept, w));
         at = block_scan(own, sums, total);
-        if (tid < kClusterCtas) st_cluster(mapa_shared(smem_u32(&given[rank]), static_cast<uint32_t>(tid)), static_cast<uint32_t>(total));
-        cluster_sync();
-        for (int r = 0; r < kClusterCtas; ++r) {
+        if constexpr (CTAS > 1) {
+            if (tid < CTAS) st_cluster(mapa_shared(smem_u32(&given[rank]), static_cast<uint32_t>(tid)), static_cast<uint32_t>(total));
+        } else if (tid == 0) {
+            given[0] = total;
+        }
+        sync_ctas<CTAS>();
+        for (int r = 0; r < CTAS; ++r) {
             before += r < rank ? given[r] : 0;
             R += given[r];
         }
     }
-    // children that get a page of their own, in a run per thread
-    const int per_b = (B + kForkThreads - 1) / kForkThreads;
-    const int b0 = min(B, tid * per_b), b1 = min(B, b0 + per_b);
+    if (odd) report_bad_page(p.status);
+    // children that get a page of their own
     int mine = 0, A = 0;
     if (!bad)
-        for (int b = b0; b < b1; ++b) mine += copies(b, p.parents[b]) ? 1 : 0;
+        for (int b = b0; b < b1; ++b) mine += copies(b, parent(b)) ? 1 : 0;
     int a = block_scan(mine, sums, A);
 
     // all or nothing
     bad = bad || n + R > p.num_pages || A > n + R;
     if (bad) {
-        cluster_sync();   // the stack's height has been read by all
+        sync_ctas<CTAS>();   // the stack's height has been read by all, and nobody looks into another CTA's memory
         if (rank == 0) {
             for (int b = tid; b < B; b += kForkThreads) {
                 p.seqlens[b] = 0;
@@ -179,14 +198,14 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kForkThre
     if (R > 0) {
         int32_t* to = p.free_pages + n + before + at;
         for (int w = w0; w < w1; ++w)
-            for (uint32_t v = bits[w]; v; v &= v - 1) *to++ = (rank * p.words + w) * 32 + __ffs(v) - 1;
+            for (uint32_t v = joined_word<CTAS>(gone, w) & ~joined_word<CTAS>(kept, w); v; v &= v - 1) *to++ = w * 32 + __ffs(v) - 1;
     }
-    cluster_sync();   // the stack is written, and its height read
+    sync_ctas<CTAS>();   // the stack is written, and its height read
     if (rank == 0 && tid == 0) *p.free_count_out = n + R - A;
     for (int b = b0; b < b1; ++b) {
-        const int i = p.parents[b];
+        const int i = parent(b);
         const bool copy = copies(b, i);
-        if (b % kClusterCtas == rank) {
+        if (b % CTAS == rank) {
             int from = -1, to = -1;
             if (copy) {
                 const int last = held(i) - 1;
@@ -228,22 +247,25 @@ extern "C" int fmha_page_fork(const int32_t* parents, int B, const int32_t* ctx_
         return set_error(FMHA_ERR_INVALID, "fmha_page_fork: new_table must not be block_table");
     if (B > kMaxForkRequests || B_old > kMaxForkRequests)
         return set_error(FMHA_ERR_UNSUPPORTED, "fmha_page_fork: more than 8192 requests");
-    if (static_cast<long long>(max_pages) * page_size > (1LL << 31) - 256 || num_pages > kMaxPoolPages)
-        return set_error(FMHA_ERR_UNSUPPORTED, "fmha_page_fork: max_pages * page_size past 2^31, or more than 2^20 pages");
+    if (static_cast<long long>(max_pages) * page_size > (1LL << 31) - 256 || num_pages > kMaxForkPages)
+        return set_error(FMHA_ERR_UNSUPPORTED, "fmha_page_fork: max_pages * page_size past 2^31, or more than 2^19 pages");
     int* status = device_status_ptr();
     if (!status) return set_error(FMHA_ERR_CUDA, "no CUDA device");
-    const int words = (num_pages + 32 * kClusterCtas - 1) / (32 * kClusterCtas);
+    const int words = (num_pages + 31) / 32, segments = (max_pages + kSegment - 1) / kSegment;
     const ForkParams p{parents, B, ctx_lens, B_old, page_size, FastDiv(static_cast<uint32_t>(page_size)), block_table, max_pages,
-                       free_pages, free_count, num_pages, new_table, seqlens, copy_src, copy_dst, copy_tokens, free_count_out, status, words};
-    // clusters that copy rows: one for each 16384 entries that they may have
-    const long long entries = static_cast<long long>(B) * max_pages;
-    const int most = num_sms() / kClusterCtas - 1;
-    const int copiers = entries <= 16384 ? 0 : static_cast<int>(entries / 16384 < most ? entries / 16384 : most);
-    const int smem = 8 * B_old + 4 * words;
+                       free_pages, free_count, num_pages, new_table, seqlens, copy_src, copy_dst, copy_tokens, free_count_out, status, words, segments};
+    // Runs of 256 entries that the tables may have: two a warp of one CTA, or else a cluster (its barriers cost a small call about 2
+    // us); beyond two a warp of that, more clusters, to copy rows
+    const long long work = static_cast<long long>(B > B_old ? B : B_old) * segments;
+    constexpr int kTwo = 2 * kForkThreads / 32;
+    const bool one = work <= kTwo;
+    const int most = num_sms() / kForkCtas - 1, want = static_cast<int>(work / (kTwo * kForkCtas) < most ? work / (kTwo * kForkCtas) : most);
+    const auto kernel = one ? page_fork_kernel<1> : page_fork_kernel<kForkCtas>;
+    const int ctas = one ? 1 : (1 + (want > 0 ? want : 0)) * kForkCtas;
+    const int smem = 8 * B_old + 8 * words;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    FMHA_CHECK_CUDA(set_smem_limit_once(reinterpret_cast<const void*>(page_fork_kernel), 8 * kMaxForkRequests + kMaxPoolPages / 8 / kClusterCtas));
-    FMHA_CHECK_CUDA(launch_pdl(page_fork_kernel, dim3(static_cast<unsigned>((1 + copiers) * kClusterCtas)), dim3(kForkThreads),
-                               static_cast<size_t>(smem), st, p));
+    FMHA_CHECK_CUDA(set_smem_limit_once(reinterpret_cast<const void*>(kernel), 8 * kMaxForkRequests + kMaxForkPages / 4));
+    FMHA_CHECK_CUDA(launch_pdl(kernel, dim3(static_cast<unsigned>(ctas)), dim3(kForkThreads), static_cast<size_t>(smem), st, p));
     count_launch();
     return FMHA_OK;
 }

@@ -324,7 +324,7 @@ size_t fmha_prefix_workspace_size(int B, int Hq, int Sq, const fmha_kv_cache* ca
  * choice of a beam search, a prompt forked into samples, requests that end, a batch put in another order.
  *   parents: int32[B], the request that child b continues, or a negative number: an empty slot.
  *   ctx_lens: int32[B_old], tokens in the cache; block_table: int32[B_old][max_pages]; page_size.
- *   free_pages, free_count, num_pages (at most 2^20): the stack of free pages, as in fmha_page_table.
+ *   free_pages, free_count, num_pages (at most 2^19): the stack of free pages, as in fmha_page_table.
  * A child has its parent's tokens and pages, except that of several children of one parent all but the first
  * get a page of their own in place of a partly filled last one, whose tokens are to be copied (fmha_page_copy).
  * A request without children ends.  First the pages that rows of ended requests name and no row of a

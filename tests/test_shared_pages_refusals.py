@@ -62,7 +62,7 @@ def fork(lib, parents=A, B=2, ctx=A, old=2, page=16, table=A, width=4, free=A, c
 @pytest.mark.parametrize("bad, code", [(dict([(k, None)]), 1) for k in "parents ctx table free count new lens src dst tok out".split()] +
                          [(dict([(k, ODD)]), 1) for k in "parents ctx table free count new lens src dst tok out".split()] +
                          [(dict(B=-1), 1), (dict(old=-1), 1), (dict(page=0), 1), (dict(pages=0), 1), (dict(width=0), 1), (dict(new=A), 1),
-                          (dict(B=8193), 2), (dict(old=8193), 2), (dict(width=1 << 28), 2), (dict(pages=(1 << 20) + 1), 2)])
+                          (dict(B=8193), 2), (dict(old=8193), 2), (dict(width=1 << 28), 2), (dict(pages=(1 << 19) + 1), 2)])
 def test_page_fork(lib, bad, code):
     assert fork(lib, **bad) == code
     assert b"fmha_page_fork" in lib.fmha_last_error()
