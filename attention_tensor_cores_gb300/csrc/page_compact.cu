@@ -5,10 +5,11 @@
 // k-th free id below U; as many of either exist.  With f(x) the number of free pages below x, a used page x >= U is
 // the (x - U - (f(x) - f(U)))-th to move, and f(U) pages move in all.
 //
-// One launch of single CTAs or clusters of eight.  Each reads the whole stack into a set of bits that every CTA of it gets a copy
-// of, and sums it in blocks of 256 pages: f is a sum and up to eight popcounts, its inverse a binary search and as many.
-// Everything else is a lookup per output.  The stack names each page once if the set has as many bits as it has entries.
-// Bound: latency, stack -> set -> copy -> outputs.
+// One CTA, or clusters of eight.  Each reads the whole stack into a set of bits that every CTA of it gets a copy of, and sums
+// it in blocks of 256 pages: f is a sum and up to eight popcounts, its inverse a binary search and as many, for each page that
+// moves.  The stack names each page once if the set has as many bits as it has entries.  The tables' new entries are looked up
+// in new_ids, by the one CTA or by a second launch (with f and its inverse for each entry: 13,000 cycles of 34,000).
+// Bound: latency, stack -> set -> copy -> new ids -> tables.
 #include <cuda_runtime.h>
 
 #include "cluster_bits.cuh"
@@ -43,6 +44,39 @@ struct CompactParams {
     int blocks;   // runs of 256 pages, 8 words of the set each
 };
 
+// The rows' new entries from new_ids, by `step` threads of which this is the first-th: a warp for 128 entries at a time,
+// several warps a row where there are more of them
+__device__ __forceinline__ void translate_rows(const CompactParams& p, int first, int step)
+{
+    const int lane = static_cast<int>(lane_id()), warps = step / 32, shared = max(1, min((p.max_pages + 127) / 128, warps / max(p.B, 1)));
+    const long long room = static_cast<long long>(p.max_pages) * p.page;
+    bool odd = false;
+    for (int v = first / 32; v < p.B * shared; v += warps) {
+        const int b = v / shared;
+        const long long len = p.seqlens[b], held_tokens = len < 0 ? 0 : len > room ? room : len;
+        const int k = p.by_page.up(static_cast<int>(held_tokens));
+        const size_t row = static_cast<size_t>(b) * p.max_pages;
+        for (int s = v - b * shared; s * 128 < k; s += shared) {
+            int x[4], to[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int j = s * 128 + u * 32 + lane;
+                x[u] = j < k ? p.table[row + j] : 0;
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) to[u] = x[u] >= 0 && x[u] < p.num_pages ? __ldcg(p.new_ids + x[u]) : -1;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int j = s * 128 + u * 32 + lane;
+                if (j >= k) continue;
+                odd = odd || to[u] < 0;   // no page, or a free one
+                p.new_table[row + j] = to[u] < 0 ? x[u] : to[u];
+            }
+        }
+    }
+    if (odd) report_bad_page(p.status);
+}
+
 template <int CTAS>
 __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kCompactThreads, 1) page_compact_kernel(const __grid_constant__ CompactParams p)
 {
@@ -52,7 +86,7 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kCompactThreads, 
     int* below = reinterpret_cast<int*>(slice + (CTAS > 1 ? p.blocks + 8 * CTAS : 0));   // free pages before each block
     __shared__ int sums[32];
     griddep_launch_dependents();
-    const int tid = threadIdx.x, lane = tid & 31, N = p.num_pages;
+    const int tid = threadIdx.x, N = p.num_pages;
     const int rank = CTAS > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     for (int i = tid; i < words; i += kCompactThreads) bits[i] = 0;
     griddep_wait();
@@ -158,24 +192,17 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kCompactThreads, 
         *p.moves = M;
         if (bad) report_bad_page(p.status);
     }
-    // a warp per request: its row
-    bool odd = false;
-    for (int b = first / 32; b < p.B; b += step / 32) {
-        const long long len = p.seqlens[b], held_tokens = len < 0 ? 0 : len > room ? room : len;
-        const int k = p.by_page.up(static_cast<int>(held_tokens));
-        const size_t row = static_cast<size_t>(b) * p.max_pages;
-#pragma unroll 4
-        for (int j = lane; j < k; j += 32) {
-            const int x = p.table[row + j];
-            int to = x;
-            if (!fine(x) || (!bad && is_free(x)))
-                odd = true;
-            else if (!bad && x >= U)
-                to = nth_free(mover(x));
-            p.new_table[row + j] = to;
-        }
+    if constexpr (CTAS == 1) {
+        __syncthreads();   // the new ids are written
+        translate_rows(p, first, step);
     }
-    if (odd) report_bad_page(p.status);
+}
+
+__global__ void __launch_bounds__(256) page_translate_kernel(const __grid_constant__ CompactParams p)
+{
+    griddep_launch_dependents();
+    griddep_wait();
+    translate_rows(p, blockIdx.x * 256 + threadIdx.x, gridDim.x * 256);
 }
 
 }  // namespace
@@ -207,16 +234,21 @@ extern "C" int fmha_page_compact(const int32_t* seqlens, int B, int page_size, c
     const int blocks = (num_pages + 255) / 256;
     const CompactParams p{seqlens, B, page_size, FastDiv(static_cast<uint32_t>(page_size)), block_table, max_pages, free_pages, free_count,
                           num_pages, new_ids, new_table, copy_src, copy_dst, n_copies, copy_count, free_pages_out, status, blocks};
-    // a CTA for up to 8192 pages and as many outputs; else a cluster for each 65536 outputs
-    const long long outputs = 3LL * num_pages + static_cast<long long>(B) * max_pages;
-    const bool one = num_pages <= 8192 && outputs <= 32768;
-    const int most = num_sms() / kCompactCtas > 0 ? num_sms() / kCompactCtas : 1;
-    const int clusters = static_cast<int>(1 + outputs / 65536 < most ? 1 + outputs / 65536 : most);
+    // A CTA for up to 8192 pages and tables of as many entries; else a cluster for each 32768 pages, up to eight (more would not all be
+    // on the GPU at a time: a cluster's SMs are neighbours)
+    const long long entries = static_cast<long long>(B) * max_pages;
+    const bool one = num_pages <= 8192 && entries <= 8192;
+    const int clusters = 1 + num_pages / 32768 < 8 ? 1 + num_pages / 32768 : 8;
     const auto kernel = one ? page_compact_kernel<1> : page_compact_kernel<kCompactCtas>;
     const int smem = 36 * blocks + (one ? 0 : 4 * (blocks + 8 * kCompactCtas));
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     FMHA_CHECK_CUDA(set_smem_limit_once(reinterpret_cast<const void*>(kernel), 40 * (kMaxCompactPages / 256) + 4 * 8 * kCompactCtas));
     FMHA_CHECK_CUDA(launch_pdl(kernel, dim3(static_cast<unsigned>(one ? 1 : clusters * kCompactCtas)), dim3(kCompactThreads), static_cast<size_t>(smem), st, p));
     count_launch();
+    if (!one && B > 0) {
+        const long long most = 4LL * (num_sms() > 0 ? num_sms() : 1), want = (entries + 1023) / 1024;
+        FMHA_CHECK_CUDA(launch_pdl(page_translate_kernel, dim3(static_cast<unsigned>(want < most ? want : most)), dim3(256), 0, st, p));
+        count_launch();
+    }
     return FMHA_OK;
 }

@@ -37,12 +37,9 @@ __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const __grid_co
     griddep_wait();
     const int i = blockIdx.x;
     const bool report = blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0;
-    if (p.count) {
-        const int c = *p.count;
-        if (report && i == 0 && (c < 0 || c > p.n)) report_bad_page(p.status);
-        if (i >= c) return;
-    }
-    const int from = p.src[i], to = p.dst[i], wanted = p.tokens ? p.tokens[i] : p.page;
+    const int from = p.src[i], to = p.dst[i], wanted = p.tokens ? p.tokens[i] : p.page, c = p.count ? *p.count : p.n;
+    if (report && i == 0 && (c < 0 || c > p.n)) report_bad_page(p.status);
+    if (i >= c) return;
     if (from < 0 || to < 0) return;
     const int t = min(max(wanted, 0), p.page);
     const bool fine = from < p.num_pages && to < p.num_pages;

@@ -255,13 +255,13 @@ extern "C" int fmha_page_fork(const int32_t* parents, int B, const int32_t* ctx_
     const ForkParams p{parents, B, ctx_lens, B_old, page_size, FastDiv(static_cast<uint32_t>(page_size)), block_table, max_pages,
                        free_pages, free_count, num_pages, new_table, seqlens, copy_src, copy_dst, copy_tokens, free_count_out, status, words, segments};
     // Runs of 256 entries that the tables may have: two a warp of one CTA, or else a cluster (its barriers cost a small call about 2
-    // us); beyond two a warp of that, more clusters, to copy rows
+    // us); beyond two a warp of that, up to seven clusters more, to copy rows (with more than eight not all would be on the GPU at a time)
     const long long work = static_cast<long long>(B > B_old ? B : B_old) * segments;
     constexpr int kTwo = 2 * kForkThreads / 32;
     const bool one = work <= kTwo;
-    const int most = num_sms() / kForkCtas - 1, want = static_cast<int>(work / (kTwo * kForkCtas) < most ? work / (kTwo * kForkCtas) : most);
+    const int most = 7, want = static_cast<int>(work / (kTwo * kForkCtas) < most ? work / (kTwo * kForkCtas) : most);
     const auto kernel = one ? page_fork_kernel<1> : page_fork_kernel<kForkCtas>;
-    const int ctas = one ? 1 : (1 + (want > 0 ? want : 0)) * kForkCtas;
+    const int ctas = one ? 1 : (1 + want) * kForkCtas;
     const int smem = 8 * B_old + 8 * words;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     FMHA_CHECK_CUDA(set_smem_limit_once(reinterpret_cast<const void*>(kernel), 8 * kMaxForkRequests + kMaxForkPages / 4));

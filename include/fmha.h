@@ -356,7 +356,7 @@ int fmha_page_copy(const fmha_kv_cache* caches, int n_caches, const int32_t* src
                    const int32_t* count, fmha_stream_t stream);
 
 /*
- * Used pages to the low ids, in one launch: with n = *free_count of num_pages (at most 2^20) pages free, the used ones
+ * Used pages to the low ids, in one launch or two: with n = *free_count of num_pages (at most 2^20) pages free, the used ones
  * end up in 0 .. num_pages - n - 1.  The k-th used page behind them moves to the k-th free page among them.  The data
  * moves with fmha_page_copy(copy_src, copy_dst, NULL, n_copies, copy_count) in every layer.
  *   seqlens: int32[B], tokens of each request; block_table: int32[B][max_pages]; free_pages: int32[num_pages].
