@@ -27,8 +27,8 @@
 //    num_splits == 1 each CTA takes whole units instead.
 //  * Paged keys and values (PAGED): the producer gathers a tile page by page (see the producer), and
 //    the work split comes from the requests' lengths inside the kernel (see Line).
-//  * REST: the first tiles of some requests' keys are attended to by another kernel (prefix.cu), which leaves the prefix of the
-//    tiles behind them.  What is not a request's whole attention goes to the workspace as partials that a third kernel merges.
+//  * REST: the first tiles of some requests' keys are attended to by other CTAs of the launch (prefix_kernel.cuh), which finds the
+//    work split.  What is not a request's whole attention goes to the workspace as partials that a second kernel merges.
 //  * Roles (decode_kernel<D, CAUSAL, NC, PAGED>): warps 0-3 softmax.  EPI (see
 //    has_epilogue_warps): warps 4-7 epilogue, warp 8 TMA producer, warp 9 MMA issuer, warp 10 the second
 //    producer of paged tiles, the rest only completes its warpgroup; at the end of a work item the
@@ -598,40 +598,65 @@ __device__ __forceinline__ void write_empty_entry(const DecodeParams& p, int b)
 // Columns the softmax computes for units of G rows (the MMA's N stays kN): 1, 4, 8 or 16.
 inline int decode_columns(int G) { return G <= 1 ? 1 : G <= 4 ? 4 : G <= 8 ? 8 : 16; }
 
-template <int D, bool CAUSAL, int NC, bool PAGED = false, bool REST = false>
-__global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()>(), 1)
-    decode_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
-                  const __grid_constant__ CUtensorMap vmap, const __grid_constant__ DecodeParams p)
+// A CTA's shared memory beside the tiles
+template <int D, bool PAGED>
+struct DecodeShared {
+    static constexpr int S = DecodeCfg<D>::kStages;
+    uint64_t q_full[2], q_empty[2], k_full[S], k_empty[S], v_full[S], v_empty[S];
+    // S, P and O of a tile alternate between two buffers without barriers for "empty": the MMA warp issues
+    // QK(k), PV(k - 1), QK(k + 1), .. and PV(k) waits for P(k), by when the softmax has read S(k) and O(k - 2);
+    // it stores P(k) after it has read O(k - 2), by when PV(k - 2) has read P(k - 2).
+    uint64_t s_full[2], p_full[2], o_full[2], mma_done;
+    uint64_t ep_full[2], ep_empty[2];   // softmax -> epilogue handoff
+    float ep_m[2][kN];                  // the columns' reference maxima
+    uint32_t tmem_slot;
+    int abort_flag;
+    float red_max[4][kN];
+    float red_sum[4][kN];
+    float col_inv[kN], col_lse[kN];   // per query column: 1 / L and the LSE of this range
+    int ep_abort, fx_last;          // softmax warps: abort snapshot, "this CTA merges"
+    int fx_n;
+    int fx_slot[kMaxFixSlots];
+    float fx_w[kN][kFixChunk], fx_lse[kN];   // merge: per column, the partials' weights and the merged LSE
+    int pre_sh[PAGED ? kInlineB + 1 : 1], keys_sh[PAGED ? kInlineB : 1];
+    int2 sums_sh[PAGED ? 12 : 1];
+    int4 start_raw[2];
+};
+
+// REST: what the launch has found out, and what it has set up
+struct RestPlan {
+    const int *pre, *keys;   // prefix of the batch entries' tiles, and their keys (or NULL)
+    Line line;
+    Start first;
+    int end;
+    uint32_t tmem;
+};
+
+// The kernel's body for CTA `cta` of `ctas`; smem: the tiles' shared memory, 1024-byte aligned
+template <int D, bool CAUSAL, int NC, bool PAGED, bool REST>
+__device__ __forceinline__ void decode_body(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap, const DecodeParams& p,
+                                            DecodeShared<D, PAGED>& sh, uint8_t* smem, int cta, int ctas, const RestPlan& plan)
 {
     using C = DecodeCfg<D>;
     constexpr int S = C::kStages;
     constexpr bool EPI = has_epilogue_warps<NC, PAGED>();
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-
-    __shared__ uint64_t q_full[2], q_empty[2], k_full[S], k_empty[S], v_full[S], v_empty[S];
-    // S, P and O of a tile alternate between two buffers without barriers for "empty": the MMA warp issues
-    // QK(k), PV(k - 1), QK(k + 1), .. and PV(k) waits for P(k), by when the softmax has read S(k) and O(k - 2);
-    // it stores P(k) after it has read O(k - 2), by when PV(k - 2) has read P(k - 2).
-    __shared__ uint64_t s_full[2], p_full[2], o_full[2], mma_done;
-    __shared__ uint64_t ep_full[2], ep_empty[2];   // softmax -> epilogue handoff
-    __shared__ float ep_m[2][kN];                  // the columns' reference maxima
-    __shared__ uint32_t tmem_slot;
-    __shared__ int abort_flag;
-    __shared__ float red_max[4][kN];
-    __shared__ float red_sum[4][kN];
-    __shared__ float col_inv[kN], col_lse[kN];   // per query column: 1 / L and the LSE of this range
-    __shared__ int ep_abort, fx_last;          // softmax warps: abort snapshot, "this CTA merges"
-    __shared__ int fx_n;
-    __shared__ int fx_slot[kMaxFixSlots];
-    __shared__ float fx_w[kN][kFixChunk], fx_lse[kN];   // merge: per column, the partials' weights and the merged LSE
-    __shared__ int pre_sh[PAGED ? kInlineB + 1 : 1], keys_sh[PAGED ? kInlineB : 1];
-    __shared__ int2 sums_sh[PAGED ? 12 : 1];
-    __shared__ int4 start_raw[2];
-    Start* start_sh = reinterpret_cast<Start*>(start_raw);
+    auto &q_full = sh.q_full, &q_empty = sh.q_empty, &s_full = sh.s_full, &p_full = sh.p_full, &o_full = sh.o_full, &ep_full = sh.ep_full, &ep_empty = sh.ep_empty;
+    auto &k_full = sh.k_full, &k_empty = sh.k_empty, &v_full = sh.v_full, &v_empty = sh.v_empty;
+    auto &ep_m = sh.ep_m;
+    auto &red_max = sh.red_max, &red_sum = sh.red_sum;
+    auto &col_inv = sh.col_inv, &col_lse = sh.col_lse, &fx_lse = sh.fx_lse;
+    auto &fx_slot = sh.fx_slot;
+    auto &fx_w = sh.fx_w;
+    auto &pre_sh = sh.pre_sh;
+    auto &keys_sh = sh.keys_sh;
+    auto &sums_sh = sh.sums_sh;
+    uint64_t& mma_done = sh.mma_done;
+    uint32_t& tmem_slot = sh.tmem_slot;
+    int &abort_flag = sh.abort_flag, &ep_abort = sh.ep_abort, &fx_last = sh.fx_last, &fx_n = sh.fx_n;
+    Start* start_sh = reinterpret_cast<Start*>(sh.start_raw);
 
     const int warp = threadIdx.x / 32;
-    griddep_launch_dependents();
+    if constexpr (!REST) griddep_launch_dependents();
     const WaitCtl wc{&abort_flag, p.status, p.limit};
 
     if (threadIdx.x == 0) {
@@ -654,9 +679,11 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
         mbar_init(&mma_done, 1);
         fence_barrier_init();
     }
-    if (warp == mma_warp<EPI>()) {
-        tmem_alloc(&tmem_slot, C::tmem_cols(NC, PAGED));
-        tmem_relinquish();
+    if constexpr (!REST) {
+        if (warp == mma_warp<EPI>()) {
+            tmem_alloc(&tmem_slot, C::tmem_cols(NC, PAGED));
+            tmem_relinquish();
+        }
     }
     if constexpr (PAGED) {
         if (threadIdx.x == tma_warp<EPI>() * 32) {
@@ -668,16 +695,22 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tmem_slot;   // S buffers at columns 0/16, handoff at 64/96, O buffers at o_col()
-    griddep_wait();   // the previous kernel of the stream has completed: global memory from here on
-    if (blockIdx.x == 0 && threadIdx.x == 0 && p.nv_ts) *p.nv_ts = *p.nv_sg;   // single-pass NVFP4: report s_g
+    const uint32_t tmem = REST ? plan.tmem : tmem_slot;   // S buffers at columns 0/16, handoff at 64/96, O buffers at o_col()
+    if constexpr (!REST) griddep_wait();   // the previous kernel of the stream has completed: global memory from here on
+    if (!REST && cta == 0 && threadIdx.x == 0 && p.nv_ts) *p.nv_ts = *p.nv_sg;   // single-pass NVFP4: report s_g
 
     const int *pre = p.prefix, *keys = nullptr;
     Start first;        // paged split mode: the CTA's range of tiles
     int end = 0;
     Line line;
-    if constexpr (PAGED) {
-        const int B = p.U / p.Hkv, c = static_cast<int>(blockIdx.x), lane = static_cast<int>(threadIdx.x) & 31;
+    if constexpr (REST) {
+        pre = plan.pre;
+        keys = plan.keys;
+        line = plan.line;
+        first = plan.first;
+        end = plan.end;
+    } else if constexpr (PAGED) {
+        const int B = p.U / p.Hkv, c = cta, lane = static_cast<int>(threadIdx.x) & 31;
         // the CTA's cut at x, in batch entry b of nt tiles a unit whose first tile is s0
         auto start_at = [&](int x, int b, int s0, int nt) {
             Start r;
@@ -706,7 +739,7 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
             }
             const int start = inc - nt;
             line.T = __shfl_sync(0xffffffffu, inc, 31) * p.Hkv;
-            line.P = paged_ctas(line.T, __popc(__ballot_sync(0xffffffffu, n > 0)) * p.Hkv, static_cast<int>(gridDim.x));
+            line.P = paged_ctas(line.T, __popc(__ballot_sync(0xffffffffu, n > 0)) * p.Hkv, ctas);
             keys_sh[lane] = n;
             pre_sh[lane] = start;
             if (lane == 31) pre_sh[32] = inc;
@@ -758,7 +791,7 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
                 with_keys += v.y;
             }
             line.T = total * p.Hkv;
-            line.P = paged_ctas(line.T, with_keys * p.Hkv, static_cast<int>(gridDim.x));
+            line.P = paged_ctas(line.T, with_keys * p.Hkv, ctas);
             const int cut[2] = {line.cut(c), line.cut(c + 1)};
             int run = before + inc - own;
             for (int b = b0; b < b1; ++b) {
@@ -791,13 +824,13 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
     }
 
     Sched<PAGED, REST> sched;
-    sched.init(&p, blockIdx.x, gridDim.x, pre, keys, first, end);
+    sched.init(&p, cta, ctas, pre, keys, first, end);
     Item it;
 
     // fills fx_slot with the slots of the unit's partials
     auto partial_slots = [&](const Item& it) {
         if constexpr (PAGED) return paged_partial_slots(p, pre, line, it.b, it.head * p.chunks + it.chunk, fx_slot, kMaxFixSlots);
-        return unit_partial_slots(p, it.u, static_cast<int>(gridDim.x), fx_slot, kMaxFixSlots);
+        return unit_partial_slots(p, it.u, ctas, fx_slot, kMaxFixSlots);
     };
 
     // The epilogue of one item, run by 128 threads: the epilogue warpgroup (named barrier 2) or, without
@@ -1500,16 +1533,29 @@ __global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()
 
     tc_fence_before();
     __syncthreads();
-    if (warp == mma_warp<EPI>()) tmem_dealloc(tmem, C::tmem_cols(NC, PAGED));
-    if constexpr (PAGED) {
+    if constexpr (!REST) {
+        if (warp == mma_warp<EPI>()) tmem_dealloc(tmem, C::tmem_cols(NC, PAGED));
+    }
+    if constexpr (PAGED && !REST) {
         const int B = p.U / p.Hkv;
-        if (blockIdx.x == 0)
+        if (cta == 0)
             for (int b = threadIdx.x; b < B; b += blockDim.x)
                 if (p.seqlens[b] < 0 || p.seqlens[b] > p.cap) report_bad_page(p.status);
         if (p.fixup)   // no combine kernel runs: entries without keys are written here
-            for (int b = blockIdx.x; b < B; b += gridDim.x)
+            for (int b = cta; b < B; b += ctas)
                 if (pre[b + 1] == pre[b]) write_empty_entry(p, b);
     }
+}
+
+template <int D, bool CAUSAL, int NC, bool PAGED = false>
+__global__ void __launch_bounds__(decode_threads<has_epilogue_warps<NC, PAGED>()>(), 1)
+    decode_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                  const __grid_constant__ CUtensorMap vmap, const __grid_constant__ DecodeParams p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ DecodeShared<D, PAGED> sh;
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    decode_body<D, CAUSAL, NC, PAGED, false>(qmap, kmap, vmap, p, sh, smem, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), RestPlan{});
 }
 
 // Exclusive prefix of per-unit tile counts (ragged keys), one block.

@@ -22,6 +22,104 @@
 namespace atc_gb300 {
 namespace {
 
+struct PagedWs {
+    size_t prefix_off, ctr_off, lse_off, o_off, stage_off, amax_off, total;
+};
+
+// The kernel merges split units itself, except for single-pass NVFP4, whose rows a combine kernel encodes (as in
+// the dense decode), and for more SMs than it has slots for a unit's partials.  It finds the work split itself,
+// except for very large batches, and where the combine kernel, which takes it from global memory, is to see it.
+bool needs_combine(bool encode, int nsm) { return encode || nsm > kMaxFixSlots; }
+bool needs_prefix(int B, bool encode, int nsm) { return needs_combine(encode, nsm) || B > kInlineB; }
+
+PagedWs paged_ws(int B, int Hq, int Sq, const fmha_kv_cache* c, const fmha_opts* o)
+{
+    auto al = [](size_t x) { return (x + 255) & ~size_t(255); };
+    const Shape s = paged_shape(B, Hq, Sq, c);
+    if (s.U == 0) return {};   // nothing to do, nothing to do it in
+    const int nsm = num_sms() > 0 ? num_sms() : 256;   // sized for the largest plausible SM count
+    const bool split = o && o->num_splits != 1;
+    const size_t slots = split ? static_cast<size_t>(s.U) + nsm : 0;
+    PagedWs w{};
+    size_t off = 0;
+    w.prefix_off = off;
+    off += split && needs_prefix(B, o->nvfp4_scale_in != nullptr, nsm) ? al((static_cast<size_t>(B) + 2) * 4) : 0;
+    w.ctr_off = off;
+    off += split ? al(static_cast<size_t>(s.U) * 8) : 0;
+    w.lse_off = off;
+    off += al(slots * kN * 4);
+    w.o_off = off;
+    off += al(slots * kN * c->D * 4);
+    const bool two_pass = o && o->out_kind == FMHA_OUT_NVFP4 && !o->nvfp4_scale_in;
+    w.stage_off = off;
+    off += two_pass && !o->out_f32 ? al(static_cast<size_t>(B) * Hq * Sq * c->D * 4) : 0;
+    w.amax_off = off;
+    off += two_pass ? 256 : 0;
+    w.total = off;
+    return w;
+}
+
+template <int D, bool CAUSAL>
+auto kernel_for(int G) -> decltype(&decode_kernel<D, CAUSAL, 1, true>)
+{
+    switch (decode_columns(G)) {
+        case 1: return decode_kernel<D, CAUSAL, 1, true>;
+        case 4: return decode_kernel<D, CAUSAL, 4, true>;
+        case 8: return decode_kernel<D, CAUSAL, 8, true>;
+        default: return decode_kernel<D, CAUSAL, 16, true>;
+    }
+}
+
+template <int D, bool CAUSAL>
+int run_paged(const PagedArgs& a, bool split, const PagedWs& w, uint8_t* base, cudaStream_t st)
+{
+    using C = DecodeCfg<D>;
+    const int nsm = num_sms();
+    if (nsm <= 0) return set_error(FMHA_ERR_CUDA, "cannot query the SM count");
+    const Shape s = paged_shape(a.B, a.Hq, a.Sq, a.c);
+    CUtensorMap maps[3];
+    DecodeParams p;
+    const int rc = paged_setup<D>(a, s, maps, p);
+    if (rc) return rc;
+    p.split = split ? 1 : 0;
+    p.fixup = split && !needs_combine(a.nv_sg != nullptr, nsm) ? 1 : 0;
+    p.prefix = split && needs_prefix(a.B, a.nv_sg != nullptr, nsm) ? reinterpret_cast<const int32_t*>(base + w.prefix_off) : nullptr;
+    p.o_stage = a.o_stage;
+    p.amax_bits = a.amax_bits;
+    p.nv_sg = a.nv_sg;
+    p.nv_codes = a.nv_codes;
+    p.nv_scales = a.nv_scales;
+    p.nv_ts = a.nv_ts;
+    p.part_lse = split ? reinterpret_cast<float*>(base + w.lse_off) : nullptr;
+    p.part_o = split ? reinterpret_cast<float*>(base + w.o_off) : nullptr;
+    p.unit_ctr = split ? reinterpret_cast<unsigned long long*>(base + w.ctr_off) : nullptr;
+    p.gen = next_call_tag();
+
+    // one CTA per SM, or fewer when even full tables have fewer key tiles (whole units: fewer units)
+    const long long tiles = split ? static_cast<long long>(s.U) * ((p.cap + kTileKV - 1) / kTileKV) : s.U;
+    const unsigned grid = static_cast<unsigned>(tiles < nsm ? tiles : nsm);
+    p.ctas = static_cast<int>(grid);
+    if (p.prefix) {
+        FMHA_CHECK_CUDA(launch_pdl(tile_prefix_kernel<true>, dim3(1), dim3(1024), 0, st, p, const_cast<int32_t*>(p.prefix)));
+        count_launch();
+    }
+    const auto kernel = kernel_for<D, CAUSAL>(s.G);
+    const int smem = C::smem_bytes(decode_columns(s.G), true);
+    FMHA_CHECK_CUDA(set_smem_limit_once(reinterpret_cast<const void*>(kernel), smem));
+    timing_mark_begin(st);
+    const cudaError_t e = launch_pdl(kernel, dim3(grid), dim3(decode_threads<true>()), static_cast<size_t>(smem),
+                                     st, maps[0], maps[1], maps[2], p);
+    timing_mark_end(st);
+    FMHA_CHECK_CUDA(e);
+    count_launch();
+    if (split && !p.fixup) {
+        FMHA_CHECK_CUDA(launch_pdl(combine_kernel<true>, dim3(static_cast<unsigned>(s.U * s.G)), dim3(static_cast<unsigned>(D)), 0,
+                                   st, p, static_cast<int>(grid)));
+        count_launch();
+    }
+    return FMHA_OK;
+}
+
 int check_paged(const fmha_kv_cache* c, int B, int Hq, int Sq, int max_pages, const fmha_opts* o)
 {
     const char* who = "fmha_fwd_paged";
