@@ -554,11 +554,23 @@ struct Plan {
 };
 
 // What a step of the kernel costs where memory does not bound it, in 0.1 us: a key tile with two row tiles, with one, a tile of own keys,
-// and a request and key/value head of them (B300, D = 128 and 64: slopes over the number of groups and requests)
+// and a request and key/value head of them (D = 128 and 64: slopes over the number of groups and requests)
 template <int D>
 struct Cost {
-    static constexpr int kTwo = D == 128 ? 25 : 20, kOne = D == 128 ? 15 : 10, kOwn = D == 128 ? 10 : 7, kUnit = 10;
+    static constexpr int kTwo = D == 128 ? 25 : 20, kOne = D == 128 ? 15 : 10;
+    static constexpr int own(bool many) { return D == 128 ? (many ? 12 : 10) : (many ? 11 : 7); }   // more than 8 rows, which 16 columns hold
+    static constexpr int unit(bool many) { return many ? 30 : 10; }
+    static constexpr int kStart = 60;   // what CTAs of common keys take more than those of own keys, whatever their part
 };
+
+// x of n CTAs such that common / x + kStart = own / (n - x): both kinds end at the same time
+template <int D>
+__device__ __forceinline__ float common_share(float n, float common, float own)
+{
+    constexpr float d = Cost<D>::kStart;
+    const float h = d * n - common - own;
+    return (h + sqrtf(h * h + 4.f * d * common * n)) / (2.f * d);
+}
 
 // By the whole CTA.  scratch: 3 N + 1 ints; pre, keys: B + 1 and B ints of shared memory, or NULL (then the prefix is global)
 template <int D>
@@ -619,15 +631,15 @@ __device__ __forceinline__ void make_plan(const PrefixParams& p, int* scratch, i
         with_keys += sums2[w].x;
     }
     out.own.T = total * p.rest_units;
-    // the common keys get the share of the CTAs that their work is of all
+    // the CTAs of common keys
     using K = Cost<D>;
     const long long cost = static_cast<long long>(K::kOne) * (out.common.T - twos) + static_cast<long long>(K::kTwo) * twos,
-                    other = static_cast<long long>(p.rest_units) * (static_cast<long long>(K::kOwn) * total + static_cast<long long>(K::kUnit) * with_keys);
+                    other = static_cast<long long>(p.rest_units) * (static_cast<long long>(K::own(p.R > 8)) * total + static_cast<long long>(K::unit(p.R > 8)) * with_keys);
     // (in pairs of CTAs, see prefix_kernel)
     out.border = out.common.P = 0;
     if (out.common.T > 0) {
         const int pairs = ctas / 2;
-        const int share = other > 0 ? min(max(static_cast<int>((pairs * cost + (cost + other) / 2) / (cost + other)), 1), pairs - 1) : pairs;
+        const int share = other > 0 ? min(max(static_cast<int>(common_share<D>(static_cast<float>(ctas), static_cast<float>(cost), static_cast<float>(other)) * 0.5f + 0.5f), 1), pairs - 1) : pairs;
         out.common.P = paged_ctas(out.common.T, units, 2 * share);
         out.border = (out.common.P + 1) & ~1;
     }
