@@ -180,7 +180,9 @@ def fmha_fwd(q, k, v, out, lse, scale: float, stream=None):
 def make_opts(out_kind=FMHA_OUT_BF16, seqlens_k=None, num_splits=0, workspace=None,
               out_scales=None, out_tensor_scale=None, out_f32=None, causal=False,
               nvfp4_scale_in=None, out_amax=None, wide_variant=FMHA_WIDE_AUTO) -> fmha_opts:
+    """Options of a call; they keep the tensors they name alive."""
     o = fmha_opts()
+    o.tensors = (seqlens_k, workspace, out_scales, out_tensor_scale, out_f32, nvfp4_scale_in, out_amax)
     o.wide_variant = wide_variant
     o.causal = 1 if causal else 0
     o.nvfp4_scale_in = None if nvfp4_scale_in is None else nvfp4_scale_in.data_ptr()
