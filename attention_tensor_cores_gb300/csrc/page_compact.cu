@@ -56,7 +56,7 @@ __device__ __forceinline__ void translate_rows(const CompactParams& p, int first
         const long long len = p.seqlens[b], held_tokens = len < 0 ? 0 : len > room ? room : len;
         const int k = p.by_page.up(static_cast<int>(held_tokens));
         const size_t row = static_cast<size_t>(b) * p.max_pages;
-        for (int s = v - b * shared; s * 128 < k; s += shared) {
+        for (int s = v - b * shared; static_cast<long long>(s) * 128 < k; s += shared) {
             int x[4], to[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {

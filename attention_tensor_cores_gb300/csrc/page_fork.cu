@@ -13,7 +13,8 @@
 //
 // One launch.  A CTA, or a cluster of eight for larger tables, marks gone and kept pages in sets of bits, counts the freed
 // ones in the order of ids and hands out the copies' pages; more clusters, if the tables are large, copy the rows meanwhile.
-// Bound: latency, a chain of lengths and parents -> rows -> sets -> stack -> last pages.
+// Bound: latency, a chain of lengths and parents -> rows -> sets -> stack -> last pages.  2 groups of 4 beams 5.7 us, one request
+// into 64 samples 5.2, 128 groups of 4 with 16384 tokens each at most 9.1 (from a CUDA graph).
 #include <cuda_runtime.h>
 
 #include "cluster_bits.cuh"
@@ -104,7 +105,7 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kForkThreads, 1) 
         const int shared = max(1, min(p.segments, nw / max(n, 1)));   // warps of a row
         for (int v = w; v < n * shared; v += nw) {
             const int i = v / shared, k = count(i);
-            for (int s = v - i * shared; s * kSegment < k; s += shared) {
+            for (int s = v - i * shared; static_cast<long long>(s) * kSegment < k; s += shared) {
                 const int32_t* row = from(i);
                 int x[kSegment / 32];
 #pragma unroll

@@ -135,3 +135,54 @@ def test_the_data_follows():
     after = [[x[new[b, j]] for b in range(3) for j in range(up(lens[b], 16))] for x in (k, v)]
     assert all(torch.equal(x, y) for p, q in zip(before, after) for x, y in zip(p, q))
     assert new[0, 0] < 30 and max(int(new[b, j]) for b in range(3) for j in range(up(lens[b], 16))) < 30
+
+
+def test_captured():
+    """The graph of a compaction and its copies, replayed over other tables and stacks."""
+    rng = np.random.default_rng(12)
+    pages, P = 40_000, 16     # two launches
+    i32 = dict(dtype=torch.int32, device="cuda")
+    scenes = [scene(pages, 30, used, P, rng) for used in (17_000, 25_000, 39_999)]
+    width = max(s[1].shape[1] for s in scenes)
+    lens, n = torch.zeros(30, **i32), torch.zeros(1, **i32)
+    table, new = torch.full((30, width), -1, **i32), torch.zeros(30, width, **i32)
+    stack, ids, out, src, dst, moves = (torch.zeros(k, **i32) for k in (pages, pages, pages, pages // 2, pages // 2, 1))
+    k, v = (torch.zeros(pages, 1, P, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    cache = F.make_kv_cache(k, v)
+
+    def step():
+        F.fmha_page_compact(lens, P, table, stack, n, ids, new, src, dst, moves, out)
+        F.fmha_page_copy([cache], src, dst, None, moves)
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for s in scenes:
+        lens.copy_(torch.tensor(s[0]))
+        table[:, :s[1].shape[1]] = torch.tensor(s[1], **i32)
+        stack[:len(s[2])] = torch.tensor(s[2], **i32)
+        n.fill_(len(s[2]))
+        k.copy_(torch.randint(-128, 128, k.shape, device="cuda"))
+        v.copy_(-k)
+        before = k.clone()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert F.fmha_check_status() == F.FMHA_OK
+        used = pages - len(s[2])
+        for b in range(30):
+            h = up(s[0][b], P)
+            assert h == 0 or int(new[b, :h].max()) < used
+            assert torch.equal(k[new[b, :h].long()], before[table[b, :h].long()]) and torch.equal(v[new[b, :h].long()], -before[table[b, :h].long()])
+        assert out[:pages - used].tolist() == list(range(pages - 1, used - 1, -1))
+
+
+def test_longest_row():
+    """A row of nearly 2^31 entries, all of the pool's only page."""
+    i32 = dict(dtype=torch.int32, device="cuda")
+    width = (1 << 31) - 300
+    table, new = torch.zeros(1, width, **i32), torch.full((1, width), -9, **i32)
+    ids, moves, n = torch.zeros(1, **i32), torch.zeros(1, **i32), torch.zeros(1, **i32)
+    src, dst, stack, out = (torch.zeros(4, **i32) for _ in range(4))
+    F.fmha_page_compact(torch.tensor([width - 1], **i32), 1, table, stack[:1], n, ids, new, src, dst, moves, out[:1])
+    assert F.fmha_check_status() == F.FMHA_OK
+    assert int(new[0, -1]) == -9 and not any(bool(c.any()) for c in new[0, :-1].split(1 << 28))

@@ -166,3 +166,19 @@ def test_large_batch():
     table, left = shared_rows(lens, [0] * B, 1, P, rng, pages, 8)
     parents = rng.integers(-1, B, B)
     check([int(x) for x in parents], lens, P, table, left, pages)
+
+
+def test_longest_row():
+    """A row of nearly 2^31 entries, all of the pool's only page: handed on, then given back."""
+    i32 = dict(dtype=torch.int32, device="cuda")
+    width = (1 << 31) - 300
+    table, new = torch.zeros(1, width, **i32), torch.full((1, width), -9, **i32)
+    lens, seqlens, src, dst, tok, n = torch.tensor([width - 1], **i32), *(torch.zeros(1, **i32) for _ in range(5))
+    stack = torch.full((1,), -5, **i32)
+    F.fmha_page_fork(torch.zeros(1, **i32), lens, 1, table, stack, n, new, seqlens, src, dst, tok, n)
+    assert F.fmha_check_status() == F.FMHA_OK
+    assert seqlens.item() == width - 1 and n.item() == 0 and src.item() == -1
+    assert int(new[0, -1]) == -9 and not any(bool(c.any()) for c in new[0, :-1].split(1 << 28))
+    F.fmha_page_fork(torch.full((1,), -1, **i32), lens, 1, table, stack, n, new, seqlens, src, dst, tok, n)
+    assert F.fmha_check_status() == F.FMHA_OK
+    assert n.item() == 1 and stack.item() == 0 and seqlens.item() == 0
