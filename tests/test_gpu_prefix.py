@@ -197,3 +197,128 @@ def test_nan_and_infinite_scores():
     bad = torch.zeros(4, 4, 1, dtype=torch.bool)
     bad[1, 2] = bad[3, 0] = True
     assert torch.equal(out.isnan().all(-1).cpu(), bad) and torch.equal(lse.isnan().cpu(), bad)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_forced_timeout_is_reported(D):
+    """With a wait limit of one cycle the kernel drains and reports; the next call is right."""
+    gr = Groups([[1500, 1400, 1300], [1300]], [1280, 0], 16, 2, D)
+    q = torch.randn(4, 8, 1, D, generator=torch.Generator().manual_seed(5)).to(torch.bfloat16)
+    assert F.fmha_check_status() == 0
+    F.fmha_set_wait_limit(1)
+    try:
+        call(q.cuda(), gr)
+        rc = F.fmha_check_status()
+    finally:
+        F.fmha_set_wait_limit(0)
+    assert rc == F.FMHA_ERR_TIMEOUT
+    out, lse = call(q.cuda(), gr)
+    assert F.fmha_check_status() == 0
+    check_attention(out, lse, attention_ref(q, *gr.dense, gr.lens, D ** -0.5, False))
+
+
+def test_other_stream_and_no_lse():
+    gr = Groups([[700, 800, 650], [50]], [640, 0], 16, 2, 64)
+    q = torch.randn(4, 8, 1, 64, generator=torch.Generator().manual_seed(5)).to(torch.bfloat16).cuda()
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream()
+    out, lse = call(q, gr, stream=stream)
+    stream.synchronize()
+    ref = attention_ref(q.cpu(), *gr.dense, gr.lens, 0.125, False)
+    assert F.fmha_check_status(stream) == 0
+    check_attention(out, lse, ref)
+    cache = F.make_kv_cache(gr.k, gr.v)
+    ws = torch.empty(F.fmha_prefix_workspace_size(4, 8, 1, cache, F.make_opts()), dtype=torch.uint8, device="cuda")
+    F.fmha_fwd_prefix(q, cache, gr.table, gr.seqlens, gr.cu, gr.prefix_lens, out.zero_(), None, 0.125, F.make_opts(workspace=ws))
+    check_attention(out, None, ref)
+    # an output that is only 16-byte aligned
+    wide = torch.zeros(out.numel() + 4, device="cuda")[4:].view(out.shape)
+    F.fmha_fwd_prefix(q, cache, gr.table, gr.seqlens, gr.cu, gr.prefix_lens, wide, lse, 0.125, F.make_opts(out_kind=F.FMHA_OUT_F32, workspace=ws))
+    assert F.fmha_check_status() == 0
+    check_attention(wide, lse, ref, bf16=False)
+
+
+def test_nothing_to_do():
+    gr = Groups([[700, 800]], [640], 16, 2, 64)
+    cache = F.make_kv_cache(gr.k, gr.v)
+    empty = torch.empty(0, 8, 1, 64, dtype=torch.bfloat16, device="cuda")
+    none = torch.zeros(0, dtype=torch.int32, device="cuda")
+    F.fmha_fwd_prefix(empty, cache, gr.table[:0], none, torch.zeros(1, dtype=torch.int32, device="cuda"), none, empty, None, 1.0, F.make_opts())
+    q = torch.empty(2, 8, 0, 64, dtype=torch.bfloat16, device="cuda")
+    F.fmha_fwd_prefix(q, cache, gr.table, gr.seqlens, gr.cu, gr.prefix_lens, q, None, 1.0, F.make_opts())
+    with pytest.raises(F.FmhaError) as e:      # no workspace
+        F.fmha_fwd_prefix(torch.zeros(2, 8, 1, 64, dtype=torch.bfloat16, device="cuda"), cache, gr.table, gr.seqlens, gr.cu, gr.prefix_lens,
+                          torch.zeros(2, 8, 1, 64, dtype=torch.bfloat16, device="cuda"), None, 1.0, F.make_opts())
+    assert e.value.code == F.FMHA_ERR_WORKSPACE
+
+
+def test_far_pages():
+    """Pages past 2^31 elements of the pool."""
+    gr = Groups([[300, 290, 280, 270, 260], [40]], [256, 0], 16, 1, 64)
+    pages, big = gr.k.shape[0], torch.zeros((1 << 32) // 1 + (1 << 20), dtype=torch.bfloat16, device="cuda")
+    step = (1 << 32) // pages // 64 * 64
+    k, v = (big.as_strided(gr.k.shape, (step, 1024, 64, 1), o) for o in (0, 1024))
+    k.copy_(gr.k)
+    v.copy_(gr.v)
+    gr.k, gr.v = k, v
+    q = torch.randn(6, 4, 1, 64, generator=torch.Generator().manual_seed(5)).to(torch.bfloat16)
+    out, lse = call(q.cuda(), gr)
+    assert F.fmha_check_status() == 0
+    check_attention(out, lse, attention_ref(q, *gr.dense, gr.lens, 0.125, False))
+
+
+@pytest.mark.parametrize("groups, members", [(8192, 1), (3000, 2), (1, 8192), (40, 100)])
+def test_large_batches(groups, members):
+    """Against the paged attention (the 64-bit statement would take minutes)."""
+    rng = torch.Generator().manual_seed(groups)
+    B, P, D = groups * members, 16, 64
+    m = 20 if members > 1 else 0                     # common pages of each group
+    rest = torch.randint(1, 30, (B,), generator=rng)
+    lens = (m * P + rest).int()
+    table = torch.full((B, m + 3), -1, dtype=torch.int32)
+    table[:, :m] = torch.arange(groups * m).view(groups, m).repeat_interleave(members, 0) if m else 0
+    table[:, m:m + 2] = groups * m + torch.arange(2 * B).view(B, 2)
+    pages = groups * m + 2 * B
+    k, v = (torch.randn(pages, 1, P, D, device="cuda").to(torch.bfloat16) for _ in range(2))
+    cache = F.make_kv_cache(k, v)
+    q = torch.randn(B, 2, 1, D, device="cuda").to(torch.bfloat16)
+    table, lens = table.cuda(), lens.cuda()
+    cu, prefix = torch.arange(0, B + 1, members).int().cuda(), torch.full((groups,), m * P, dtype=torch.int32, device="cuda")
+    outs = []
+    for name in ("fmha_prefix_workspace_size", "fmha_paged_workspace_size"):
+        ws = torch.full((getattr(F, name)(B, 2, 1, cache, F.make_opts()),), 0xff, dtype=torch.uint8, device="cuda")
+        out, lse = torch.zeros(q.shape, device="cuda"), torch.zeros(B, 2, 1, device="cuda")
+        opts = F.make_opts(out_kind=F.FMHA_OUT_F32, workspace=ws)
+        if "prefix" in name:
+            F.fmha_fwd_prefix(q, cache, table, lens, cu, prefix, out, lse, 0.125, opts)
+        else:
+            F.fmha_fwd_paged(q, cache, table, lens, out, lse, 0.125, opts)
+        assert F.fmha_check_status() == 0
+        outs.append((out, lse))
+    # each is within check_attention's bound of the exact result, (2^-12 + 2^-13 + 2^-16) sum p |v| <= .. max |v|; |lse| stays below 64
+    assert (outs[0][0] - outs[1][0]).abs().max() <= 2 * float(v.abs().max()) * (2.0 ** -12 + 2.0 ** -13 + 2.0 ** -16)
+    assert float(outs[0][1].abs().max()) < 64
+    assert (outs[0][1] - outs[1][1]).abs().max() <= 2 * (2.0 ** -12 + 2.0 ** -14)
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_sweep(seed):
+    r = torch.Generator().manual_seed(1000 + seed)
+
+    def pick(*xs):
+        return xs[int(torch.randint(0, len(xs), (1,), generator=r))]
+
+    def upto(n):
+        return int(torch.randint(0, n + 1, (1,), generator=r))
+    P, Hkv, Sq = pick(8, 16, 24, 64, 128), pick(1, 2, 3, 5), pick(1, 1, 2, 3, 4)
+    G = pick(1, 2, 3, 4, 5, 8, 16, 21)
+    lens, prefix = [], []
+    for _ in range(1 + upto(4)):
+        p = upto(1500) // P * P
+        kind = upto(5)
+        lens.append([0 if kind == 0 and upto(3) == 0 else max(0, p + upto(300) - (upto(200) if kind == 1 else 0)) for _ in range(upto(12))])
+        prefix.append(p)
+    if not any(lens):
+        lens, prefix = [[5]], [0]
+    run(lens, prefix, P=P, Hq=G * Hkv, Hkv=Hkv, Sq=Sq, D=pick(64, 128), layout=pick("hnd", "nhd", "kv"), causal=Sq > 1 and upto(2) > 0,
+        kind=pick(F.FMHA_OUT_BF16, F.FMHA_OUT_BF16, F.FMHA_OUT_F32), seed=seed, scale=pick(1.0, 1.0, 3.0))
