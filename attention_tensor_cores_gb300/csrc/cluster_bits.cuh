@@ -1,6 +1,7 @@
 // Sets of pages as bits in shared memory, filled by the CTAs of a cluster together: each marks what it reads in a
 // whole set of its own, and the parts of the eight meet in an OR, a slice per CTA, so the order of the marks does not show.
-// (Marks straight into a set spread over the cluster's memory measured 20 us for 95,000 pages, one each 4 cycles; this 3.)
+// (Marks straight into a set spread over the cluster's memory cost one SM-to-SM atomic each: a compaction of 300,000 pages took
+// 63.4 us so, 17.4 with this and the tables translated from new_ids; a fork of 512 beams of 16384 tokens 27.9, now 9.1.)
 #pragma once
 #include "ptx.cuh"
 

