@@ -626,7 +626,6 @@ struct DecodeShared {
 // REST: what the launch has found out, and what it has set up
 struct RestPlan {
     const int *pre, *keys;   // prefix of the batch entries' tiles, and their keys (or NULL)
-    Line line;
     Start first;
     int end;
     uint32_t tmem;
@@ -706,7 +705,6 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& qmap, const CUten
     if constexpr (REST) {
         pre = plan.pre;
         keys = plan.keys;
-        line = plan.line;
         first = plan.first;
         end = plan.end;
     } else if constexpr (PAGED) {

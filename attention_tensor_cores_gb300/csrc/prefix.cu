@@ -4,6 +4,7 @@
 
 #include "paged_run.cuh"
 #include "prefix.h"
+#include "prefix_split.cuh"
 
 namespace atc_gb300 {
 namespace {
@@ -12,8 +13,9 @@ struct MergeParams {
     int rows, Hkv, R, nb;
     int shares;                // warps of a row: 1, 2, 4 or 8
     int G, chunks;             // of the decode kernel's units
+    int weigh;
     const int4* plan;
-    const int32_t* rest_prefix;
+    const int2* own;
     const float *common_o, *common_lse;   // partials of the groups' common keys
     const float *own_o, *own_lse;         // and of the requests' own: [U + SMs][16]
     void* out;                 // BF16 or F32, or NULL
@@ -37,21 +39,17 @@ __global__ void __launch_bounds__(256, 5) prefix_merge_kernel(const __grid_const
     if (row >= p.rows) return;   // the last block's, warps of whole rows
     const int unit = row / p.R, rr = row - unit * p.R, b = unit / p.Hkv, h = unit - b * p.Hkv, B = p.rows / (p.R * p.Hkv);
     const int4 head = p.plan[0], g = p.plan[1 + b];   // g: place, tiles, requests and first one of the group
-    const int before = p.rest_prefix[b], nt = p.rest_prefix[b + 1] - before;
-    Line own_line;
-    own_line.T = p.rest_prefix[B] * p.Hkv * p.chunks;
-    own_line.P = p.rest_prefix[B + 1];
-
-    // the CTAs [c, c + n) of a line have pieces of its unit of tiles [s, e)
-    const auto find = [](const Line& line, int s, int e, int& c, int& n) {
+    const int2 o = p.own[b];
+    // the CTAs [c, c + n) of a line have pieces of its unit of nt tiles at place s
+    const auto find = [](const Line& line, int s, int nt, UnitCost u, int& c, int& n) {
         const float per = static_cast<float>(line.P) / static_cast<float>(line.T);
-        const auto at = [&](int i) { return unit_cut(line.cut(i), s, e); };
+        const auto at = [&](int i) { return tile_at(line.cut(i) - s, nt, u); };
         c = max(min(static_cast<int>(static_cast<float>(s) * per), line.P - 1), 0);
-        while (c > 0 && at(c) > s) --c;
-        while (at(c + 1) <= s) ++c;
-        int d = max(min(static_cast<int>(static_cast<float>(e) * per), line.P), c + 1);
-        while (d < line.P && at(d) < e) ++d;
-        while (d > c + 1 && at(d - 1) >= e) --d;
+        while (c > 0 && at(c) > 0) --c;
+        while (at(c + 1) <= 0) ++c;
+        int d = max(min(static_cast<int>(static_cast<float>(s + u.of(nt)) * per), line.P), c + 1);
+        while (d < line.P && at(d) < nt) ++d;
+        while (d > c + 1 && at(d - 1) >= nt) --d;
         n = d - c;
     };
     // partial i of n1 + n2: first those of the group's common keys (of a pair of row tiles with one tile two a piece, `second` rows
@@ -61,17 +59,21 @@ __global__ void __launch_bounds__(256, 5) prefix_merge_kernel(const __grid_const
     if (g.y > 0) {
         Line line;
         line.T = head.x;
-        line.P = head.y;
-        const int pairs = row_pairs(g.z, p.nb), mem = b - g.w, r = mem / (2 * p.nb), s = g.x + (h * pairs + r) * g.y;
-        const int rows = min(2 * p.nb, g.z - r * 2 * p.nb) * p.R;
-        find(line, s, s + g.y, c1, n1);
+        line.P = head.y & (kByTiles - 1);
+        const UnitCost u = head.y & kByTiles ? UnitCost{1, 0, Cost<D>::common(g.z > p.nb).least} : Cost<D>::common(g.z > p.nb);
+        const int pairs = row_pairs(g.z, p.nb), mem = b - g.w, r = mem / (2 * p.nb), rows = min(2 * p.nb, g.z - r * 2 * p.nb) * p.R;
+        find(line, g.x + (h * pairs + r) * u.of(g.y), g.y, u, c1, n1);
         second = rows > p.nb * p.R ? 0 : rows;
         n1 <<= second ? 1 : 0;
         first1 = 2 * static_cast<long long>(g.w * p.Hkv + h * g.z + r * 2 * p.nb) * p.R + (mem - r * 2 * p.nb) * p.R + rr;
     }
-    if (nt > 0) {
-        const int chunk = rr / p.G, i = h * p.chunks + chunk, units = p.Hkv * p.chunks, s = before * units + i * nt;
-        find(own_line, s, s + nt, c2, n2);
+    if (o.y > 0) {
+        Line line;
+        line.T = head.z;
+        line.P = head.w;
+        const UnitCost u = p.weigh ? Cost<D>::own(p.R > 8) : UnitCost{};
+        const int chunk = rr / p.G, i = h * p.chunks + chunk, units = p.Hkv * p.chunks;
+        find(line, o.x + i * u.of(o.y), o.y, u, c2, n2);
         first2 = static_cast<long long>(b * units + i) * kN + rr - chunk * p.G;
     }
     if (p.out && n1 == 0 && n2 == 1) return;   // one piece was all of it and wrote the row (for all warps of the row)
@@ -82,16 +84,16 @@ __global__ void __launch_bounds__(256, 5) prefix_merge_kernel(const __grid_const
     for (int i0 = 0; i0 < mine; i0 += 32) {   // a lane per partial
         const int i = (i0 + lane) * p.shares + share, n = min(mine - i0, 32);
         long long at = 0;
-        const float *lse = p.common_lse, *o = p.common_o;
+        const float *lse = p.common_lse, *src = p.common_o;
         if (i < n1) {
             at = first1 + static_cast<long long>(c1 + (second ? i >> 1 : i)) * (2 * kRows) + (second && (i & 1) ? second : 0);
         } else {
             at = first2 + static_cast<long long>(c2 + i - n1) * kN;
             lse = p.own_lse;
-            o = p.own_o;
+            src = p.own_o;
         }
         const float x = lane < n ? __ldcg(lse + at) : -INFINITY;
-        o += at * D;
+        src += at * D;
         const float top = fmax_nan(m, redux_max_nan(x));
         if (top == -INFINITY) continue;   // no visible key so far
         const float keep = m == -INFINITY ? 0.f : __expf(m - top), w = lane < n ? __expf(x - top) : 0.f;
@@ -101,16 +103,16 @@ __global__ void __launch_bounds__(256, 5) prefix_merge_kernel(const __grid_const
         for (int v = 0; v < V; ++v) acc[v] *= keep;
 #pragma unroll 4
         for (int k = 0; k < n; ++k) {
-            const float* src = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), k)) + lane * V;
+            const float* from = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), k)) + lane * V;
             const float wk = __shfl_sync(0xffffffffu, w, k);
             if constexpr (V == 4) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(from));
                 acc[0] = fmaf(wk, v.x, acc[0]);
                 acc[1] = fmaf(wk, v.y, acc[1]);
                 acc[2] = fmaf(wk, v.z, acc[2]);
                 acc[3] = fmaf(wk, v.w, acc[3]);
             } else {
-                const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+                const float2 v = __ldcg(reinterpret_cast<const float2*>(from));
                 acc[0] = fmaf(wk, v.x, acc[0]);
                 acc[1] = fmaf(wk, v.y, acc[1]);
             }
@@ -170,7 +172,7 @@ __global__ void __launch_bounds__(256, 5) prefix_merge_kernel(const __grid_const
 }
 
 struct PrefixWs {
-    size_t plan_off, pre_off, common_lse_off, common_o_off, own_lse_off, own_o_off, stage_off, amax_off, total;
+    size_t plan_off, own_off, pre_off, common_lse_off, common_o_off, own_lse_off, own_o_off, stage_off, amax_off, total;
 };
 
 // With so many key tiles at most, all requests' tables full, every request is read by itself.  The plan, a cold softmax
@@ -197,7 +199,8 @@ PrefixWs prefix_ws(int B, int Hq, int Sq, const fmha_kv_cache* c, const fmha_opt
         off += al(bytes);
     };
     take(w.plan_off, (1 + static_cast<size_t>(B)) * sizeof(int4));
-    take(w.pre_off, (static_cast<size_t>(B) + 2) * 4);
+    take(w.own_off, static_cast<size_t>(B) * sizeof(int2));
+    take(w.pre_off, (static_cast<size_t>(B) + 1) * 4);
     take(w.common_lse_off, common * 4);
     take(w.common_o_off, common * c->D * 4);
     take(w.own_lse_off, own * 4);
@@ -318,7 +321,9 @@ extern "C" int fmha_fwd_prefix(const void* q, const fmha_kv_cache* cache, const 
     p.part_lse = reinterpret_cast<float*>(base + w.common_lse_off);
     p.plan = reinterpret_cast<int4*>(base + w.plan_off);
     p.rest_prefix = reinterpret_cast<int32_t*>(base + w.pre_off);
+    p.own = reinterpret_cast<int2*>(base + w.own_off);
     p.rest_units = p.Hkv * shape.chunks;
+    p.weigh = most < kMaxWeighed ? 1 : 0;
     p.status = device_status_ptr();
     p.limit = wait_limit();
 
@@ -345,7 +350,8 @@ extern "C" int fmha_fwd_prefix(const void* q, const fmha_kv_cache* cache, const 
     m.G = shape.G;
     m.chunks = shape.chunks;
     m.plan = p.plan;
-    m.rest_prefix = p.rest_prefix;
+    m.own = p.own;
+    m.weigh = p.weigh;
     m.common_o = p.part_o;
     m.common_lse = p.part_lse;
     m.own_o = reinterpret_cast<float*>(base + w.own_o_off);

@@ -31,9 +31,11 @@ struct PrefixParams {
     float* part_o;       // [rows][D] partials of common keys
     float* part_lse;
     // for the merge
-    int4* plan;          // [1 + B]: (tiles, CTAs) of the common keys' line; of each request its group's place on it, tiles, requests and first one
-    int32_t* rest_prefix;   // [B + 2]: tiles before each request's own, their number and the CTAs that they are split over
+    int4* plan;          // [1 + B]: (cost, CTAs) of the common and of the own keys' line; of each request its group's place, tiles, requests and first one
+    int2* own;           // [B]: each request's place on the own keys' line and its tiles there
+    int32_t* rest_prefix;   // [B + 1]: tiles before each request's own, and their number, when there are too many for shared memory
     int rest_units;      // units of a request's own keys
+    int weigh;           // the lines count costs, not tiles
     int* status;
     long long limit;
 };

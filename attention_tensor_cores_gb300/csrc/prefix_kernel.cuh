@@ -12,7 +12,7 @@
 //    bound, the others own keys, which memory bounds, as many of either as their work's share.  Lengths are on the device, so
 //    every CTA sums the groups and the requests itself (make_plan).
 //  * Work split.  The key tiles of all problems of a kind (group, kv-head and pair of row tiles; request and kv-head) are laid end to end
-//    and cut for the CTAs (as in decode_kernel.cuh); what is not a request's whole attention goes to the workspace as
+//    and cut for the CTAs (as in decode_kernel.cuh), by what they cost (prefix_split.cuh); what is not a request's whole attention goes to the workspace as
 //    normalised partials.
 //
 // Common keys:
@@ -32,6 +32,7 @@
 
 #include "paged_run.cuh"
 #include "prefix.h"
+#include "prefix_split.cuh"
 
 namespace atc_gb300 {
 namespace {
@@ -545,36 +546,24 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& qmap, const CUten
 
 // ---- the work split ----------------------------------------------------------------------------------------
 // What the launch's CTAs find out, each by itself, from the lengths: the common keys' line of tiles and its CTAs, the first of
-// the launch; the own keys' line and its CTAs, the others.
+// the launch; the own keys' line and its CTAs, the others.  first and end count tiles.
 struct Plan {
-    Line common, own;
+    Line common, own;   // of costs (UnitCost)
     int border;    // CTAs below take common keys
     Start first;   // of this CTA's part of its line
     int end;
 };
 
-// What a step of the kernel costs where memory does not bound it, in 0.1 us: a key tile with two row tiles, with one, a tile of own keys,
-// and a request and key/value head of them (D = 128 and 64: slopes over the number of groups and requests)
-template <int D>
-struct Cost {
-    static constexpr int kTwo = D == 128 ? 25 : 20, kOne = D == 128 ? 15 : 10;
-    static constexpr int own(bool many) { return D == 128 ? (many ? 12 : 10) : (many ? 11 : 7); }   // more than 8 rows, which 16 columns hold
-    static constexpr int unit(bool many) { return many ? 30 : 10; }
-    static constexpr int kStart = 60;   // what CTAs of common keys take more than those of own keys, whatever their part
-};
-
-// x of n CTAs such that common / x + kStart = own / (n - x): both kinds end at the same time
-template <int D>
-__device__ __forceinline__ float common_share(float n, float common, float own)
+// x of n CTAs such that common / x + d = own / (n - x): both kinds end at the same time
+__device__ __forceinline__ float common_share(float n, float common, float own, float d)
 {
-    constexpr float d = Cost<D>::kStart;
     const float h = d * n - common - own;
     return (h + sqrtf(h * h + 4.f * d * common * n)) / (2.f * d);
 }
 
 // By the whole CTA.  scratch: 3 N + 1 ints; pre, keys: B + 1 and B ints of shared memory, or NULL (then the prefix is global)
 template <int D>
-__device__ __forceinline__ void make_plan(const PrefixParams& p, int* scratch, int* pre, int* keys, int4* sums, int2* sums2, Start* start_sh, Plan& out)
+__device__ __forceinline__ void make_plan(const PrefixParams& p, int* scratch, int* pre, int* keys, int4* sums, int4* sums2, Start* start_sh, Plan& out)
 {
     const int B = p.B, N = p.gr.n, tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
     const int cta = static_cast<int>(blockIdx.x), ctas = static_cast<int>(gridDim.x);
@@ -584,7 +573,15 @@ __device__ __forceinline__ void make_plan(const PrefixParams& p, int* scratch, i
     const int per_b = (B + kPrefixThreads - 1) / kPrefixThreads, b0 = min(B, tid * per_b), b1 = min(B, b0 + per_b);
     const int len0 = b0 < b1 ? p.seqlens[b0] : 0;
     const bool grouped = load_groups(p.gr, B, cu, tiles, [&](int b) { return keys_of(p, b); });
-    const auto weight = [&](int g) { return p.Hkv * row_pairs(cu[g + 1] - cu[g], p.gr.nb) * tiles[g]; };
+    const UnitCost own = p.weigh ? Cost<D>::own(p.R > 8) : UnitCost{};
+    UnitCost one = Cost<D>::common(false), two = Cost<D>::common(true);
+    if (!p.weigh) {
+        one.tile = two.tile = 1;
+        one.start = two.start = 0;
+    }
+    const auto units_of = [&](int g) { return p.Hkv * row_pairs(cu[g + 1] - cu[g], p.gr.nb); };
+    const auto cost_of_kind = [&](int kind) { return kind & 1 ? two : one; };
+    const auto cost_of = [&](int g) { return cost_of_kind(cu[g + 1] - cu[g] > p.gr.nb ? 1 : 0); };
     const int g_first = grouped && b0 < b1 ? group_of(cu, N, b0) : 0;
     const auto length = [&](int b) { return b == b0 ? len0 : p.seqlens[b]; };
     const auto own_tiles = [&](int b, int& g) {   // and g becomes b's group
@@ -592,13 +589,17 @@ __device__ __forceinline__ void make_plan(const PrefixParams& p, int* scratch, i
             while (cu[g + 1] <= b) ++g;
         return max((min(max(length(b), 0), p.cap) + kTileKV - 1) / kTileKV - (grouped ? tiles[g] : 0), 0);
     };
-    int wg = 0, twos = 0, units = 0, wb = 0, with_keys = 0, g = g_first;
+    // each thread's sums: tiles, costs and units of common keys, tiles and requests of own ones
+    int wg = 0, cg = 0, units = 0, wb = 0, with_keys = 0, g = g_first, most = 0, least = INT32_MAX;
     bool odd = !grouped;
     for (int x = g0; x < g1; ++x) {
         if (tiles[x] == 0) continue;
-        wg += weight(x);
-        units += weight(x) / tiles[x];
-        twos += cu[x + 1] - cu[x] > p.gr.nb ? weight(x) : 0;
+        units += units_of(x);
+        const int kind = 2 * tiles[x] + (cu[x + 1] - cu[x] > p.gr.nb ? 1 : 0);
+        most = max(most, kind);
+        least = min(least, kind);
+        wg += units_of(x) * tiles[x];
+        cg += units_of(x) * cost_of(x).of(tiles[x]);
     }
     for (int b = b0; b < b1; ++b) {
         const int n = length(b), t = own_tiles(b, g);
@@ -607,87 +608,115 @@ __device__ __forceinline__ void make_plan(const PrefixParams& p, int* scratch, i
         wb += t;
         with_keys += t > 0 ? 1 : 0;
     }
-    const int ig = warp_scan_inc(wg), ib = warp_scan_inc(wb);
+    const int ig = warp_scan_inc(wg), ic = warp_scan_inc(cg), ib = warp_scan_inc(wb), ik = warp_scan_inc(with_keys);
     units = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(units)));
-    twos = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(twos)));
-    with_keys = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(with_keys)));
+    most = __reduce_max_sync(0xffffffffu, most);
+    least = __reduce_min_sync(0xffffffffu, least);
     if (lane == 31) {
-        sums[warp] = make_int4(ig, ib, units, twos);
-        sums2[warp] = make_int2(with_keys, 0);
+        sums[warp] = make_int4(ig, ic, ib, ik);
+        sums2[warp] = make_int4(units, most, least, 0);
     }
     if (tid == 0) start_sh[0] = start_sh[1] = Start{};
     __syncthreads();
-    int at_g = ig - wg, at_b = ib - wb, total = 0;
-    units = twos = with_keys = 0;
-    out.common.T = 0;
+    int at_g = ig - wg, at_c = ic - cg, at_b = ib - wb, at_k = ik - with_keys, shared = 0, total = 0;
+    units = with_keys = 0;
     for (int w = 0; w < kPrefixThreads / 32; ++w) {
         const int4 v = sums[w];
         at_g += w < warp ? v.x : 0;
-        at_b += w < warp ? v.y : 0;
-        out.common.T += v.x;
-        total += v.y;
-        units += v.z;
-        twos += v.w;
-        with_keys += sums2[w].x;
+        at_c += w < warp ? v.y : 0;
+        at_b += w < warp ? v.z : 0;
+        at_k += w < warp ? v.w : 0;
+        shared += v.x;
+        out.common.T = w == 0 ? v.y : out.common.T + v.y;
+        total += v.z;
+        with_keys += v.w;
+        const int4 u = sums2[w];
+        units += u.x;
+        most = max(most, u.y);
+        least = min(least, u.z);
     }
-    out.own.T = total * p.rest_units;
-    // the CTAs of common keys
-    using K = Cost<D>;
-    const long long cost = static_cast<long long>(K::kOne) * (out.common.T - twos) + static_cast<long long>(K::kTwo) * twos,
-                    other = static_cast<long long>(p.rest_units) * (static_cast<long long>(K::own(p.R > 8)) * total + static_cast<long long>(K::unit(p.R > 8)) * with_keys);
-    // (in pairs of CTAs, see prefix_kernel)
+    out.own.T = p.rest_units * (own.start * with_keys + own.tile * total);
+    // the CTAs of common keys, in pairs (see prefix_kernel)
     out.border = out.common.P = 0;
-    if (out.common.T > 0) {
-        const int pairs = ctas / 2;
-        const int share = other > 0 ? min(max(static_cast<int>(common_share<D>(static_cast<float>(ctas), static_cast<float>(cost), static_cast<float>(other)) * 0.5f + 0.5f), 1), pairs - 1) : pairs;
-        out.common.P = paged_ctas(out.common.T, units, 2 * share);
-        out.border = (out.common.P + 1) & ~1;
+    bool even = false;
+    if (shared > 0) {
+        using K = Cost<D>;
+        const int room = total > 0 ? (ctas & ~1) - 2 : ctas;
+        const float n = static_cast<float>(ctas), scale = p.weigh ? 1.f : static_cast<float>(K::own(p.R > 8).tile),
+                    C = scale * static_cast<float>(out.common.T), O = scale * static_cast<float>(out.own.T);
+        float x = n;
+        if (total > 0) {
+            // both kinds end at the same time, and common keys not before memory has given all
+            x = common_share(n, C, O, K::start(most & 1));
+            x = fminf(x, C / fmaxf(K::kRead * (static_cast<float>(shared) + static_cast<float>(total) * static_cast<float>(p.rest_units)) - K::kFirst, 1.f));
+        }
+        const int fewest = cost_of_kind(most).least;   // tiles that a CTA may have
+        x = fminf(x, static_cast<float>(max(shared / fewest, units)));
+        int P = min(max(2 * static_cast<int>(x * 0.5f + 0.5f), 2), room);
+        // units that are all the same: as many CTAs for each, if what that moves x by costs less than units cut across
+        if (most == least && p.weigh) {
+            const int k = min(min(static_cast<int>(x / static_cast<float>(units) + 0.5f), room / units), max((most >> 1) / fewest, 1));
+            const float off = fabsf(static_cast<float>(k * units) - x), y = fmaxf(n - x, 1.f);
+            even = k > 0 && off * fmaxf(C / (x * x), O / (y * y)) < static_cast<float>(cost_of_kind(most).start);
+            if (even) P = k * units;
+        }
+        out.common.P = P;
+        out.border = (P + 1) & ~1;
+        if (even) {
+            one.tile = two.tile = 1;
+            one.start = two.start = 0;
+            out.common.T = shared;
+            at_c = at_g;
+        }
     }
-    out.own.P = paged_ctas(out.own.T, with_keys * p.rest_units, max(ctas - out.border, 1));
+    out.own.P = paged_ctas(total * p.rest_units, with_keys * p.rest_units, max(ctas - out.border, 1));
     // whoever has the entry that one of the CTA's two cuts falls in says so
     const bool common = cta < out.border;
     const Line& line = common ? out.common : out.own;
     const int c = common ? cta : cta - out.border;
     const bool works = c < line.P && line.T > 0;
     const int cut[2] = {works ? line.cut(c) : 0, works ? line.cut(c + 1) : 0};
-    const auto owns = [&](int e, int s0, int nt, int n) {   // entry e: n units of nt tiles from s0 on
+    const auto owns = [&](int e, int at, int tile0, UnitCost u, int nt, int n) {   // entry e: n units of nt tiles from tile0 on, at `at` of the line
+        const int of = u.of(nt);
 #pragma unroll
         for (int k = 0; k < 2; ++k)
-            if (works && s0 <= cut[k] && cut[k] < s0 + nt * n) {
+            if (works && at <= cut[k] && cut[k] < at + of * n) {
                 Start r;
-                const int i = (cut[k] - s0) / nt, s = s0 + i * nt, x = unit_cut(cut[k], s, s + nt);
-                r.g = x;
+                const int i = (cut[k] - at) / of, x = tile_at(cut[k] - at - i * of, nt, u);
+                r.g = tile0 + i * nt + x;
                 r.b = e;
-                r.i = x == s + nt ? i + 1 : i;
-                r.t0 = x == s + nt ? 0 : x - s;
+                r.i = x == nt ? i + 1 : i;
+                r.t0 = x == nt ? 0 : x;
                 start_sh[k] = r;
             }
     };
     for (int x = g0; x < g1; ++x) {
-        place[x] = at_g;
+        place[x] = at_c;
         if (tiles[x] == 0) continue;
-        if (common) owns(x, at_g, tiles[x], weight(x) / tiles[x]);
-        at_g += weight(x);
+        if (common) owns(x, at_c, at_g, cost_of(x), tiles[x], units_of(x));
+        at_g += units_of(x) * tiles[x];
+        at_c += units_of(x) * cost_of(x).of(tiles[x]);
     }
     __syncthreads();   // the groups' places; and the keys' sums have been read
     g = g_first;
     for (int b = b0; b < b1; ++b) {
-        const int t = own_tiles(b, g);
-        if (!common) owns(b, at_b * p.rest_units, t, p.rest_units);
-        if (pre) pre[b] = at_b;
-        const bool mine = b % ctas == cta;   // for the merge
-        if (mine || !pre) p.rest_prefix[b] = at_b;   // without shared memory every CTA writes it, the same, and reads its own
-        if (mine) p.plan[1 + b] = grouped ? make_int4(place[g], tiles[g], cu[g + 1] - cu[g], cu[g]) : make_int4(0, 0, 1, b);
+        const int t = own_tiles(b, g), at = p.rest_units * (own.start * at_k + own.tile * at_b);
+        if (!common && t > 0) owns(b, at, at_b * p.rest_units, own, t, p.rest_units);
+        if (pre)
+            pre[b] = at_b;
+        else
+            p.rest_prefix[b] = at_b;   // without shared memory every CTA writes it, the same, and reads its own
+        if (b % ctas == cta) {   // for the merge
+            p.plan[1 + b] = grouped ? make_int4(place[g], tiles[g], cu[g + 1] - cu[g], cu[g]) : make_int4(0, 0, 1, b);
+            p.own[b] = make_int2(at, t);
+        }
         at_b += t;
+        at_k += t > 0 ? 1 : 0;
     }
     if (tid == 0) {
-        if (pre) pre[B] = total;
-        if (cta == 0 || !pre) {
-            p.rest_prefix[B] = total;
-            p.rest_prefix[B + 1] = out.own.P;
-        }
-        if (cta == 0) p.plan[0] = make_int4(out.common.T, out.common.P, 0, 0);
-        if (works && c + 1 == line.P) start_sh[1].g = line.T;   // the cut behind the last tile
+        (pre ? pre : p.rest_prefix)[B] = total;
+        if (cta == 0) p.plan[0] = make_int4(out.common.T, out.common.P | (even || !p.weigh ? kByTiles : 0), out.own.T, out.own.P);
+        if (works && c + 1 == line.P) start_sh[1].g = common ? shared : total * p.rest_units;   // the cut behind the last tile
     }
     if (cta == 0 && odd) report_bad_page(p.status);
     fence_proxy_async_smem();   // what was written here before key tiles land in it
@@ -711,8 +740,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrefixThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ PrefixShared<D> sh;
-    __shared__ int4 sums[kPrefixThreads / 32], start_raw[2];
-    __shared__ int2 sums2[kPrefixThreads / 32];
+    __shared__ int4 sums[kPrefixThreads / 32], sums2[kPrefixThreads / 32], start_raw[2];
     __shared__ uint32_t tmem_slot;
     Own& own = *reinterpret_cast<Own*>(smem + kOffOwn);
     griddep_launch_dependents();
@@ -731,7 +759,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrefixThreads, 1)
     if (cta < plan.border) {
         prefix_body<D>(qtiles, kmap, vmap, p, sh, smem, cta, plan.first, plan.end, tmem_slot);
     } else {
-        const RestPlan rest{fits ? own.pre_sh : p.rest_prefix, fits ? own.keys_sh : nullptr, plan.own, plan.first, plan.end, tmem_slot};
+        const RestPlan rest{fits ? own.pre_sh : p.rest_prefix, fits ? own.keys_sh : nullptr, plan.first, plan.end, tmem_slot};
         decode_body<D, CAUSAL, NC, true, true>(qunits, kmap, vmap, dp, own, smem, cta - plan.border, static_cast<int>(gridDim.x) - plan.border, rest);
     }
     tc_fence_before();

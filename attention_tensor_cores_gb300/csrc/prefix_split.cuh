@@ -1,0 +1,49 @@
+// How the key tiles of fmha_fwd_prefix are cut for its CTAs, and which pieces of a row's keys that makes: the attention kernel and
+// the merge find out the same.
+#pragma once
+#include "paged_run.cuh"
+#include "prefix.h"
+
+namespace atc_gb300 {
+namespace {
+
+// What a unit costs: a key tile of it, and that there is one more (its queries, its first tile, its partials).  A cut leaves
+// `least` tiles on either side, or the unit whole.
+struct UnitCost {
+    int tile = 1, start = 0, least = kMinPiece;
+    __host__ __device__ int of(int nt) const { return start + nt * tile; }
+};
+
+// In 0.05 us, where memory does not bound it: least squares over the CTAs' times in 13 problems of Hq32 Hkv8 D128 and Hq16 Hkv4 D64
+// (of D = 128 and D = 64).  The lines of units are cut where the costs are equal; by tiles alone the CTAs with the end of one unit
+// and the beginning of the next were the last by 7 us.
+template <int D>
+struct Cost {
+    __host__ __device__ static UnitCost common(bool two)   // a row tile of each side, or one for both
+    {
+        return two ? UnitCost{D == 128 ? 42 : 37, D == 128 ? 105 : 50, 2} : UnitCost{D == 128 ? 22 : 16, D == 128 ? 80 : 40, 3};
+    }
+    __host__ __device__ static UnitCost own(bool many)     // more than 8 rows, which 16 columns hold
+    {
+        return {D == 128 ? (many ? 13 : 11) : (many ? 12 : 9), many ? 42 : 11, kMinPiece};
+    }
+    // what CTAs of common keys take more than those of own keys, whatever their part
+    static constexpr float start(bool two) { return D == 128 ? (two ? 120.f : 80.f) : (two ? 60.f : 40.f); }
+    static constexpr float kRead = D == 128 ? 0.18f : 0.09f;    // a tile from memory, with all SMs
+    static constexpr float kFirst = D == 128 ? 240.f : 180.f;   // from the beginning of the reads to a CTA's common keys, and from these to its end
+};
+constexpr int kByTiles = 1 << 16;   // in the plan, beside the CTAs of a line that counts tiles
+// With more tiles the sums of costs would pass 31 bits; each tile counts as one then
+constexpr long long kMaxWeighed = 1 << 23;
+
+// The cut at x, from the unit's place on: the first tile behind it of nt (0 or nt when it is not inside)
+__device__ __forceinline__ int tile_at(int x, int nt, UnitCost u)
+{
+    if (x <= u.start) return 0;
+    const int t = static_cast<int>(static_cast<unsigned>(x - u.start) / static_cast<unsigned>(u.tile));
+    if (t >= nt) return nt;
+    return 2 * t <= nt ? (t < u.least ? 0 : t) : (nt - t < u.least ? nt : t);
+}
+
+}  // namespace
+}  // namespace atc_gb300
