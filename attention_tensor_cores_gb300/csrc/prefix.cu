@@ -29,7 +29,7 @@ struct MergeParams {
 // round trips to L2 and one for each four partials more; where there are few rows, up to eight warps share theirs (16 requests
 // of Hq32 Hkv8 D128 behind 8192 common keys: 29.6 us a call, 33.7 with a warp per row).
 template <int D>
-__global__ void __launch_bounds__(256, 5) prefix_merge_kernel(const __grid_constant__ MergeParams p)
+__global__ void __launch_bounds__(256, 4) prefix_merge_kernel(const __grid_constant__ MergeParams p)
 {
     constexpr int V = D / 32;   // features of a lane
     griddep_launch_dependents();
@@ -40,17 +40,18 @@ __global__ void __launch_bounds__(256, 5) prefix_merge_kernel(const __grid_const
     const int unit = row / p.R, rr = row - unit * p.R, b = unit / p.Hkv, h = unit - b * p.Hkv, B = p.rows / (p.R * p.Hkv);
     const int4 head = p.plan[0], g = p.plan[1 + b];   // g: place, tiles, requests and first one of the group
     const int2 o = p.own[b];
-    // the CTAs [c, c + n) of a line have pieces of its unit of nt tiles at place s
-    const auto find = [](const Line& line, int s, int nt, UnitCost u, int& c, int& n) {
-        const float per = static_cast<float>(line.P) / static_cast<float>(line.T);
-        const auto at = [&](int i) { return tile_at(line.cut(i) - s, nt, u); };
-        c = max(min(static_cast<int>(static_cast<float>(s) * per), line.P - 1), 0);
-        while (c > 0 && at(c) > 0) --c;
-        while (at(c + 1) <= 0) ++c;
-        int d = max(min(static_cast<int>(static_cast<float>(s + u.of(nt)) * per), line.P), c + 1);
-        while (d < line.P && at(d) < nt) ++d;
-        while (d > c + 1 && at(d - 1) >= nt) --d;
-        n = d - c;
+    // the CTAs [c, c + n) of a line have pieces of its unit of nt tiles at place s; a lane looks at a cut
+    const auto find = [&](const Line& line, int s, int nt, UnitCost u, int& c, int& n) {
+        const int at_s = static_cast<int>(static_cast<float>(s) * (static_cast<float>(line.P) / static_cast<float>(line.T)));
+        for (int i = max(min(at_s, line.P) - 1, 0);; i += 32) {   // a cut that is not behind s, although the quotient is rounded
+            const int t = tile_at(line.cut(min(i + lane, line.P)) - s, nt, u);
+            const unsigned before = __ballot_sync(0xffffffffu, t <= 0), behind = __ballot_sync(0xffffffffu, t >= nt);
+            if (before) c = i + 31 - __clz(before);
+            if (behind) {
+                n = i + __ffs(behind) - 1 - c;
+                return;
+            }
+        }
     };
     // partial i of n1 + n2: first those of the group's common keys (of a pair of row tiles with one tile two a piece, `second` rows
     // apart), then the request's own
@@ -77,6 +78,15 @@ __global__ void __launch_bounds__(256, 5) prefix_merge_kernel(const __grid_const
         first2 = static_cast<long long>(b * units + i) * kN + rr - chunk * p.G;
     }
     if (p.out && n1 == 0 && n2 == 1) return;   // one piece was all of it and wrote the row (for all warps of the row)
+    const auto load = [](float (&x)[V], const float* from) {
+        if constexpr (V == 4) {
+            const float4 y = __ldcg(reinterpret_cast<const float4*>(from));
+            x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w;
+        } else {
+            const float2 y = __ldcg(reinterpret_cast<const float2*>(from));
+            x[0] = y.x, x[1] = y.y;
+        }
+    };
     float m = -INFINITY, l = 0.f, acc[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.f;
@@ -94,6 +104,17 @@ __global__ void __launch_bounds__(256, 5) prefix_merge_kernel(const __grid_const
         }
         const float x = lane < n ? __ldcg(lse + at) : -INFINITY;
         src += at * D;
+        // the first rows are on their way before it is known what they weigh
+        constexpr int kAhead = 8;
+        const auto row_of = [&](int k) {
+            return reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), k)) + lane * V;
+        };
+        float v[kAhead][V];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const float* from = row_of(k);
+            if (k < n) load(v[k], from);
+        }
         const float top = fmax_nan(m, redux_max_nan(x));
         if (top == -INFINITY) continue;   // no visible key so far
         const float keep = m == -INFINITY ? 0.f : __expf(m - top), w = lane < n ? __expf(x - top) : 0.f;
@@ -101,21 +122,20 @@ __global__ void __launch_bounds__(256, 5) prefix_merge_kernel(const __grid_const
         l = l * keep + warp_sum(w);
 #pragma unroll
         for (int v = 0; v < V; ++v) acc[v] *= keep;
-#pragma unroll 4
-        for (int k = 0; k < n; ++k) {
-            const float* from = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), k)) + lane * V;
+        const auto add = [&](const float (&x)[V], float wk) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] = fmaf(wk, x[i], acc[i]);
+        };
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
             const float wk = __shfl_sync(0xffffffffu, w, k);
-            if constexpr (V == 4) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(from));
-                acc[0] = fmaf(wk, v.x, acc[0]);
-                acc[1] = fmaf(wk, v.y, acc[1]);
-                acc[2] = fmaf(wk, v.z, acc[2]);
-                acc[3] = fmaf(wk, v.w, acc[3]);
-            } else {
-                const float2 v = __ldcg(reinterpret_cast<const float2*>(from));
-                acc[0] = fmaf(wk, v.x, acc[0]);
-                acc[1] = fmaf(wk, v.y, acc[1]);
-            }
+            if (k < n) add(v[k], wk);
+        }
+#pragma unroll 8
+        for (int k = kAhead; k < n; ++k) {
+            float x[V];
+            load(x, row_of(k));
+            add(x, __shfl_sync(0xffffffffu, w, k));
         }
     }
     if (p.shares > 1) {
