@@ -324,7 +324,7 @@ extern "C" int fmha_fwd_prefix(const void* q, const fmha_kv_cache* cache, const 
     p.Hkv = cache->Hkv;
     p.R = Hq / cache->Hkv * Sq;
     p.Sq = Sq;
-    p.gr = Groups{cu_groups, prefix_lens, N, kRows / p.R};
+    p.gr = Groups{cu_groups, prefix_lens, N, kRows / p.R, p.R, shape.chunks};
     p.causal = o.causal && Sq > 1;   // one query sees every key either way
     p.c = scale * kLog2e;
     p.seqlens = seqlens;

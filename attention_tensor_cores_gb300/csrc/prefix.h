@@ -14,6 +14,7 @@ struct Groups {
     const int32_t* prefix = nullptr;   // [n] tokens in the same pages
     int n = 0;
     int nb = 0;                        // requests in a row tile
+    int R = 0, chunks = 0;             // of a request and key/value head: rows, and units of at most 16 of them
 };
 
 struct PrefixParams {

@@ -45,18 +45,18 @@ static_assert(kPrefixThreads == decode_threads<true>(), "common and own keys in 
 constexpr uint32_t kRegsSide = 208;
 static_assert(128 * (2 * kRegsSide + kRegsCtl) <= kPrefixThreads * 168, "register split exceeds the launch allocation");
 
-// A group's keys are shared when that spares at least so many tiles of one key/value head: its rows' partials cost
-// about as much.
-constexpr int kMinShared = 4;
-
 // Tiles of keys that the requests [b0, b1) of a group read together.  n0: keys of the first one, through whose row
-// they are read.
+// they are read.  None, unless what each request would take for them is more than what they take together and in the merge.
+template <int D>
 __device__ __forceinline__ int shared_tiles(const Groups& gr, int b0, int b1, int prefix, int n0)
 {
+    using K = Cost<D>;
     const int members = b1 - b0;
     if (members < 2) return 0;
-    const int tiles = min(max(prefix, 0), n0) / kTileKV, row_tiles = (members + gr.nb - 1) / gr.nb;
-    return static_cast<long long>(members - row_tiles) * tiles < kMinShared ? 0 : tiles;
+    const int tiles = min(max(prefix, 0), n0) / kTileKV;
+    const long long alone = static_cast<long long>(members) * gr.chunks * tiles * K::kAgain,
+                    together = static_cast<long long>(row_pairs(members, gr.nb)) * K::common(members > gr.nb).of(tiles) + static_cast<long long>(members) * gr.R * K::kMerge;
+    return alone > together ? tiles : 0;
 }
 
 // last g < n with start[g] <= x (start non-decreasing, start[0] <= x)
@@ -72,7 +72,7 @@ __device__ __forceinline__ int group_of(const int* start, int n, int x)
 
 // The groups' first requests and shared tiles into shared memory (2 n + 1 ints), by the whole block.  keys(b): request b's
 // keys.  Returns whether cu is a list of groups of B requests; if not, nothing is shared.
-template <typename Keys>
+template <int D, typename Keys>
 __device__ __forceinline__ bool load_groups(const Groups& gr, int B, int* cu, int* tiles, Keys&& keys)
 {
     bool bad = false;
@@ -82,7 +82,7 @@ __device__ __forceinline__ bool load_groups(const Groups& gr, int B, int* cu, in
         bad = bad || cu[g] < 0 || cu[g] > B || (g > 0 ? cu[g] < cu[g - 1] : cu[g] != 0) || (g == gr.n && cu[g] != B);
     const bool grouped = !__syncthreads_or(bad);
     for (int g = threadIdx.x; g < gr.n; g += blockDim.x)
-        tiles[g] = grouped && cu[g + 1] > cu[g] ? shared_tiles(gr, cu[g], cu[g + 1], gr.prefix[g], keys(cu[g])) : 0;
+        tiles[g] = grouped && cu[g + 1] > cu[g] ? shared_tiles<D>(gr, cu[g], cu[g + 1], gr.prefix[g], keys(cu[g])) : 0;
     __syncthreads();
     return grouped;
 }
@@ -267,7 +267,7 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& qmap, const CUten
                 if (g < N) {
                     b0 = p.gr.cu[g];
                     members = p.gr.cu[g + 1] - b0;
-                    if (members > 0) nt = shared_tiles(p.gr, b0, b0 + members, p.gr.prefix[g], keys_of(p, b0));
+                    if (members > 0) nt = shared_tiles<D>(p.gr, b0, b0 + members, p.gr.prefix[g], keys_of(p, b0));
                 }
                 for (int l = 0; l < 32 && go && pos < end; ++l) {
                     const int t = __shfl_sync(0xffffffffu, nt, l), fb = __shfl_sync(0xffffffffu, b0, l), m = __shfl_sync(0xffffffffu, members, l);
@@ -572,7 +572,7 @@ __device__ __forceinline__ void make_plan(const PrefixParams& p, int* scratch, i
     const int per_g = (N + kPrefixThreads - 1) / kPrefixThreads, g0 = min(N, tid * per_g), g1 = min(N, g0 + per_g);
     const int per_b = (B + kPrefixThreads - 1) / kPrefixThreads, b0 = min(B, tid * per_b), b1 = min(B, b0 + per_b);
     const int len0 = b0 < b1 ? p.seqlens[b0] : 0;
-    const bool grouped = load_groups(p.gr, B, cu, tiles, [&](int b) { return keys_of(p, b); });
+    const bool grouped = load_groups<D>(p.gr, B, cu, tiles, [&](int b) { return keys_of(p, b); });
     const UnitCost own = p.weigh ? Cost<D>::own(p.R > 8) : UnitCost{};
     UnitCost one = Cost<D>::common(false), two = Cost<D>::common(true);
     if (!p.weigh) {

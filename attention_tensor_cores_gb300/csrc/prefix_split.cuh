@@ -27,6 +27,10 @@ struct Cost {
     {
         return {D == 128 ? (many ? 13 : 11) : (many ? 12 : 9), many ? 42 : 11, kMinPiece};
     }
+    // A tile that each request reads for itself, from memory or from L2; a row in the merge.  Shared and one by one, us: groups of
+    // requests 64 x 2 behind 500 to 1000 keys 68.9 and 56.6, behind 1000 to 2000 94.3 and 109.3, 256 x 2 behind 300 to 500 152.8 and
+    // 140.7, behind 1000 265.2 and 320.3, 4 x 64 behind 128 63.5 and 52.0 (Hq32 Hkv8 D128); D = 64, 64 x 2 behind 1000 to 2000 72.8 and 65.0.
+    static constexpr int kAgain = D == 128 ? 20 : 12, kMerge = 5;
     // what CTAs of common keys take more than those of own keys, whatever their part
     static constexpr float start(bool two) { return D == 128 ? (two ? 120.f : 80.f) : (two ? 60.f : 40.f); }
     static constexpr float kRead = D == 128 ? 0.18f : 0.09f;    // a tile from memory, with all SMs
