@@ -25,11 +25,12 @@ struct MergeParams {
     unsigned* amax_bits;
 };
 
-// Merges the partials of a row: the pieces of its group's common keys and of its own.  A warp per row takes three dependent
-// round trips to L2 and one for each four partials more; where there are few rows, up to eight warps share theirs (16 requests
-// of Hq32 Hkv8 D128 behind 8192 common keys: 29.6 us a call, 33.7 with a warp per row).
+// Merges the partials of a row: the pieces of its group's common keys and of its own.  Bound by latency: the plan, then LSEs and
+// the first eight partials together, then eight partials at a time.  Where there are few rows, up to eight warps share theirs
+// (16 requests of Hq32 Hkv8 D128 behind 8192 common keys, about 30 partials a row: 26.3 us a call from a graph, 29.4 with a warp
+// per row); twice the warps made 64 requests behind 2048 keys 29.4 us instead of 26.3.
 template <int D>
-__global__ void __launch_bounds__(256, 4) prefix_merge_kernel(const __grid_constant__ MergeParams p)
+__global__ void __launch_bounds__(256, 3) prefix_merge_kernel(const __grid_constant__ MergeParams p)
 {
     constexpr int V = D / 32;   // features of a lane
     griddep_launch_dependents();
@@ -197,9 +198,9 @@ struct PrefixWs {
 
 // With so many key tiles at most, all requests' tables full, every request is read by itself.  The plan, a cold softmax
 // and the merge cost about 20 us; a tile that another request has just brought to L2 costs the paged attention 4 to 5 ns.
-// Hkv8 D128, shared against one by one: 4 requests behind 8192 keys (2240 tiles) 22.6 and 20.5 us, 8 of them (4416) 23.8 and
-// 28.4; 8 groups of 4 behind up to 2000 keys (4608) 27.3 and 20.5, 4 behind 4096 (4480) 30.6 and 28.4; one group of 16 behind 8192
-// (8800) 27.8 and 47.2.
+// Hkv8 D128, shared against one by one: 4 requests behind 8192 keys (2240 tiles) 24.3 and 20.9 us, 8 of them (4416) 25.5 and
+// 28.8; 8 groups of 4 behind up to 2000 keys (4608) 28.1 and 20.7, 4 behind 4096 (4480) 32.5 and 28.2; one group of 16 behind 8192
+// (8800) 26.1 and 47.4.
 constexpr long long kFewTiles = 6000;
 // Requests with more rows are not shared; the paged attention takes them in chunks
 constexpr int kMaxSharedRows = 64;
@@ -261,8 +262,12 @@ int run_prefix(const PrefixParams& p, MergeParams& m, const PagedArgs& a, cudaSt
     if (rc) return rc;
     m.shares = 1;
     while (m.shares < 8 && static_cast<long long>(m.rows) * m.shares * 2 <= 16LL * num_sms()) m.shares *= 2;   // half of the warps that fit
-    const int per = 8 / m.shares;
-    FMHA_CHECK_CUDA(launch_pdl(prefix_merge_kernel<D>, dim3(static_cast<unsigned>((m.rows + per - 1) / per)), dim3(256), 0, st, m));
+    const int per = 8 / m.shares, blocks = (m.rows + per - 1) / per, each = (blocks + num_sms() - 1) / num_sms();
+    // Blocks that start early would fill the SMs whose CTA ends first.  Shared memory that they do not use leaves as many on each SM
+    // as make them reach over all (16 requests behind 8192 keys, calls back to back: 29.3 us without, 26.3 with).
+    constexpr int kSpread = 200 * 1024;
+    FMHA_CHECK_CUDA(set_smem_limit_once(reinterpret_cast<const void*>(prefix_merge_kernel<D>), kSpread));
+    FMHA_CHECK_CUDA(launch_pdl(prefix_merge_kernel<D>, dim3(static_cast<unsigned>(blocks)), dim3(256), static_cast<size_t>(each < 3 ? kSpread / each : 0), st, m));
     count_launch();
     return FMHA_OK;
 }

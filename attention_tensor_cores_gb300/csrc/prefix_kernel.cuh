@@ -727,7 +727,7 @@ __device__ __forceinline__ void make_plan(const PrefixParams& p, int* scratch, i
 
 // Common keys by the first CTAs, own keys by the others.  Clusters of two CTAs, for nothing but their places: the two SMs of a
 // cluster share an instruction cache, and a CTA takes half as long again when its neighbour runs the other kind's code
-// (four groups of 64 requests behind 32768 keys, calls back to back: 393 us where CTAs come to lie as SMs get free, 262 in pairs).
+// (four groups of 64 requests behind 32768 keys, calls back to back: 410 us where CTAs come to lie as SMs get free, 262 in pairs).
 template <int D, bool CAUSAL, int NC>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrefixThreads, 1)
     prefix_kernel(const __grid_constant__ CUtensorMap qtiles, const __grid_constant__ CUtensorMap qunits, const __grid_constant__ CUtensorMap kmap,
