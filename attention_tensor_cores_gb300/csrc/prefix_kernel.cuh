@@ -558,7 +558,7 @@ struct Plan {
 __device__ __forceinline__ float common_share(float n, float common, float own, float d)
 {
     const float h = d * n - common - own;
-    return (h + sqrtf(h * h + 4.f * d * common * n)) / (2.f * d);
+    return __fdividef(h + __fsqrt_rn(h * h + 4.f * d * common * n), 2.f * d);
 }
 
 // By the whole CTA.  scratch: 3 N + 1 ints; pre, keys: B + 1 and B ints of shared memory, or NULL (then the prefix is global)
@@ -618,23 +618,18 @@ __device__ __forceinline__ void make_plan(const PrefixParams& p, int* scratch, i
     }
     if (tid == 0) start_sh[0] = start_sh[1] = Start{};
     __syncthreads();
-    int at_g = ig - wg, at_c = ic - cg, at_b = ib - wb, at_k = ik - with_keys, shared = 0, total = 0;
-    units = with_keys = 0;
-    for (int w = 0; w < kPrefixThreads / 32; ++w) {
-        const int4 v = sums[w];
-        at_g += w < warp ? v.x : 0;
-        at_c += w < warp ? v.y : 0;
-        at_b += w < warp ? v.z : 0;
-        at_k += w < warp ? v.w : 0;
-        shared += v.x;
-        out.common.T = w == 0 ? v.y : out.common.T + v.y;
-        total += v.z;
-        with_keys += v.w;
-        const int4 u = sums2[w];
-        units += u.x;
-        most = max(most, u.y);
-        least = min(least, u.z);
-    }
+    // a lane per warp
+    const bool is_warp = lane < kPrefixThreads / 32, is_before = lane < warp;
+    const int4 v = is_warp ? sums[lane] : make_int4(0, 0, 0, 0), u = is_warp ? sums2[lane] : make_int4(0, 0, INT32_MAX, 0);
+    const auto sum = [](int x) { return static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(x))); };
+    const int shared = sum(v.x), total = sum(v.z);
+    int at_g = ig - wg + sum(is_before ? v.x : 0), at_c = ic - cg + sum(is_before ? v.y : 0), at_b = ib - wb + sum(is_before ? v.z : 0),
+        at_k = ik - with_keys + sum(is_before ? v.w : 0);
+    out.common.T = sum(v.y);
+    with_keys = sum(v.w);
+    units = sum(u.x);
+    most = __reduce_max_sync(0xffffffffu, u.y);
+    least = __reduce_min_sync(0xffffffffu, u.z);
     out.own.T = p.rest_units * (own.start * with_keys + own.tile * total);
     // the CTAs of common keys, in pairs (see prefix_kernel)
     out.border = out.common.P = 0;
@@ -648,16 +643,16 @@ __device__ __forceinline__ void make_plan(const PrefixParams& p, int* scratch, i
         if (total > 0) {
             // both kinds end at the same time, and common keys not before memory has given all
             x = common_share(n, C, O, K::start(most & 1));
-            x = fminf(x, C / fmaxf(K::kRead * (static_cast<float>(shared) + static_cast<float>(total) * static_cast<float>(p.rest_units)) - K::kFirst, 1.f));
+            x = fminf(x, __fdividef(C, fmaxf(K::kRead * (static_cast<float>(shared) + static_cast<float>(total) * static_cast<float>(p.rest_units)) - K::kFirst, 1.f)));
         }
         const int fewest = cost_of_kind(most).least;   // tiles that a CTA may have
         x = fminf(x, static_cast<float>(max(shared / fewest, units)));
         int P = min(max(2 * static_cast<int>(x * 0.5f + 0.5f), 2), room);
         // units that are all the same: as many CTAs for each, if what that moves x by costs less than units cut across
         if (most == least && p.weigh) {
-            const int k = min(min(static_cast<int>(x / static_cast<float>(units) + 0.5f), room / units), max((most >> 1) / fewest, 1));
+            const int k = min(min(static_cast<int>(__fdividef(x, static_cast<float>(units)) + 0.5f), room / units), max((most >> 1) / fewest, 1));
             const float off = fabsf(static_cast<float>(k * units) - x), y = fmaxf(n - x, 1.f);
-            even = k > 0 && off * fmaxf(C / (x * x), O / (y * y)) < static_cast<float>(cost_of_kind(most).start);
+            even = k > 0 && off * fmaxf(__fdividef(C, x * x), __fdividef(O, y * y)) < static_cast<float>(cost_of_kind(most).start);
             if (even) P = k * units;
         }
         out.common.P = P;
@@ -678,15 +673,23 @@ __device__ __forceinline__ void make_plan(const PrefixParams& p, int* scratch, i
     const int cut[2] = {works ? line.cut(c) : 0, works ? line.cut(c + 1) : 0};
     const auto owns = [&](int e, int at, int tile0, UnitCost u, int nt, int n) {   // entry e: n units of nt tiles from tile0 on, at `at` of the line
         const int of = u.of(nt);
+        const bool has[2] = {works && at <= cut[0] && cut[0] < at + of * n, works && at <= cut[1] && cut[1] < at + of * n};
+        if (!has[0] && !has[1]) return;
+        int i[2], x[2];   // of both, so that the divisions run beside one another
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const unsigned off = has[k] ? static_cast<unsigned>(cut[k] - at) : 0u;
+            i[k] = static_cast<int>(off / static_cast<unsigned>(of));
+            x[k] = tile_at(static_cast<int>(off) - i[k] * of, nt, u);
+        }
 #pragma unroll
         for (int k = 0; k < 2; ++k)
-            if (works && at <= cut[k] && cut[k] < at + of * n) {
+            if (has[k]) {
                 Start r;
-                const int i = (cut[k] - at) / of, x = tile_at(cut[k] - at - i * of, nt, u);
-                r.g = tile0 + i * nt + x;
+                r.g = tile0 + i[k] * nt + x[k];
                 r.b = e;
-                r.i = x == nt ? i + 1 : i;
-                r.t0 = x == nt ? 0 : x;
+                r.i = x[k] == nt ? i[k] + 1 : i[k];
+                r.t0 = x[k] == nt ? 0 : x[k];
                 start_sh[k] = r;
             }
     };
