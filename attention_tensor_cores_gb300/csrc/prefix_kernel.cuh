@@ -700,32 +700,37 @@ __device__ __forceinline__ void make_plan(const PrefixParams& p, int* scratch, i
         at_g += units_of(x) * tiles[x];
         at_c += units_of(x) * cost_of(x).of(tiles[x]);
     }
-    __syncthreads();   // the groups' places; and the keys' sums have been read
-    g = g_first;
-    for (int b = b0; b < b1; ++b) {
-        const int t = own_tiles(b, g), at = p.rest_units * (own.start * at_k + own.tile * at_b);
-        if (!common && t > 0) owns(b, at, at_b * p.rest_units, own, t, p.rest_units);
-        if (pre)
-            pre[b] = at_b;
-        else
-            p.rest_prefix[b] = at_b;   // without shared memory every CTA writes it, the same, and reads its own
-        if (b % ctas == cta) {   // for the merge
-            p.plan[1 + b] = grouped ? make_int4(place[g], tiles[g], cu[g + 1] - cu[g], cu[g]) : make_int4(0, 0, 1, b);
-            p.own[b] = make_int2(at, t);
+    // f(b, place of request b on the line, its tiles and those before it, its group)
+    const auto requests = [&](auto&& f) {
+        int g = g_first, tile = at_b, unit = at_k;
+        for (int b = b0; b < b1; ++b) {
+            const int t = own_tiles(b, g);
+            f(b, p.rest_units * (own.start * unit + own.tile * tile), t, tile, g);
+            tile += t;
+            unit += t > 0 ? 1 : 0;
         }
-        at_b += t;
-        at_k += t > 0 ? 1 : 0;
-    }
+    };
+    if (!common || !pre)
+        requests([&](int b, int at, int t, int tile, int) {
+            if (!common && t > 0) owns(b, at, tile * p.rest_units, own, t, p.rest_units);
+            (pre ? pre : p.rest_prefix)[b] = tile;   // without shared memory every CTA writes it, the same, and reads its own
+        });
     if (tid == 0) {
         (pre ? pre : p.rest_prefix)[B] = total;
-        if (cta == 0) p.plan[0] = make_int4(out.common.T, out.common.P | (even || !p.weigh ? kByTiles : 0), out.own.T, out.own.P);
         if (works && c + 1 == line.P) start_sh[1].g = common ? shared : total * p.rest_units;   // the cut behind the last tile
     }
-    if (cta == 0 && odd) report_bad_page(p.status);
-    fence_proxy_async_smem();   // what was written here before key tiles land in it
     __syncthreads();
     out.first = start_sh[0];
     out.end = works ? start_sh[1].g : 0;
+    // for the merge
+    if (tid == 0 && cta == 0) p.plan[0] = make_int4(out.common.T, out.common.P | (even || !p.weigh ? kByTiles : 0), out.own.T, out.own.P);
+    requests([&](int b, int at, int t, int, int g) {
+        if (b % ctas != cta) return;
+        p.plan[1 + b] = grouped ? make_int4(place[g], tiles[g], cu[g + 1] - cu[g], cu[g]) : make_int4(0, 0, 1, b);
+        p.own[b] = make_int2(at, t);
+    });
+    if (cta == 0 && odd) report_bad_page(p.status);
+    fence_proxy_async_smem();   // what was written here before key tiles land in it, behind the body's first barrier
 }
 
 // Common keys by the first CTAs, own keys by the others.  Clusters of two CTAs, for nothing but their places: the two SMs of a
