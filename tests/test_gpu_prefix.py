@@ -322,3 +322,59 @@ def test_sweep(seed):
         lens, prefix = [[5]], [0]
     run(lens, prefix, P=P, Hq=G * Hkv, Hkv=Hkv, Sq=Sq, D=pick(64, 128), layout=pick("hnd", "nhd", "kv"), causal=Sq > 1 and upto(2) > 0,
         kind=pick(F.FMHA_OUT_BF16, F.FMHA_OUT_BF16, F.FMHA_OUT_F32), seed=seed, scale=pick(1.0, 1.0, 3.0))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq, Hkv, Sq, members", [(1, 1, 1, 140), (2, 2, 1, 70), (3, 1, 1, 50), (5, 1, 1, 30), (14, 2, 1, 20), (8, 1, 1, 17), (16, 1, 1, 16),
+                                                  (17, 1, 1, 9), (4, 1, 4, 9), (21, 1, 1, 7), (32, 1, 1, 9), (31, 1, 1, 5), (11, 1, 3, 9), (43, 1, 1, 6),
+                                                  (48, 1, 1, 9), (63, 1, 1, 5), (16, 1, 4, 12), (64, 1, 1, 12)])
+def test_common_keys_are_read_through_the_first_row(Hq, Hkv, Sq, members, D):
+    """With the common entries of the other rows outside the pool: only a call that does share them is right and reports nothing."""
+    prefix = 4096
+    gr = Groups([[prefix + 5 * i + Sq - 1 for i in range(members)], [300, 200]], [prefix, 0], 16, Hkv, D)
+    gr.table[1:members, :prefix // 16] = -1
+    q = torch.randn(members + 2, Hq, Sq, D, generator=torch.Generator().manual_seed(5)).to(torch.bfloat16)
+    out, lse = call(q.cuda(), gr, causal=Sq > 1)
+    assert F.fmha_check_status() == F.FMHA_OK
+    check_attention(out, lse, attention_ref(q, *gr.dense, gr.lens, D ** -0.5, Sq > 1))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("prefixes, members", [([1280] * 6, 9), ([1280, 2560, 640, 3200], 9), ([1280] * 40, 9), ([640, 2560] * 12, 40), ([1280], 64)])
+def test_equal_and_other_groups(prefixes, members, D):
+    """Units of one length, cut into as many pieces each, and of several."""
+    lens = [[p + 3 * i + g % 5 for i in range(members)] for g, p in enumerate(prefixes)]
+    gr = Groups(lens, prefixes, 16, 2, D)
+    for g, p in enumerate(prefixes):
+        gr.table[g * members + 1:(g + 1) * members, :p // 16] = -1
+    q = torch.randn(len(gr.lens), 8, 1, D, generator=torch.Generator().manual_seed(5)).to(torch.bfloat16)
+    out, lse = call(q.cuda(), gr)
+    assert F.fmha_check_status() == F.FMHA_OK
+    check_attention(out, lse, attention_ref(q, *gr.dense, gr.lens, D ** -0.5, False))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_two_graphs_share_a_workspace(D):
+    """Two captured calls of one workspace, replayed in turn on one stream."""
+    grs = [Groups([[2000 + i for i in range(n)], [77]], [1920, 0], 16, 2, D, seed=n) for n in (20, 9)]
+    qs = [torch.randn(len(g.lens), 8, 1, D, generator=torch.Generator().manual_seed(5)).to(torch.bfloat16) for g in grs]
+    caches = [F.make_kv_cache(g.k, g.v) for g in grs]
+    need = max(F.fmha_prefix_workspace_size(*q.shape[:3], c, F.make_opts()) for q, c in zip(qs, caches))
+    opts = F.make_opts(workspace=torch.full((need,), 0xff, dtype=torch.uint8, device="cuda"))
+    dev = [q.cuda() for q in qs]
+    outs = [(torch.zeros_like(q), torch.zeros(q.shape[:3], device="cuda")) for q in dev]
+    graphs = []
+    for q, c, g, (out, lse) in zip(dev, caches, grs, outs):
+        F.fmha_fwd_prefix(q, c, g.table, g.seqlens, g.cu, g.prefix_lens, out, lse, D ** -0.5, opts)
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            F.fmha_fwd_prefix(q, c, g.table, g.seqlens, g.cu, g.prefix_lens, out, lse, D ** -0.5, opts)
+    for _ in range(5):
+        for out, lse in outs:
+            out.zero_(), lse.zero_()
+        for graph in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        assert F.fmha_check_status() == F.FMHA_OK
+        for q, g, (out, lse) in zip(qs, grs, outs):
+            check_attention(out, lse, attention_ref(q, *g.dense, g.lens, D ** -0.5, False))
