@@ -307,6 +307,7 @@ size_t fmha_paged_workspace_size(int B, int Hq, int Sq, const fmha_kv_cache* cac
  *   q, cache, block_table, max_pages, seqlens, out, lse, scale: as in fmha_fwd_paged, and the same results within
  *   rounding.  Where sharing would not pay the call is fmha_fwd_paged's and does not look at the groups: with more than 64
  *   rows per key/value head, (Hq / Hkv) * Sq, or at most 6000 tiles of 128 keys in all heads if every table row were full.
+ *   Of the others a group's keys are read once where that takes less than its requests' own reads, in whole tiles of 128.
  *   opts: out_kind, workspace (always needed: fmha_prefix_workspace_size() bytes), causal and the NVFP4 fields;
  *   num_splits 0 (or above 1); seqlens_k must be NULL.
  * Lengths and pages out of bounds as in fmha_fwd_paged; with cu_groups that is no such list nothing is

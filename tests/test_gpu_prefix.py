@@ -378,3 +378,16 @@ def test_two_graphs_share_a_workspace(D):
         assert F.fmha_check_status() == F.FMHA_OK
         for q, g, (out, lse) in zip(qs, grs, outs):
             check_attention(out, lse, attention_ref(q, *g.dense, g.lens, D ** -0.5, False))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_tables_of_many_tiles(D):
+    """Room for more than 2^23 key tiles: the work is cut by tiles, not by what they cost."""
+    gr = Groups([[2000 + 9 * i for i in range(9)], [1300 + i for i in range(5)], [77, 0]], [1920, 1280, 0], 16, 2, D)
+    gr.table = torch.nn.functional.pad(gr.table, (0, (1 << 23) // 32 * 8 + 8), value=-1)     # 16 requests, 2 heads, 8 entries a tile
+    for first, last, p in ((0, 9, 1920), (9, 14, 1280)):
+        gr.table[first + 1:last, :p // 16] = -1
+    q = torch.randn(16, 8, 1, D, generator=torch.Generator().manual_seed(5)).to(torch.bfloat16)
+    out, lse = call(q.cuda(), gr)
+    assert F.fmha_check_status() == F.FMHA_OK
+    check_attention(out, lse, attention_ref(q, *gr.dense, gr.lens, D ** -0.5, False))
