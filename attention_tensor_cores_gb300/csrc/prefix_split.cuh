@@ -17,6 +17,9 @@ struct UnitCost {
 // In 0.05 us, where memory does not bound it: least squares over the CTAs' times in 13 problems of Hq32 Hkv8 D128 and Hq16 Hkv4 D64
 // (of D = 128 and D = 64).  The lines of units are cut where the costs are equal; by tiles alone the CTAs with the end of one unit
 // and the beginning of the next were the last by 7 us.
+// The least pieces, us a call from a graph (Hq32 Hkv8 D128): own keys of few rows of 4 tiles at least instead of 1, 64 requests behind
+// 8192 keys 45.1 for 43.2; common ones of two row tiles of 1 or 3 instead of 2, 64 behind 2048 27.8 and 28.3 for 25.0; of one
+// row tile of 2 instead of 3, 32 behind 4096 25.7 for 25.2, of 4, Hq16 Hkv4 Sq4 D64 16 groups of 4 behind up to 5001 36.5 for 34.2.
 template <int D>
 struct Cost {
     __host__ __device__ static UnitCost common(bool two)   // a row tile of each side, or one for both
@@ -25,7 +28,7 @@ struct Cost {
     }
     __host__ __device__ static UnitCost own(bool many)     // more than 8 rows, which 16 columns hold
     {
-        return {D == 128 ? (many ? 13 : 11) : (many ? 12 : 9), many ? 42 : 11, kMinPiece};
+        return {D == 128 ? (many ? 13 : 11) : (many ? 12 : 9), many ? 42 : 11, many ? kMinPiece : 1};
     }
     // A tile that each request reads for itself, from memory or from L2; a row in the merge.  Shared and one by one, us: groups of
     // requests 64 x 2 behind 500 to 1000 keys 68.9 and 56.6, behind 1000 to 2000 94.3 and 109.3, 256 x 2 behind 300 to 500 152.8 and
