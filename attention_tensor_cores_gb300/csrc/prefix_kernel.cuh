@@ -24,6 +24,10 @@
 //  * P goes to the tensor core as two BF16, the rounded weight (half a step, 2^-9) and what the rounding left, both over the
 //    S that they come from (16 keys' scores become 8 columns of pairs of either), in an MMA each: P is good to 2^-17
 //    as in fmha_fwd_paged, and the output's rounding is the only one that shows.
+//  * Long pieces.  The tensor core cuts off what its sums have no bits for: C products added up (an MMA each, 16 a tile) may lose
+//    C 2^-23 of sum p |v|, always towards zero (values of 1, 1024 tiles: 3.7e-4).  So a side's accumulator takes at most kChain
+//    tiles, 2^-13 of it, and what follows of a piece is merged with its partials by the threads that stored them (a part more
+//    costs 3 to 7 us: 4 groups of 64 behind 32768 keys, in pieces of 85 tiles, 275 us a call for 268).
 //  * Roles: warps 0-3 and 4-7 the sides, 8 K, 9 Q and V, 10 MMA (a warp for each side's products measured slower: 1.58 us a
 //    tile of 128 rows and keys against 1.32), 11 finds the pieces and hands them to the others through a ring in shared
 //    memory.  Every wait is bounded, as in decode_kernel.cuh.
@@ -40,6 +44,7 @@ namespace {
 constexpr int kItems = 4;           // slots of the item ring
 constexpr int kItemReaders = 11;    // K, V and MMA warps, eight softmax warps
 constexpr int kPrefixThreads = 384;
+constexpr int kChain = 64;          // key tiles that an accumulator takes: 1024 MMAs
 static_assert(kPrefixThreads == decode_threads<true>(), "common and own keys in one launch");
 // registers: two softmax warpgroups and the control warpgroup, 2 * 208 + 88 = 504 of an SM quarter's 512
 constexpr uint32_t kRegsSide = 208;
@@ -124,12 +129,13 @@ __device__ __forceinline__ int warp_scan_inc(int v)
     return v;
 }
 
-// A piece of a problem
+// A piece of a problem, or a part of a long one
 struct PrefixItem {
     int t0, t1;      // tiles of keys (none: no more pieces)
     int trow, head;  // row of the block table: the group's first request
     int b0, rows;    // first request of the first row tile, and rows of both
     int prow;        // first row of the partials
+    bool again;      // which hold the piece's earlier tiles
 };
 
 template <int D>
@@ -283,13 +289,22 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& qmap, const CUten
                             it.b0 = fb + r * 2 * p.gr.nb;
                             it.rows = min(2 * p.gr.nb, m - r * 2 * p.gr.nb) * p.R;
                             it.prow = 2 * (fb * p.Hkv + head * m + r * 2 * p.gr.nb) * p.R + cta * 2 * kRows;
+                            it.again = false;
                             pos += it.t1 - it.t0;
                             t0 = 0;
                             if (++r == pairs) {
                                 r = 0;
                                 ++head;
                             }
-                            go = emit(it);
+                            // in parts of one length, if it is long (of one row tile the sides take every other key tile)
+                            const int last = it.t1, n = last - it.t0, most = it.rows > tile_rows ? kChain : 2 * kChain, parts = (n + most - 1) / most;
+                            const int each = (n + parts - 1) / parts;
+                            do {
+                                it.t1 = min(last, it.t0 + each);
+                                go = emit(it);
+                                it.t0 = it.t1;
+                                it.again = true;
+                            } while (go && it.t0 < last);
                         }
                     }
                     i = 0;
@@ -404,7 +419,7 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& qmap, const CUten
         // Ahead of the first piece the code below runs once on what happens to be in O's columns, so that it is in the
         // instruction cache by the time the first scores are: cold, a tile takes 5600 cycles instead of 1700
         for (bool cold = true;; cold = false) {
-            PrefixItem it{0, 0, 0, 0, 0, 2 * kRows, 0};
+            PrefixItem it{0, 0, 0, 0, 0, 2 * kRows, 0, false};
             if (!cold) {
                 if (!__all_sync(0xffffffffu, mbar_wait(&item_full[ir.idx], ir.phase, wc))) break;
                 it = items[ir.idx];
@@ -513,9 +528,20 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& qmap, const CUten
             }
             if (busy) {
                 const bool none = l == 0.f;   // no visible key; a NaN score makes the sum, the row and its LSE NaN
-                const float inv = none ? 0.f : 1.f / l;
+                float inv = none ? 0.f : 1.f / l, lse = none ? -INFINITY : (m + __log2f(l)) * kLn2;
                 const bool store = tid < rows && !aborted(wc);
                 const size_t row = static_cast<size_t>(it.prow) + (side ? (two ? tile_rows : it.rows) : 0) + tid;
+                const bool merge = it.again && store;
+                float keep = 0.f;   // the weight of the partials that are there
+                if (merge) {
+                    const float before = ld_global(p.part_lse + row), top = fmax_nan(before, lse);
+                    if (top != -INFINITY) {
+                        const float wb = __expf(before - top), w = __expf(lse - top), sum = wb + w;
+                        keep = wb / sum;
+                        inv *= w / sum;
+                        lse = top + __logf(sum);
+                    }
+                }
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     uint32_t o[32];
@@ -526,11 +552,19 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& qmap, const CUten
                     float x[32];
 #pragma unroll
                     for (int i = 0; i < 32; ++i) x[i] = none || !any ? 0.f : __uint_as_float(o[i]) * inv;
+                    if (merge)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float y[8];
+                            ld_global_v8(y, p.part_o + row * D + c + 8 * i);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) x[8 * i + k] = fmaf(keep, y[k], x[8 * i + k]);
+                        }
                     if (store)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) st_global_v8(p.part_o + row * D + c + 8 * i, x + 8 * i);
                 }
-                if (store) p.part_lse[row] = none ? -INFINITY : (m + __log2f(l)) * kLn2;
+                if (store) p.part_lse[row] = lse;
             }
             if (any) {
                 tc_fence_before();
