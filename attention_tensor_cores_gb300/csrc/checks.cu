@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kQkThreads) qk_gemm_kernel(const __grid_consta
     for (int col = 0; col < 128; col += 16) {
         uint32_t r[16];
         tmem_ld16(tmem_addr(tmem, warp * 32, col), r);
-        tmem_ld_wait();
+        tmem_ld_wait(r);
         if (row < Sq && !aborted(wc)) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -127,12 +127,12 @@ __global__ void __launch_bounds__(128) tmem_roundtrip_kernel(uint32_t* out)
     tmem_st_wait();
     uint32_t r[32];
     tmem_ld32(tmem_addr(tmem, warp * 32, 0), r);
-    tmem_ld_wait();
+    tmem_ld_wait(r);
     for (int i = 0; i < 32; ++i) out[lane * 64 + i] = r[i];
     uint32_t r2[16];
     for (int chunk = 2; chunk < 4; ++chunk) {
         tmem_ld16(tmem_addr(tmem, warp * 32, chunk * 16), r2);
-        tmem_ld_wait();
+        tmem_ld_wait(r2);
         for (int i = 0; i < 16; ++i) out[lane * 64 + chunk * 16 + i] = r2[i];
     }
     tc_fence_before();
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(128) pv_swapab_kernel(const __grid_constant__ 
     tc_fence_after();
     uint32_t r[16];
     tmem_ld16(tmem_addr(tmem, warp * 32, 0), r);
-    tmem_ld_wait();
+    tmem_ld_wait(r);
     const int lane = threadIdx.x;
     for (int i = 0; i < 16; ++i) out[lane * 16 + i] = __uint_as_float(r[i]);
     tc_fence_before();
@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(128) pv_ts_kernel(const __grid_constant__ CUte
     for (int col = 0; col < D; col += 16) {
         uint32_t r[16];
         tmem_ld16(tmem_addr(tmem, warp * 32, col), r);
-        tmem_ld_wait();
+        tmem_ld_wait(r);
         for (int i = 0; i < 16; ++i) out[q * D + col + i] = __uint_as_float(r[i]);
     }
     tc_fence_before();
@@ -407,7 +407,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128)
     for (int c = 0; c < N; c += 32) {
         uint32_t r[32];
         tmem_ld32p(tmem_addr(tmem, warp * 32, c), r);
-        tmem_ld_wait();
+        tmem_ld_wait(r);
         float* o = out + (static_cast<size_t>(rank) * 128 + threadIdx.x) * N + c;
 #pragma unroll
         for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(r[i]);

@@ -1324,11 +1324,11 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& qmap, const CUten
             if constexpr (PAGED) {   // and what the roundings of P left (see store_p)
                 uint32_t ow[NC];
                 tmem_ld<NC>(tmem + lane_base + C::o_col(NC, PAGED, orr.idx) + (NC == 16 ? 16 : 8), ow);
-                tmem_ld_wait();
+                tmem_ld_wait(ov, ow);
 #pragma unroll
                 for (int q = 0; q < NC; ++q) ov[q] = __float_as_uint(__uint_as_float(ov[q]) + __uint_as_float(ow[q]));
             } else {
-                tmem_ld_wait();
+                tmem_ld_wait(ov);
             }
             orr.advance();
             if (moved_prev) {
@@ -1394,7 +1394,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& qmap, const CUten
                 tc_fence_after();
                 uint32_t sv[NC];
                 tmem_ld<NC>(tmem + lane_base + sr.idx * 16, sv);
-                tmem_ld_wait();
+                tmem_ld_wait(sv);
                 sr.advance();
 
                 const int kv = t * kTileKV + tid;
@@ -1511,7 +1511,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& qmap, const CUten
             {
                 uint32_t hv[2 * NC];
                 tmem_ld<2 * NC>(tmem + lane_base + 64 + hr.idx * 32, hv);
-                tmem_ld_wait();
+                tmem_ld_wait(hv);
 #pragma unroll
                 for (int q = 0; q < NC; ++q) {
                     acc[q] = __uint_as_float(hv[q]);

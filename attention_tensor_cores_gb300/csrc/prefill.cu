@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(prefill_threads<RING>(), 1)
                 uint32_t* su = reinterpret_cast<uint32_t*>(s);
 #pragma unroll
                 for (int c4 = 0; c4 < kTN / 32; ++c4) tmem_ld32p(tS + c4 * 32, su + c4 * 32);
-                tmem_ld_wait();
+                tmem_ld_wait<kTN>(su);
                 tc_fence_before();
                 mbar_arrive(&s_free[C::kSharedS ? 0 : q]);
                 if ((j + 1) * kTN > lim) {
@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(prefill_threads<RING>(), 1)
                     for (int c4 = 0; c4 < D / 32; ++c4) {
                         uint32_t o[32];
                         tmem_ld32p(tO + c4 * 32, o);
-                        tmem_ld_wait();
+                        tmem_ld_wait(o);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
                         tmem_st32(tO + c4 * 32, o);
@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(prefill_threads<RING>(), 1)
                 uint32_t o[32];
                 if (T > 0) {
                     tmem_ld32p(tO + c4 * 32, o);
-                    tmem_ld_wait();
+                    tmem_ld_wait(o);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) o[i] = 0u;

@@ -453,7 +453,7 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& qmap, const CUten
                     uint32_t* su = reinterpret_cast<uint32_t*>(s);
 #pragma unroll
                     for (int c4 = 0; c4 < kTileKV / 32; ++c4) tmem_ld32p(tS + c4 * 32, su + c4 * 32);
-                    tmem_ld_wait();
+                    tmem_ld_wait<kTileKV>(su);
                     const int see = lim - t * kTileKV;
                     if (see < kTileKV) {
 #pragma unroll
@@ -482,7 +482,7 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& qmap, const CUten
                         for (int c = 0; c < D; c += 16) {
                             uint32_t o[16];
                             tmem_ld16(tO + c, o);
-                            tmem_ld_wait();
+                            tmem_ld_wait(o);
 #pragma unroll
                             for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
                             tmem_st16(tO + c, o);

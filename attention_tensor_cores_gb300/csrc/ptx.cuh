@@ -517,18 +517,34 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32])
         : "r"(taddr));
 }
 
-__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-
-// The same, and what follows needs these registers of an earlier load: none of it is moved ahead of the wait
-__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32])
+// Registers that a load from Tensor Memory fills, behind the wait for it: what uses them stays behind this place, as it would not
+// behind the wait alone.  (Volatile statements keep their order among themselves, others follow their operands.)
+template <int N>
+__device__ __forceinline__ void loaded_registers(uint32_t* r)
 {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-        : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-          "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
-          "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
-          "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
-        :
-        : "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// Waits for this thread's loads from Tensor Memory, into r (and into `second`)
+template <int N>
+__device__ __forceinline__ void tmem_ld_wait(uint32_t* r)
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+    loaded_registers<N>(r);
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[N])
+{
+    tmem_ld_wait<N>(static_cast<uint32_t*>(r));
+}
+
+template <int N, int M>
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[N], uint32_t (&second)[M])
+{
+    tmem_ld_wait(r);
+    loaded_registers<M>(second);
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16])

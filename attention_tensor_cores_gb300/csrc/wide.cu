@@ -528,7 +528,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
                 uint32_t* su = reinterpret_cast<uint32_t*>(s);
 #pragma unroll
                 for (int c4 = 0; c4 < kWKeys / 32; ++c4) tmem_ld32p(tmem + lane_base + kWColS + c4 * 32, su + c4 * 32);
-                tmem_ld_wait();
+                tmem_ld_wait<kWKeys>(su);
                 tc_fence_before();
                 arrive_lead(&s_empty);
                 if ((t + 1) * kWKeys > lim) {
@@ -597,7 +597,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
                     for (int c4 = 0; c4 < kWHalf / 32; ++c4) {
                         uint32_t o[32];
                         tmem_ld32p(tmem + lane_base + kWColO + c4 * 32, o);
-                        tmem_ld_wait();
+                        tmem_ld_wait(o);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
                         tmem_st32(tmem + lane_base + kWColO + c4 * 32, o);
@@ -626,7 +626,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
                 uint32_t o[32];
                 if (T > 0) {   // uniform over the CTA; a unit without keys (whole-unit order) gives O = 0
                     tmem_ld32p(tmem + lane_base + kWColO + c4 * 32, o);
-                    tmem_ld_wait();
+                    tmem_ld_wait(o);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) o[i] = 0u;
