@@ -545,6 +545,7 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& qmap, const CUten
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     uint32_t o[32];
+                    __syncwarp();   // tcgen05.ld is warp-collective, and rows that are none have left others to their partials
                     if (any) {
                         tmem_ld32(tO + c, o);
                         tmem_ld_wait(o);

@@ -98,3 +98,20 @@ def test_nan_in_a_part(where, D):
     assert bad.any() and torch.equal(lse.isnan().cpu(), bad) and torch.equal(out.isnan().all(-1).cpu(), bad)
     fine = ~bad[:, 0, 0]
     check_attention(out.cpu()[fine], lse.cpu()[fine], tuple(x[fine] for x in ref), bf16=False)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_forced_timeout_in_parts(D):
+    """With a wait limit of one cycle the kernel drains and reports, whatever part it is in; the next call is right."""
+    gr, q, ref = many([9] * 170, [200] * 170, D, 16, 1, seed=11, P=128, short=300)
+    assert F.fmha_check_status() == F.FMHA_OK
+    F.fmha_set_wait_limit(1)
+    try:
+        call(q, gr)
+        rc = F.fmha_check_status()
+    finally:
+        F.fmha_set_wait_limit(0)
+    assert rc == F.FMHA_ERR_TIMEOUT
+    out, lse = call(q, gr)
+    assert F.fmha_check_status() == F.FMHA_OK
+    check_attention(out, lse, ref)
