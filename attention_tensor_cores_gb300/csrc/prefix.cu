@@ -38,7 +38,7 @@ __global__ void __launch_bounds__(256, 3) prefix_merge_kernel(const __grid_const
     __shared__ float part[8][D], part_m[8], part_l[8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, share = warp % p.shares, row = (blockIdx.x * 8 + warp) / p.shares;
     if (row >= p.rows) return;   // the last block's, warps of whole rows
-    const int unit = row / p.R, rr = row - unit * p.R, b = unit / p.Hkv, h = unit - b * p.Hkv, B = p.rows / (p.R * p.Hkv);
+    const int unit = row / p.R, rr = row - unit * p.R, b = unit / p.Hkv, h = unit - b * p.Hkv;
     const int4 head = p.plan[0], g = p.plan[1 + b];   // g: place, tiles, requests and first one of the group
     const int2 o = p.own[b];
     // the CTAs [c, c + n) of a line have pieces of its unit of nt tiles at place s; a lane looks at a cut
