@@ -200,7 +200,11 @@ struct PrefixWs {
 // and the merge cost about 20 us; a tile that another request has just brought to L2 costs the paged attention 4 to 5 ns.
 // Hkv8 D128, shared against one by one: 4 requests behind 8192 keys (2240 tiles) 24.3 and 20.9 us, 8 of them (4416) 25.5 and
 // 28.8; 8 groups of 4 behind up to 2000 keys (4608) 28.1 and 20.7, 4 behind 4096 (4480) 32.5 and 28.2; one group of 16 behind 8192
-// (8800) 26.1 and 47.4.
+// (8800) 26.1 and 47.4.  No number of tiles tells these apart: 6000 sends the 8 requests of 4416 tiles the slower way by 3 us, 4400
+// would send the groups of 4 the slower way by 4 to 7.
+// The lengths are on the device, so what counts here is the room in the table.  A wide one takes short requests the longer way:
+// 4 requests of 1000 keys 19.6 us with room for 131072 tokens, 11.9 with a table of their own size; 32 of 300 keys, no
+// two of a group, 16.2 and 9.6.
 constexpr long long kFewTiles = 6000;
 // Requests with more rows are not shared; the paged attention takes them in chunks
 constexpr int kMaxSharedRows = 64;

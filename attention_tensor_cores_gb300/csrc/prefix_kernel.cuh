@@ -25,7 +25,7 @@
 //    S that they come from (16 keys' scores become 8 columns of pairs of either), in an MMA each: P is good to 2^-17
 //    as in fmha_fwd_paged, and the output's rounding is the only one that shows.
 //  * Long pieces.  The tensor core cuts off what its sums have no bits for: C products added up (an MMA each, 16 a tile) may lose
-//    C 2^-23 of sum p |v|, always towards zero (values of 1, 1024 tiles: 3.7e-4).  So a side's accumulator takes at most kChain
+//    C 2^-23 of sum p |v|, always towards zero (values of 1, 1024 tiles: 4e-4).  So a side's accumulator takes at most kChain
 //    tiles, 2^-13 of it, and what follows of a piece is merged with its partials by the threads that stored them (a part more
 //    costs 3 to 7 us: 4 groups of 64 behind 32768 keys, in pieces of 85 tiles, 275 us a call for 268).
 //  * Roles: warps 0-3 and 4-7 the sides, 8 K, 9 Q and V, 10 MMA (a warp for each side's products measured slower: 1.58 us a

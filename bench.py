@@ -35,20 +35,20 @@ FALLBACK_PEAKS = {"hbm_gbs": 6800.0, "bf16_tflops": 1900.0, "bf16_tflops_sustain
 # reported only while those sources are unchanged.
 TRAFFIC = {
     # decode B8 H32 Sq1 Skv4096 D128 (decode_kernel<128, 0, 1, 0>, 128 CTAs of two whole units): read
-    # 537,024,000 + written 3,258,880 bytes (profiles/decode_kernel_decode-B8-H32-Skv4096-D128.md)
-    "decode_kernel<128>": {"bytes": 540282880, "source_sha": "c756621bb7aae1c8"},
+    # 537,026,560 + written 2,821,376 bytes (profiles/decode_kernel_decode-B8-H32-Skv4096-D128.md)
+    "decode_kernel<128>": {"bytes": 539847936, "source_sha": "c14d961dcf543bd9"},
     # ragged GQA decode B64 Hq32 Hkv8 Skv<=32768 D128 (decode_kernel<128, 0, 4, 0>): the quarter-size workload
-    # (B16) read 1,005,862,912 + wrote 3,407,872 bytes for 1,001,226,240 algorithmic K/V bytes (1.008x); scaled
+    # (B16) read 1,005,832,448 + wrote 3,370,240 bytes for 1,001,226,240 algorithmic K/V bytes (1.008x); scaled
     # by the K/V bytes to the full workload's 4,106,002,432 (profiles/side-kernels_ragged-decode-wide-combine-nvfp4.md)
-    "decode_kernel<128>/ragged": {"bytes": 4138992895, "source_sha": "c756621bb7aae1c8"},
-    # speculative decode B8 Hq32 Hkv8 Sq4 Skv8192 D128, causal (decode_kernel<128, 1, 16, 0>): read 268,826,112 +
-    # written 2,999,040 bytes (profiles/decode_kernel_decode-B8-H32-Skv4096-D128.md)
-    "decode_kernel<128>/speculative": {"bytes": 271825152, "source_sha": "c756621bb7aae1c8"},
-    # wide-head B32 Hq128 Hkv1 Skv16384 D512, independent CTAs: read 1,081,723,648 + written 10,591,232
+    "decode_kernel<128>/ragged": {"bytes": 4138713635, "source_sha": "c14d961dcf543bd9"},
+    # speculative decode B8 Hq32 Hkv8 Sq4 Skv8192 D128, causal (decode_kernel<128, 1, 16, 0>): read 268,812,032 +
+    # written 2,853,376 bytes (profiles/decode_kernel_decode-B8-H32-Skv4096-D128.md)
+    "decode_kernel<128>/speculative": {"bytes": 271665408, "source_sha": "c14d961dcf543bd9"},
+    # wide-head B32 Hq128 Hkv1 Skv16384 D512, independent CTAs: read 1,081,742,336 + written 10,533,120
     # bytes (profiles/wide_kernel_wide-head-B32-Hq128-Hkv1-Skv16384-D512.md)
-    "wide_kernel<independent>": {"bytes": 1092314880, "source_sha": "fe78a8e3e58c1539"},
-    # same workload, CTA-pair MMA: read 1,081,789,184 + written 10,622,208 bytes (same file)
-    "wide_kernel<pair>": {"bytes": 1092411392, "source_sha": "fe78a8e3e58c1539"},
+    "wide_kernel<independent>": {"bytes": 1092275456, "source_sha": "f630400fa4869511"},
+    # same workload, CTA-pair MMA: read 1,081,844,480 + written 10,383,616 bytes (same file)
+    "wide_kernel<pair>": {"bytes": 1092228096, "source_sha": "f630400fa4869511"},
 }
 
 
